@@ -380,8 +380,8 @@ def _own(s):
                              s["dgu"][:, c:], saved_out=muon.Act8(*s["a8"], c, fmt))
         return {"dgu": s["dgu"], "a": _read(s["a8"], c)}
     held = muon.Act8(*s["saved"], c, fmt)
-    muon.act8_pack(s["wide"][:, 32:32 + c], held)
-    muon.act8_unpack(held, s["back"])
+    muon.act_pack(s["wide"][:, 32:32 + c], held)
+    muon.act_unpack(held, s["back"])
     return {"back": s["back"]}
 
 
