@@ -455,6 +455,147 @@ muon_status muon_plan_info(muon_plan p, muon_plan_info_t* info);
  */
 muon_status muon_stage_times(muon_plan p, float* ms, double* flops, int32_t n_stages);
 
+/* ====================================================================== the layer side
+ * Operators of the layer whose weight muon_step updates: they make the gradient
+ * the step reads, from activations held in 8 bits between the forward and the
+ * backward pass.  The conventions above hold, except that each call takes its
+ * tensors themselves (one matrix per argument, a pointer and a row pitch `ld`
+ * in elements, ld >= cols; rows need no alignment, aligned rows are faster)
+ * and that nothing but muon_wgrad and muon_rmsnorm_backward needs a plan.
+ * Values of a NULL optional argument are not computed.  Outputs must not
+ * overlap inputs or one another unless a call says so; tensors that interleave
+ * row by row with the same pitch (the two halves of one wide tensor) do not
+ * overlap.  A call with rows == 0 (tokens == 0) touches only what the absence
+ * of rows determines (dweight, grad: zero, or unchanged when accumulating).
+ */
+typedef enum { MUON_ACT_E4M3 = 0, MUON_ACT_INT8 = 1 } muon_act_format;
+
+/*
+ * An activation of rows x cols values held in 8 bits, in device memory of the caller.
+ *   codes   row-major bytes, row pitch ldq: e4m3 numbers (4 exponent bits, bias 7, 3
+ *           mantissa bits, largest 448), or two's-complement whole numbers -127 .. 127.
+ *   scales  row-major bytes, row pitch lds: byte g of a row belongs to columns
+ *           32 g .. 32 g + 31 and stands for 2^(byte - 127); 255 marks a group that
+ *           held an infinity or a NaN and reads back as NaN.
+ * value = code * 2^(byte - 127).  Both pointers and both pitches are multiples of 16,
+ * ldq >= cols, lds >= ceil(cols / 32); bytes that pad a row may be overwritten and are
+ * never used.  Every writer picks the smallest 2^e that brings the group's largest
+ * magnitude within the codes' range (448 or 127), with -110 <= e <= 119 (e4m3) or
+ * 121 (int8), and rounds value / 2^e to the nearest code, ties to even, saturating at
+ * the largest.  Within that range of e every value is exact in bf16 (at most 8
+ * significant bits, a normal number): readers lose nothing to bf16 operands.
+ */
+typedef struct {
+    void* codes;
+    void* scales;
+    int64_t ldq, lds;
+    int32_t format;      /* muon_act_format */
+    int32_t reserved;    /* 0 */
+} muon_act8;
+
+/*
+ * muon_act_pack / muon_act_unpack - x (rows x cols, dtype) to 8 bits, and back:
+ * y = code * scale rounded to dtype (exact).  1 <= cols <= 2^20, 0 <= rows < 2^31.
+ */
+muon_status muon_act_pack(const void* x, int64_t rows, int64_t cols, int64_t ldx, muon_dtype dtype,
+                          const muon_act8* out, void* stream);
+muon_status muon_act_unpack(const muon_act8* in, int64_t rows, int64_t cols, void* y, int64_t ldy, muon_dtype dtype,
+                            void* stream);
+
+/*
+ * muon_rmsnorm_forward - the residual's addition and the root-mean-square norm, per row:
+ *   h = x + residual (h = x when residual is NULL);  r = 1 / sqrt(mean(h^2) + eps);
+ *   xhat = r h;  y = xhat weight.
+ *   x, residual, h, y   rows x cols of dtype, 1 <= cols <= 32768; h may be x or residual
+ *                       itself (same pointer and pitch), y may be x.
+ *   weight              cols fp32.
+ *   h, y, saved, rstd   optional outputs: the sum, the scaled norm, an 8-bit copy, and
+ *                       r (rows fp32).  At least one of them.
+ *   saved_weighted      zero: saved holds xhat, from which muon_rmsnorm_backward
+ *                       continues and muon_wgrad forms the gradient of a weight that read
+ *                       y (with col_scale = weight); nonzero: saved holds y, the operand
+ *                       of an 8-bit product.
+ *   eps                 > 0, finite.
+ * h is kept in fp32 within the call and rounded to dtype only where it is stored.
+ */
+muon_status muon_rmsnorm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* weight,
+                                 int64_t rows, int64_t cols, muon_dtype dtype, float eps, void* h, int64_t ldh,
+                                 void* y, int64_t ldy, const muon_act8* saved, int32_t saved_weighted, float* rstd,
+                                 void* stream);
+
+/*
+ * muon_swiglu_forward - a = silu(gate) up, silu(z) = z / (1 + exp(-z)), rows x cols of
+ * dtype, 1 <= cols <= 2^20.  Optional outputs: a, and 8-bit copies of gate, up and a;
+ * at least one of them.  a may be gate or up itself (same pointer and pitch).
+ */
+muon_status muon_swiglu_forward(const void* gate, int64_t ldg, const void* up, int64_t ldu, int64_t rows, int64_t cols,
+                                muon_dtype dtype, void* a, int64_t lda, const muon_act8* saved_gate,
+                                const muon_act8* saved_up, const muon_act8* saved_out, void* stream);
+
+/*
+ * muon_swiglu_backward - from da and the 8-bit gate and up, s = 1 / (1 + exp(-gate)):
+ *   dgate = da up s (1 + gate (1 - s)),  dup = da gate s,  and optionally saved_out, the
+ * 8-bit copy of silu(gate) up that the gradient of the down projection reads (so the
+ * forward pass need not keep it).  da, dgate, dup of dtype; dgate or dup may be da itself.
+ */
+muon_status muon_swiglu_backward(const void* da, int64_t ldda, const muon_act8* saved_gate, const muon_act8* saved_up,
+                                 int64_t rows, int64_t cols, muon_dtype dtype, void* dgate, int64_t lddg, void* dup,
+                                 int64_t lddu, const muon_act8* saved_out, void* stream);
+
+/*
+ * A grad plan owns what the two gradient reductions need on the current device: one
+ * workspace allocation of muon_grad_plan_workspace_size bytes, whatever shapes its
+ * calls have, and a status word.  Calls on one plan share the workspace: they are
+ * ordered by the caller, as those of a muon_plan.  muon_grad_plan_create
+ * synchronises the host; so do muon_grad_plan_destroy (the whole device; NULL is ignored) and
+ * muon_grad_plan_sync, which waits for stream, then reads and clears the status word
+ * (MUON_ERR_TIMEOUT as muon_sync).
+ */
+typedef struct muon_grad_plan_s* muon_grad_plan;
+muon_status muon_grad_plan_create(muon_grad_plan* out);
+muon_status muon_grad_plan_workspace_size(int64_t* bytes);
+void muon_grad_plan_destroy(muon_grad_plan p);
+muon_status muon_grad_plan_sync(muon_grad_plan p, void* stream);
+
+/*
+ * muon_rmsnorm_backward - the gradients of muon_rmsnorm_forward, per row with
+ * w = dy weight and xhat from either the 8-bit copy `saved` (saved_weighted zero) or
+ * xhat = rstd h (exactly one of saved and h is given):
+ *   dx = rstd (w - xhat mean(w xhat)) + dres,   dweight (+)= sum over rows of dy xhat.
+ *   dres      optional: the gradient that reaches h along the residual path.
+ *   dx        rows x cols of dtype (the gradient of x and of residual alike); may be dy,
+ *             h or dres itself.  Optional if dweight is given.
+ *   dweight   optional: cols fp32, overwritten, or added to when accumulate is nonzero.
+ * dweight is summed in a fixed order: the same inputs give the same bits.
+ */
+muon_status muon_rmsnorm_backward(muon_grad_plan p, const void* dy, int64_t lddy, const muon_act8* saved,
+                                  const void* h, int64_t ldh, const float* rstd, const float* weight, const void* dres,
+                                  int64_t lddres, int64_t rows, int64_t cols, muon_dtype dtype, void* dx,
+                                  int64_t lddx, float* dweight, int32_t accumulate, void* stream);
+
+/*
+ * muon_wgrad - the gradient of a weight (m x n, as muon_step takes it) of y = x W^T from
+ * the 8-bit x: grad (+)= dy^T x diag(col_scale).
+ *   dy         tokens x m, bf16.
+ *   x          tokens x n in 8 bits.
+ *   groups     0: one weight, grad is m x n.  Else the weights of `groups` experts,
+ *              1 <= groups <= 4096: offsets (device, groups + 1 int32, non-decreasing,
+ *              clamped to [0, tokens]) delimits each expert's tokens, grad is
+ *              groups x m x n, and an expert without tokens gets zero (or keeps its
+ *              gradient when accumulating).  Tokens outside every expert are not used,
+ *              whatever they hold.
+ *   col_scale  optional: n fp32, multiplied into the columns in fp32 (the norm's weight
+ *              when x holds the unweighted norm).
+ *   grad       dense row-major, grad_dtype (MUON_BF16 or MUON_F32, the plan's of
+ *              muon_step), overwritten, or added to when accumulate is nonzero.
+ * Operands are bf16 (exact for the 8-bit x), products and sums fp32.  The sums' order depends on
+ * the sizes alone: the same inputs give the same bits.  1 <= m, n <= 2^20,
+ * 0 <= tokens < 2^31.
+ */
+muon_status muon_wgrad(muon_grad_plan p, const void* dy, int64_t lddy, const muon_act8* x, int64_t tokens, int64_t m,
+                       int64_t n, const int32_t* offsets, int32_t groups, const float* col_scale, void* grad,
+                       muon_dtype grad_dtype, int32_t accumulate, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

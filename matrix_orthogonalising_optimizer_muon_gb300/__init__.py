@@ -14,6 +14,11 @@ RowNorm Muon (full NS5 every K steps, RowNorm otherwise; "Scaling Muon for
 Diffusion Transformers", sec. 3).  ``DistributedMuon`` runs the step across the
 ranks of a torch.distributed group with one owner per matrix (``partition_owners``,
 the library's ``muon_partition``) and broadcasts the updated parameters.
+
+The layer side (``activations``: ``Act8``, ``act_pack``, ``act_unpack``,
+``rmsnorm_forward``, ``swiglu_forward``, ``swiglu_backward``, ``GradPlan``) makes the
+gradients the step reads from activations held in 8 bits; its names are resolved on
+first use, as that module imports torch.
 """
 from __future__ import annotations
 
@@ -29,12 +34,29 @@ __all__ = [
     "MUON_OK", "MUON_ERR_INVALID_ARG", "MUON_ERR_UNSUPPORTED", "MUON_ERR_OOM",
     "MUON_ERR_CUDA", "MUON_ERR_TIMEOUT", "MUON_ERR_NONFINITE", "MUON_F32", "MUON_BF16",
     "MUON_MODE_NS", "MUON_MODE_ROWNORM", "EXPORTED",
+    "MuonAct8", "MUON_ACT_E4M3", "MUON_ACT_INT8",
+    "Act8", "act_pack", "act_unpack", "rmsnorm_forward", "swiglu_forward", "swiglu_backward", "GradPlan",
+    "grad_plan_workspace_size",
 ]
+
+# names of the layer side, resolved from .activations on first use
+_LAYER = ("Act8", "act_pack", "act_unpack", "rmsnorm_forward", "swiglu_forward", "swiglu_backward", "GradPlan",
+          "grad_plan_workspace_size")
+
+
+def __getattr__(name):
+    if name in _LAYER:
+        from . import activations
+        globals().update({n: getattr(activations, n) for n in _LAYER})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
+
 
 MUON_OK, MUON_ERR_INVALID_ARG, MUON_ERR_UNSUPPORTED, MUON_ERR_OOM = 0, 1, 2, 3
 MUON_ERR_CUDA, MUON_ERR_TIMEOUT, MUON_ERR_NONFINITE = 4, 5, 6
 MUON_F32, MUON_BF16 = 0, 1
 MUON_MODE_NS, MUON_MODE_ROWNORM = 0, 1
+MUON_ACT_E4M3, MUON_ACT_INT8 = 0, 1
 
 # Newton-Schulz steps and momentum the pages use ("Muon is Scalable" blog).
 DEFAULT_NS_STEPS = 5
@@ -63,8 +85,15 @@ class MuonPlanInfo(ctypes.Structure):
                 ("split_buckets", ctypes.c_int32), ("fp32_buckets", ctypes.c_int32), ("colsq_len", ctypes.c_int64)]
 
 
+class MuonAct8(ctypes.Structure):
+    """``muon_act8`` of the header."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+                ("lds", ctypes.c_int64), ("format", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
+_L, _I, _A = ctypes.c_int64, ctypes.c_int, ctypes.POINTER(MuonAct8)
 # name -> (restype, argtypes); every function declared in include/muon.h
 EXPORTED = {
     "muon_plan_create": (ctypes.c_int, [ctypes.POINTER(MuonShape), ctypes.c_int32, ctypes.c_int,
@@ -104,6 +133,19 @@ EXPORTED = {
     "muon_rownorm_matrix_noalloc": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                                    ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                                    ctypes.c_float, _P]),
+    "muon_act_pack": (_I, [_P, _L, _L, _L, _I, _A, _P]),
+    "muon_act_unpack": (_I, [_A, _L, _L, _P, _L, _I, _P]),
+    "muon_rmsnorm_forward": (_I, [_P, _L, _P, _L, _P, _L, _L, _I, ctypes.c_float, _P, _L, _P, _L, _A,
+                                  ctypes.c_int32, _P, _P]),
+    "muon_swiglu_forward": (_I, [_P, _L, _P, _L, _L, _L, _I, _P, _L, _A, _A, _A, _P]),
+    "muon_swiglu_backward": (_I, [_P, _L, _A, _A, _L, _L, _I, _P, _L, _P, _L, _A, _P]),
+    "muon_grad_plan_create": (_I, [ctypes.POINTER(_P)]),
+    "muon_grad_plan_workspace_size": (_I, [ctypes.POINTER(_L)]),
+    "muon_grad_plan_destroy": (None, [_P]),
+    "muon_grad_plan_sync": (_I, [_P, _P]),
+    "muon_rmsnorm_backward": (_I, [_P, _P, _L, _A, _P, _L, _P, _P, _P, _L, _L, _L, _I, _P, _L, _P,
+                                   ctypes.c_int32, _P]),
+    "muon_wgrad": (_I, [_P, _P, _L, _A, _L, _L, _L, _P, ctypes.c_int32, _P, _P, _I, ctypes.c_int32, _P]),
 }
 
 _lib = None
