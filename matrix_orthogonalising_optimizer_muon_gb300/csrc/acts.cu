@@ -241,6 +241,7 @@ muon_status muon_grad_plan_create(muon_grad_plan* out) {
             st = e == cudaErrorMemoryAllocation ? MUON_ERR_OOM : MUON_ERR_CUDA;
         }
     }
+    if (st == MUON_OK) st = cuda_status(wgrad_prepare());
     if (st == MUON_OK) st = cuda_status(cudaMemset(p->ws, 0, kWsHeader));
     if (st == MUON_OK) st = cuda_status(cudaDeviceSynchronize());
     if (st != MUON_OK) {
@@ -320,7 +321,7 @@ muon_status muon_wgrad(muon_grad_plan p, const void* dy, int64_t lddy, const muo
     a.dy = dy, a.lddy = lddy, a.tokens = tokens, a.m = (int)m, a.n = (int)n;
     a.offsets = offsets, a.groups = std::max(groups, 1), a.col_scale = col_scale;
     a.grad = grad, a.accumulate = accumulate != 0, a.status = p->status;
-    return cuda_status(launch_wgrad(a, grad_dtype == MUON_BF16, static_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_wgrad(a, grad_dtype == MUON_BF16, p->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

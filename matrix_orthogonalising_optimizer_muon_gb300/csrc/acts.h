@@ -87,6 +87,7 @@ cudaError_t launch_rmsnorm_forward(const NormArgs& a, bool bf16, bool vec, cudaS
 int rmsnorm_backward_blocks(long long rows, int cols, int sm_count);
 constexpr long long kNormPartialFloats = 8ll << 20;   // bound on blocks x cols
 cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a, bool bf16, bool vec, int sm_count, cudaStream_t s);
-cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, cudaStream_t s);
+cudaError_t wgrad_prepare();   // once per device, before the first launch
+cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaStream_t s);
 
 }  // namespace muon
