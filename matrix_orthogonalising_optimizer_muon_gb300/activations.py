@@ -13,8 +13,7 @@ import ctypes
 
 import torch
 
-from . import (MUON_ACT_E4M3, MUON_ACT_INT8, MUON_BF16, MUON_F32, MuonAct8, _check, _stream_handle,
-               load)
+from . import (MUON_ACT_E4M3, MUON_ACT_INT8, MUON_BF16, MUON_F32, MuonAct8, _check, load)
 
 __all__ = ["Act8", "act_pack", "act_unpack", "rmsnorm_forward", "swiglu_forward", "swiglu_backward", "GradPlan",
            "grad_plan_workspace_size"]
@@ -33,7 +32,7 @@ class Act8:
     ``scales`` are uint8 CUDA tensors whose rows are padded to multiples of 16 bytes; ``fmt``
     is "e4m3" or "int8".  ``Act8.empty`` allocates both."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "fmt", "ref")
+    __slots__ = ("codes", "scales", "rows", "cols", "fmt", "device", "ref")
 
     def __init__(self, codes, scales, cols: int, fmt: str):
         if fmt not in _FORMATS:
@@ -45,6 +44,7 @@ class Act8:
         if codes.shape[0] != scales.shape[0]:
             raise ValueError("codes and scales differ in rows: %d and %d" % (codes.shape[0], scales.shape[0]))
         self.codes, self.scales, self.rows, self.cols, self.fmt = codes, scales, codes.shape[0], cols, fmt
+        self.device = codes.get_device()
         self.ref = MuonAct8(codes.data_ptr(), scales.data_ptr(), self._pitch(codes), self._pitch(scales),
                             _FORMATS[fmt], 0)
 
@@ -63,58 +63,62 @@ class Act8:
         return self.codes.numel() + self.scales.numel()
 
 
-def _mat(t, rows, cols, dtype, name):
+def _stream(stream, dev):
+    """Handle of ``stream``, or of the current stream of device ``dev``."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _mat(t, rows, cols, dtype, dev, name):
     """(pointer, row pitch) of one operand, checked."""
     if t is None:
         return None, 0
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols \
-            or (cols > 1 and t.stride(1) != 1) or not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != dev or (cols > 1 and t.stride(1) != 1):
         raise ValueError("%s: need a %s tensor of shape (%d, %d) with unit column stride on the current CUDA device, "
                          "got %s %s strides %s on %s" % (name, dtype, rows, cols, t.dtype, tuple(t.shape),
                                                          tuple(t.stride()), t.device))
     return t.data_ptr(), t.stride(0) if rows > 1 else cols
 
 
-def _vec(t, n, name, dtype=torch.float32):
+def _vec(t, n, dev, name, dtype=torch.float32):
     if t is None:
         return None
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) \
-            or not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s: need a contiguous %s tensor of %d elements on the current CUDA device, got %s %s on %s"
                          % (name, dtype, n, t.dtype, tuple(t.shape), t.device))
     return t.data_ptr()
 
 
-def _act(a, rows, cols, name):
+def _act(a, rows, cols, dev, name):
     if a is None:
         return None
-    if a.rows != rows or a.cols != cols or not a.codes.is_cuda or a.codes.get_device() != torch.cuda.current_device():
+    if a.rows != rows or a.cols != cols or a.device != dev:
         raise ValueError("%s: need an Act8 of (%d, %d) on the current CUDA device, got (%d, %d) on %s"
                          % (name, rows, cols, a.rows, a.cols, a.codes.device))
     return ctypes.byref(a.ref)
 
 
 def _shape(t, name):
-    """(rows, cols, dtype, dtype code) of the operand that sets a call's shape."""
-    if t.dim() != 2 or t.dtype not in _DTYPES:
-        raise ValueError("%s: need a two-dimensional float32 or bfloat16 tensor, got %s %s"
-                         % (name, t.dtype, tuple(t.shape)))
-    return t.shape[0], t.shape[1], t.dtype, _DTYPES[t.dtype]
+    """(rows, cols, dtype, dtype code, current device) for the operand that sets a call's shape."""
+    if t.dim() != 2 or t.dtype not in _DTYPES or not t.is_cuda:
+        raise ValueError("%s: need a two-dimensional float32 or bfloat16 CUDA tensor, got %s %s on %s"
+                         % (name, t.dtype, tuple(t.shape), t.device))
+    rows, cols = t.shape
+    return rows, cols, t.dtype, _DTYPES[t.dtype], torch.cuda.current_device()
 
 
 def act_pack(x, out: Act8, stream=None):
     """``muon_act_pack``: x to 8 bits."""
-    rows, cols, dt, code = _shape(x, "x")
-    p, ld = _mat(x, rows, cols, dt, "x")
-    _check(load().muon_act_pack(p, rows, cols, ld, code, _act(out, rows, cols, "out"), _stream_handle(stream)),
+    rows, cols, dt, code, dev = _shape(x, "x")
+    p, ld = _mat(x, rows, cols, dt, dev, "x")
+    _check(load().muon_act_pack(p, rows, cols, ld, code, _act(out, rows, cols, dev, "out"), _stream(stream, dev)),
            "muon_act_pack")
 
 
 def act_unpack(a: Act8, out, stream=None):
     """``muon_act_unpack``: the values of an ``Act8`` into ``out`` (float32 or bfloat16)."""
-    rows, cols, dt, code = _shape(out, "out")
-    p, ld = _mat(out, rows, cols, dt, "out")
-    _check(load().muon_act_unpack(_act(a, rows, cols, "a"), rows, cols, p, ld, code, _stream_handle(stream)),
+    rows, cols, dt, code, dev = _shape(out, "out")
+    p, ld = _mat(out, rows, cols, dt, dev, "out")
+    _check(load().muon_act_unpack(_act(a, rows, cols, dev, "a"), rows, cols, p, ld, code, _stream(stream, dev)),
            "muon_act_unpack")
 
 
@@ -122,40 +126,40 @@ def rmsnorm_forward(x, weight, eps: float, residual=None, h=None, y=None, saved:
                     saved_weighted: bool = False, rstd=None, stream=None):
     """``muon_rmsnorm_forward``: h = x + residual, y = h / rms(h) * weight; ``saved`` receives the
     norm in 8 bits before the weight (for ``GradPlan``), or y itself with ``saved_weighted``."""
-    rows, cols, dt, code = _shape(x, "x")
-    px, lx = _mat(x, rows, cols, dt, "x")
-    pr, lr = _mat(residual, rows, cols, dt, "residual")
-    ph, lh = _mat(h, rows, cols, dt, "h")
-    py, ly = _mat(y, rows, cols, dt, "y")
-    _check(load().muon_rmsnorm_forward(px, lx, pr, lr, _vec(weight, cols, "weight"), rows, cols, code, eps, ph, lh,
-                                       py, ly, _act(saved, rows, cols, "saved"), 1 if saved_weighted else 0,
-                                       _vec(rstd, rows, "rstd"), _stream_handle(stream)), "muon_rmsnorm_forward")
+    rows, cols, dt, code, dev = _shape(x, "x")
+    px, lx = _mat(x, rows, cols, dt, dev, "x")
+    pr, lr = _mat(residual, rows, cols, dt, dev, "residual")
+    ph, lh = _mat(h, rows, cols, dt, dev, "h")
+    py, ly = _mat(y, rows, cols, dt, dev, "y")
+    _check(load().muon_rmsnorm_forward(px, lx, pr, lr, _vec(weight, cols, dev, "weight"), rows, cols, code, eps, ph, lh,
+                                       py, ly, _act(saved, rows, cols, dev, "saved"), 1 if saved_weighted else 0,
+                                       _vec(rstd, rows, dev, "rstd"), _stream(stream, dev)), "muon_rmsnorm_forward")
 
 
 def swiglu_forward(gate, up, out=None, saved_gate: Act8 | None = None, saved_up: Act8 | None = None,
                    saved_out: Act8 | None = None, stream=None):
     """``muon_swiglu_forward``: out = silu(gate) * up, with 8-bit copies of any of the three."""
-    rows, cols, dt, code = _shape(gate, "gate")
-    pg, lg = _mat(gate, rows, cols, dt, "gate")
-    pu, lu = _mat(up, rows, cols, dt, "up")
-    po, lo = _mat(out, rows, cols, dt, "out")
+    rows, cols, dt, code, dev = _shape(gate, "gate")
+    pg, lg = _mat(gate, rows, cols, dt, dev, "gate")
+    pu, lu = _mat(up, rows, cols, dt, dev, "up")
+    po, lo = _mat(out, rows, cols, dt, dev, "out")
     _check(load().muon_swiglu_forward(pg, lg, pu, lu, rows, cols, code, po, lo,
-                                      _act(saved_gate, rows, cols, "saved_gate"),
-                                      _act(saved_up, rows, cols, "saved_up"),
-                                      _act(saved_out, rows, cols, "saved_out"), _stream_handle(stream)),
+                                      _act(saved_gate, rows, cols, dev, "saved_gate"),
+                                      _act(saved_up, rows, cols, dev, "saved_up"),
+                                      _act(saved_out, rows, cols, dev, "saved_out"), _stream(stream, dev)),
            "muon_swiglu_forward")
 
 
 def swiglu_backward(dout, saved_gate: Act8, saved_up: Act8, dgate, dup, saved_out: Act8 | None = None, stream=None):
     """``muon_swiglu_backward``: dgate and dup from dout and the 8-bit gate and up; ``saved_out``
     receives silu(gate) * up again in 8 bits, the operand of the down projection's gradient."""
-    rows, cols, dt, code = _shape(dout, "dout")
-    pd, ldd = _mat(dout, rows, cols, dt, "dout")
-    pg, lg = _mat(dgate, rows, cols, dt, "dgate")
-    pu, lu = _mat(dup, rows, cols, dt, "dup")
-    _check(load().muon_swiglu_backward(pd, ldd, _act(saved_gate, rows, cols, "saved_gate"),
-                                       _act(saved_up, rows, cols, "saved_up"), rows, cols, code, pg, lg, pu, lu,
-                                       _act(saved_out, rows, cols, "saved_out"), _stream_handle(stream)),
+    rows, cols, dt, code, dev = _shape(dout, "dout")
+    pd, ldd = _mat(dout, rows, cols, dt, dev, "dout")
+    pg, lg = _mat(dgate, rows, cols, dt, dev, "dgate")
+    pu, lu = _mat(dup, rows, cols, dt, dev, "dup")
+    _check(load().muon_swiglu_backward(pd, ldd, _act(saved_gate, rows, cols, dev, "saved_gate"),
+                                       _act(saved_up, rows, cols, dev, "saved_up"), rows, cols, code, pg, lg, pu, lu,
+                                       _act(saved_out, rows, cols, dev, "saved_out"), _stream(stream, dev)),
            "muon_swiglu_backward")
 
 
@@ -195,38 +199,40 @@ class GradPlan:
 
     def sync(self, stream=None):
         """``muon_grad_plan_sync``: wait for the stream and raise what the device reported."""
-        _check(self.lib.muon_grad_plan_sync(self.handle, _stream_handle(stream)), "muon_grad_plan_sync")
+        _check(self.lib.muon_grad_plan_sync(self.handle, _stream(stream, torch.cuda.current_device())),
+               "muon_grad_plan_sync")
 
     def rmsnorm_backward(self, dy, weight, rstd, dx=None, dweight=None, saved: Act8 | None = None, h=None, dres=None,
                          accumulate: bool = False, stream=None):
         """``muon_rmsnorm_backward`` from ``saved`` (the unweighted norm in 8 bits) or ``h``."""
-        rows, cols, dt, code = _shape(dy, "dy")
-        py, ly = _mat(dy, rows, cols, dt, "dy")
-        ph, lh = _mat(h, rows, cols, dt, "h")
-        pr, lr = _mat(dres, rows, cols, dt, "dres")
-        px, lx = _mat(dx, rows, cols, dt, "dx")
-        _check(self.lib.muon_rmsnorm_backward(self.handle, py, ly, _act(saved, rows, cols, "saved"), ph, lh,
-                                              _vec(rstd, rows, "rstd"), _vec(weight, cols, "weight"), pr, lr, rows,
-                                              cols, code, px, lx, _vec(dweight, cols, "dweight"),
-                                              1 if accumulate else 0, _stream_handle(stream)),
+        rows, cols, dt, code, dev = _shape(dy, "dy")
+        py, ly = _mat(dy, rows, cols, dt, dev, "dy")
+        ph, lh = _mat(h, rows, cols, dt, dev, "h")
+        pr, lr = _mat(dres, rows, cols, dt, dev, "dres")
+        px, lx = _mat(dx, rows, cols, dt, dev, "dx")
+        _check(self.lib.muon_rmsnorm_backward(self.handle, py, ly, _act(saved, rows, cols, dev, "saved"), ph, lh,
+                                              _vec(rstd, rows, dev, "rstd"), _vec(weight, cols, dev, "weight"), pr, lr, rows,
+                                              cols, code, px, lx, _vec(dweight, cols, dev, "dweight"),
+                                              1 if accumulate else 0, _stream(stream, dev)),
                "muon_rmsnorm_backward")
 
     def wgrad(self, dy, x: Act8, grad, offsets=None, col_scale=None, accumulate: bool = False, stream=None):
         """``muon_wgrad``: grad (m, n) (+)= dy^T x * col_scale, dy (tokens, m) bfloat16, x (tokens, n)
         in 8 bits; with ``offsets`` (groups + 1 int32, on the device) grad is (groups, m, n), one
         weight per range of tokens."""
+        dev = torch.cuda.current_device()
         if dy.dim() != 2 or grad.dtype not in _DTYPES:
             raise ValueError("wgrad: need a two-dimensional dy and a float32 or bfloat16 grad, got %s and %s"
                              % (tuple(dy.shape), grad.dtype))
         (tokens, m), n = dy.shape, x.cols
         groups = 0 if offsets is None else offsets.numel() - 1
         shape = (m, n) if offsets is None else (groups, m, n)
-        if tuple(grad.shape) != shape or not grad.is_contiguous() \
-                or not grad.is_cuda or grad.get_device() != torch.cuda.current_device() or groups < (offsets is not None):
+        if grad.shape != shape or not grad.is_contiguous() or grad.get_device() != dev \
+                or groups < (offsets is not None):
             raise ValueError("grad: need a contiguous tensor of shape %s on the current CUDA device, got %s on %s"
                              % (shape, tuple(grad.shape), grad.device))
-        py, ly = _mat(dy, tokens, m, torch.bfloat16, "dy")
-        _check(self.lib.muon_wgrad(self.handle, py, ly, _act(x, tokens, n, "x"), tokens, m, n,
-                                   _vec(offsets, groups + 1, "offsets", torch.int32), groups,
-                                   _vec(col_scale, n, "col_scale"), grad.data_ptr(), _DTYPES[grad.dtype],
-                                   1 if accumulate else 0, _stream_handle(stream)), "muon_wgrad")
+        py, ly = _mat(dy, tokens, m, torch.bfloat16, dev, "dy")
+        _check(self.lib.muon_wgrad(self.handle, py, ly, _act(x, tokens, n, dev, "x"), tokens, m, n,
+                                   _vec(offsets, groups + 1, dev, "offsets", torch.int32), groups,
+                                   _vec(col_scale, n, dev, "col_scale"), grad.data_ptr(), _DTYPES[grad.dtype],
+                                   1 if accumulate else 0, _stream(stream, dev)), "muon_wgrad")

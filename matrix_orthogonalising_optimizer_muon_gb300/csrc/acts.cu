@@ -6,16 +6,18 @@
 struct muon_grad_plan_s {
     int device = 0;
     int sm_count = 0;
-    void* ws = nullptr;       // status word, then the partial sums
+    void* ws = nullptr;       // status word, counters, partial sums
     int* status = nullptr;
+    int* counters = nullptr;
     float* partial = nullptr;
 };
 
 namespace {
 using namespace muon_impl;
 
-constexpr size_t kWsHeader = 256;
-constexpr int64_t kGradWorkspace = (int64_t)kWsHeader + kNormPartialFloats * 4;
+constexpr size_t kWsHeader = 256 + kMaxParts * 4 * sizeof(int);   // status word, counters
+constexpr int64_t kGradWorkspace = (int64_t)kWsHeader + kPartialFloats * 4;
+static_assert(kWsHeader % 256 == 0, "the partial sums are aligned");
 
 // A strided range of device memory: `rows` rows of `width` bytes, `pitch` bytes apart.
 struct Range {
@@ -250,6 +252,7 @@ muon_status muon_grad_plan_create(muon_grad_plan* out) {
         return st;
     }
     p->status = static_cast<int*>(p->ws);
+    p->counters = reinterpret_cast<int*>(static_cast<char*>(p->ws) + 256);
     p->partial = reinterpret_cast<float*>(static_cast<char*>(p->ws) + kWsHeader);
     *out = p;
     return MUON_OK;
@@ -268,7 +271,7 @@ muon_status muon_grad_plan_sync(muon_grad_plan p, void* stream) {
     int st = 0;
     MUON_TRY(cudaMemcpy(&st, p->status, sizeof(int), cudaMemcpyDeviceToHost));
     if (st == 0) return MUON_OK;
-    MUON_TRY(cudaMemset(p->status, 0, sizeof(int)));
+    MUON_TRY(cudaMemset(p->ws, 0, kWsHeader));   // a call that gave up may have left counters behind
     return MUON_ERR_TIMEOUT;
 }
 
@@ -321,6 +324,7 @@ muon_status muon_wgrad(muon_grad_plan p, const void* dy, int64_t lddy, const muo
     a.dy = dy, a.lddy = lddy, a.tokens = tokens, a.m = (int)m, a.n = (int)n;
     a.offsets = offsets, a.groups = std::max(groups, 1), a.col_scale = col_scale;
     a.grad = grad, a.accumulate = accumulate != 0, a.status = p->status;
+    a.partial = p->partial, a.counters = p->counters;
     return cuda_status(launch_wgrad(a, grad_dtype == MUON_BF16, p->sm_count, static_cast<cudaStream_t>(stream)));
 }
 

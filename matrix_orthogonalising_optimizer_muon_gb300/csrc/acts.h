@@ -75,7 +75,10 @@ struct WgradArgs {
     void* grad;
     int accumulate;
     int* status;
+    float* partial;      // kMaxParts tiles of 256 x 256 sums
+    int* counters;       // kMaxParts * 4 words, zero between calls
 };
+constexpr int kMaxParts = 240;
 
 // bf16: the dtype of the Mat operands; vec: every one of them (and ld) 16-byte aligned.
 cudaError_t launch_act_pack(const PackArgs& a, bool bf16, bool vec, cudaStream_t s);
@@ -86,6 +89,8 @@ cudaError_t launch_rmsnorm_forward(const NormArgs& a, bool bf16, bool vec, cudaS
 // Blocks of the backward kernel for these sizes (its partial sums: blocks x cols floats).
 int rmsnorm_backward_blocks(long long rows, int cols, int sm_count);
 constexpr long long kNormPartialFloats = 8ll << 20;   // bound on blocks x cols
+constexpr long long kPartialFloats = kMaxParts * 65536ll;   // of a grad plan, for either reduction
+static_assert(kPartialFloats >= kNormPartialFloats, "one region serves both");
 cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a, bool bf16, bool vec, int sm_count, cudaStream_t s);
 cudaError_t wgrad_prepare();   // once per device, before the first launch
 cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaStream_t s);

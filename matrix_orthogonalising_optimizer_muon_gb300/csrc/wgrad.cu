@@ -16,7 +16,7 @@
 //   11-14  epilogue: column scale, addition to grad, stores
 // Two rings: x as it arrives (full_r by TMA, empty_r by the conversion), and the operands (dy
 // and converted x; ready, on the even CTA, by both CTAs' conversion warps and dy's TMA bytes,
-// empty, on both, by the MMAs), so the MMA thread has one wait and one commit per step.
+// empty, on both, by the MMAs), so the MMA warp has one wait and one commit per step.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -29,10 +29,10 @@ namespace muon {
 namespace {
 
 #ifndef W_NB
-#define W_NB 5
-#define W_NR 5
-#define W_CW 10
-#define W_CG 5
+#define W_NB 4
+#define W_NR 8
+#define W_CW 8
+#define W_CG 4
 #endif
 constexpr int kWgStepT = 64;            // tokens per step
 constexpr int kRingM = W_NB;            // steps of MMA operands
@@ -46,6 +46,7 @@ constexpr int kEpiFirst = kConvFirst + kConvWarps;
 constexpr int kWgEpiWarps = 4;
 constexpr int kWgThreads = 32 * (kEpiFirst + kWgEpiWarps);
 constexpr int kBandM = 8;               // tiles along m whose columns of dy are in flight together
+constexpr int kSortGroups = 256;        // experts that are dealt out by their number of tokens
 // A ring slot is always converted by the same warps, which so see every phase of its barriers.
 static_assert(kRingR % kConvGroups == 0 && kRingM % kConvGroups == 0 && kRows % 8 == 0, "ring sizes");
 
@@ -58,30 +59,53 @@ struct WgCfg {
     static constexpr int SLOT_BYTES = 2 * A_BYTES;          // dy, then x
     static constexpr int R_OFFSET = kRingM * SLOT_BYTES;
     static constexpr int OUT_OFFSET = R_OFFSET + kRingR * R_BYTES;
-    static constexpr int OUT_LD = 36;                       // one 32 x 32 block of floats, rows padded by 16 bytes
-    static constexpr int OUT_WARP = 32 * OUT_LD * 4;
+    static constexpr int OUT_LD = 144;                      // row of a 32 x 32 block of floats, padded by 16 bytes
+    static constexpr int OUT_WARP = 32 * OUT_LD;
     static constexpr int BAR_OFFSET = OUT_OFFSET + kWgEpiWarps * OUT_WARP;
-    static constexpr int SMEM_BYTES = BAR_OFFSET + 512 + 1024;
+    static constexpr int EXPERTS_OFFSET = BAR_OFFSET + 512;
+    static constexpr int SMEM_BYTES = EXPERTS_OFFSET + kSortGroups * 10 + 1024;
 };
 static_assert(WgCfg::SMEM_BYTES <= 232448, "weight-gradient kernel exceeds the shared memory of one CTA");
 
 struct WgradLaunch {
     CUtensorMap map_y, map_x, map_s;
     WgradArgs a;
-    int tiles_m, tiles_n, units;   // units: tiles of all groups
+    int tiles_m, tiles_n;
+    int units;                     // whole tiles of all groups, then parts of split tiles
+    int whole, parts;              // units below `whole` are tiles, the others one of `parts` of a tile
     int chain;                     // tokens one accumulator takes
     int wide;                      // rows of grad are aligned to four elements
+};
+
+// Experts by decreasing number of tokens, built by every CTA when there are several (at most
+// kSortGroups, else in their own order): dealt out in turns, equal tiles then meet in the same
+// turn, and the last turns are the short ones.
+struct Experts {
+    int begin[kSortGroups], end[kSortGroups];
+    uint16_t order[kSortGroups];
 };
 
 struct Unit {
     int m0, n0;
     long long begin, end;   // tokens
-    int group;
+    int group, tile, part;  // part < 0: the whole tile
 };
 
-__device__ __forceinline__ Unit decode_unit(const WgradLaunch& L, int u) {
+__device__ __forceinline__ void expert_range(const WgradArgs& a, int g, long long* begin, long long* end) {
+    *begin = min(max((long long)a.offsets[g], 0ll), a.tokens);
+    *end = min(max((long long)a.offsets[g + 1], *begin), a.tokens);
+}
+
+__device__ __forceinline__ Unit decode_unit(const WgradLaunch& L, const Experts* ex, int u) {
     const int per = L.tiles_m * L.tiles_n;
     Unit r;
+    r.part = -1;
+    if (u >= L.whole) {
+        const int v = u - L.whole;
+        u = L.whole + v / L.parts;
+        r.part = v % L.parts;
+    }
+    r.tile = u;
     r.group = u / per;
     int t = u - r.group * per;
     // bands of kBandM tiles along m, within a band along n: the tiles that run together share
@@ -93,8 +117,16 @@ __device__ __forceinline__ Unit decode_unit(const WgradLaunch& L, int u) {
     r.n0 = t / wide * 256;
     r.begin = 0, r.end = L.a.tokens;
     if (L.a.offsets) {
-        r.begin = min(max((long long)L.a.offsets[r.group], 0ll), L.a.tokens);
-        r.end = min(max((long long)L.a.offsets[r.group + 1], r.begin), L.a.tokens);
+        if (L.a.groups <= kSortGroups) {
+            r.group = ex->order[r.group];
+            r.begin = ex->begin[r.group], r.end = ex->end[r.group];
+        } else {
+            expert_range(L.a, r.group, &r.begin, &r.end);
+        }
+    } else if (r.part >= 0) {
+        const long long steps = (L.a.tokens + kWgStepT - 1) / kWgStepT;
+        r.begin = steps * r.part / L.parts * kWgStepT;
+        r.end = min(steps * (r.part + 1) / L.parts * kWgStepT, L.a.tokens);
     }
     return r;
 }
@@ -134,28 +166,273 @@ __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t s2) {
 
 // Four neighbouring elements, aligned to their size.
 template <bool BF16>
-__device__ __forceinline__ float4 load_four(const void* p, long long e) {
-    if (!BF16) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + e);
+__device__ __forceinline__ float4 load_four(const char* p) {
+    if (!BF16) return *reinterpret_cast<const float4*>(p);
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
     return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
 }
 template <bool BF16>
-__device__ __forceinline__ void store_four(void* p, long long e, const float4& v) {
+__device__ __forceinline__ void store_four(char* p, const float* v) {
     if (BF16)
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + e) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+        *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
     else
-        *reinterpret_cast<float4*>(static_cast<float*>(p) + e) = v;
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
+// A lane's 32 sums of a block of a part, 32 rows of 256 floats: as OutTile holds them.
+template <bool WIDE>
+__device__ __forceinline__ void part_load(const float* p, float (&f)[32]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (WIDE) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + i * 1024));
+            f[4 * i] = x.x, f[4 * i + 1] = x.y, f[4 * i + 2] = x.z, f[4 * i + 3] = x.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[4 * i + j] = __ldcg(p + (4 * i + j) * 256);
+        }
+}
+template <bool WIDE>
+__device__ __forceinline__ void part_store(float* p, const float (&f)[32]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (WIDE) {
+            *reinterpret_cast<float4*>(p + i * 1024) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[(4 * i + j) * 256] = f[4 * i + j];
+        }
+}
+
+// One lane's share of a warp's 32 rows of a tile of grad, in blocks of 32 columns: 32 sums per
+// block, as four columns (cl .. + 3) of eight rows (rl, rl + 4, ...) where the rows of grad are
+// aligned to four elements (WIDE), else as one column (lane) of all rows; either way a warp
+// touches 128-byte row pieces.  Addresses advance by additions: with one warp per scheduler
+// here, a multiplication and a comparison per store cost 80 cycles each.
+template <bool BF16, bool WIDE>
+struct OutTile {
+    static constexpr int kSize = BF16 ? 2 : 4;
+    char* p;
+    const float* scale;
+    long long step;      // bytes from a row of this lane to its next
+    int rows, cols;      // rows, and columns from this lane's first on, that exist
+    bool add;
+    __device__ __forceinline__ OutTile(const WgradLaunch& L, const Unit& w, int r0, int lane) : add(L.a.accumulate) {
+        const int row = r0 + (WIDE ? lane >> 3 : 0), col = w.n0 + (WIDE ? 4 * (lane & 7) : lane);
+        p = static_cast<char*>(L.a.grad) + (((long long)w.group * L.a.m + row) * L.a.n + col) * kSize;
+        scale = L.a.col_scale ? L.a.col_scale + col : nullptr;
+        step = (WIDE ? 4ll : 1ll) * L.a.n * kSize;
+        rows = WIDE ? min(max((L.a.m - row + 3) / 4, 0), 8) : min(max(L.a.m - row, 0), 32);
+        cols = L.a.n - col;
+    }
+
+    // f: the sums of the block at column c0 of the tile; times the column scale, and added to what
+    // is there when the call accumulates or `more`.  Every load comes before the first store.
+    __device__ __forceinline__ void put(float (&f)[32], int c0, bool more) const {
+        if (c0 >= cols) return;
+        more = more || add;
+        char* to = p + c0 * kSize;
+        const char* from = to;
+        if (WIDE) {   // n % 4 == 0: the four columns exist together
+            if (scale) {
+                const float s[4] = {scale[c0], scale[c0 + 1], scale[c0 + 2], scale[c0 + 3]};
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] *= s[i & 3];
+            }
+            if (more) {
+                float4 g[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i, from += step)
+                    if (i < rows) g[i] = load_four<BF16>(from);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[4 * i] += g[i].x, f[4 * i + 1] += g[i].y, f[4 * i + 2] += g[i].z, f[4 * i + 3] += g[i].w;
+            }
+            if (rows == 8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i, to += step) store_four<BF16>(to, f + 4 * i);
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i, to += step)
+                if (i < rows) store_four<BF16>(to, f + 4 * i);
+            return;
+        }
+        const float s = scale ? scale[c0] : 1.f;
+        if (more) {
+            float g[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i, from += step) g[i] = i < rows ? load_one<BF16>(from, 0) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = fmaf(f[i], s, g[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] *= s;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i, to += step)
+            if (i < rows) store_one<BF16>(to, 0, f[i]);
+    }
+};
 
 __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
 }
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t x) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
 }
 
-// TMA_Y: dy's rows are 16-byte aligned and come by TMA; else, and for the last step of an
-// expert's tokens, whose following rows are other experts', the conversion warps load them.
+// Eight token rows of dy (row .. row + 7 of the step at t0; zero from `left` on), columns m0 ..
+// m0 + 127, into the swizzled operand when its rows are not 16-byte aligned: a lane makes 16
+// bytes from the two aligned 16-byte pieces that hold them, two rows per pass.  Every piece
+// loaded holds an element of the row; columns at and beyond m get whatever lies there and
+// reach rows of the product that are not stored.
+__device__ __forceinline__ void copy_rows(const WgradArgs& a, long long t0, int left, int m0, int row, uint32_t dst,
+                                          int lane) {
+    const int j = lane & 15, col = m0 + 8 * j;
+    uint32_t v[4][8];
+    int d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = row + 2 * i + (lane >> 4);
+        const uintptr_t line = reinterpret_cast<uintptr_t>(a.dy) + (uintptr_t)((t0 + t) * a.lddy) * 2;
+        const uintptr_t at = line + (uintptr_t)col * 2;
+        d[i] = (int)(at & 15);
+        const uint4* p = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
+        const bool live = t < left && col < a.m;
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        if (live) x = *p;
+        if (live && d[i] && reinterpret_cast<uintptr_t>(p + 1) < line + (uintptr_t)a.m * 2) y = p[1];
+        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+        v[i][4] = y.x, v[i][5] = y.y, v[i][6] = y.z, v[i][7] = y.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = row + 2 * i + (lane >> 4);
+#pragma unroll
+        for (int k = 0; k < 6; ++k) v[i][k] = d[i] & 8 ? v[i][k + 2] : v[i][k];
+#pragma unroll
+        for (int k = 0; k < 5; ++k) v[i][k] = d[i] & 4 ? v[i][k + 1] : v[i][k];
+        const int sh = 8 * (d[i] & 2);
+        sts128(dst + (j >> 3) * WgCfg::CHUNK_BYTES + t * 128 + (((j & 7) ^ (t & 7)) << 4),
+               make_uint4(__funnelshift_r(v[i][0], v[i][1], sh), __funnelshift_r(v[i][1], v[i][2], sh),
+                          __funnelshift_r(v[i][2], v[i][3], sh), __funnelshift_r(v[i][3], v[i][4], sh)));
+    }
+}
+
+struct EpilogueArgs {
+    const Experts* ex;
+    uint32_t tmem_base, tempty_lead, blk;   // blk: this warp's staging block in shared memory
+    uint64_t* tfull;
+    volatile int* abort_flag;
+    int first, stride, q, wq, lane;
+};
+
+// One epilogue warp: TMEM lane quarter wq, 32 rows of the tile, each 32 x 32 block through
+// shared memory into the layout of OutTile.
+template <bool BF16, bool WIDE>
+__device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArgs& e) {
+    const int rl = e.lane >> 3, cl = 4 * (e.lane & 7);
+    int local = 0;
+    bool ok = true;
+    for (int u = e.first; ok && u < L.units; u += e.stride) {
+        const Unit w = decode_unit(L, e.ex, u);
+        const int chains = (int)((w.end - w.begin + L.chain - 1) / L.chain);
+        const OutTile<BF16, WIDE> out(L, w, w.m0 + 128 * e.q + 32 * e.wq, e.lane);
+        if (chains == 0) {   // an expert without tokens
+            for (int c0 = 0; c0 < 256 && !L.a.accumulate; c0 += 32) {
+                float f[32] = {};
+                out.put(f, c0, false);
+            }
+            continue;
+        }
+        // a part's sums go to the workspace, this warp's 32 x 256 of them as row-major rows
+        float* part = nullptr;
+        if (w.part >= 0)
+            part = L.a.partial + (((w.tile - L.whole) * 8ll + 4 * e.q + e.wq) * L.parts) * 8192 +
+                   (WIDE ? rl * 256 + cl : e.lane);
+        for (int ch = 0; ch < chains; ++ch) {
+            const uint32_t acc = local & 1;
+            if (!mbar_wait_idle(e.tfull + acc, local >> 1 & 1u, e.abort_flag, L.a.status, kStatusTimeoutEpilogue,
+                                true)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t tbase = e.tmem_base + acc * 256 + (static_cast<uint32_t>(e.wq * 32) << 16);
+            for (int c0 = 0; c0 < 256; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld32(tbase + c0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)   // undoes the operand's column order
+                    sts128(e.blk + e.lane * WgCfg::OUT_LD + j * 4, make_uint4(v[j], v[j + 2], v[j + 1], v[j + 3]));
+                __syncwarp();
+                float f[32];
+                if (WIDE) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 x = lds128(e.blk + (rl + 4 * i) * WgCfg::OUT_LD + cl * 4);
+                        f[4 * i] = __uint_as_float(x.x), f[4 * i + 1] = __uint_as_float(x.y);
+                        f[4 * i + 2] = __uint_as_float(x.z), f[4 * i + 3] = __uint_as_float(x.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(lds32(e.blk + i * WgCfg::OUT_LD + e.lane * 4));
+                }
+                __syncwarp();
+                if (part == nullptr) {
+                    out.put(f, c0, ch > 0);   // a later chain of tokens adds to what this warp wrote
+                } else {
+                    float* to = part + w.part * 8192 + c0;
+                    if (ch > 0) {
+                        float g[32];
+                        part_load<WIDE>(to, g);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] += g[i];
+                    }
+                    part_store<WIDE>(to, f);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (e.lane == 0) mbar_arrive_remote_cta(e.tempty_lead + acc * 8);   // TMEM alone changes hands
+            ++local;
+        }
+        if (part != nullptr && ok) {   // the warp that comes last adds up all parts, in their order
+            __threadfence();
+            __syncwarp();
+            int* count = L.a.counters + ((w.tile - L.whole) * 8 + 4 * e.q + e.wq);
+            int seen = 0;
+            if (e.lane == 0) seen = atomicAdd(count, 1);
+            if (__shfl_sync(0xffffffffu, seen, 0) == L.parts - 1) {
+                if (e.lane == 0) *count = 0;   // for the next call
+                __threadfence();
+                for (int c0 = 0; c0 < 256; c0 += 32) {
+                    float f[32];
+                    part_load<WIDE>(part + c0, f);
+                    for (int k = 1; k < L.parts; ++k) {
+                        float g[32];
+                        part_load<WIDE>(part + k * 8192 + c0, g);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] += g[i];
+                    }
+                    out.put(f, c0, false);
+                }
+            }
+        }
+    }
+}
+
+// TMA_Y: dy's rows are 16-byte aligned and come by TMA; else the conversion warps copy them.
 template <int FMT, bool TMA_Y, bool BF16>
 __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ WgradLaunch L) {
     using Cfg = WgCfg;
@@ -165,7 +442,8 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
     uint64_t* empty_r = full_r + kRingR;
     uint64_t* ready = empty_r + kRingR;
     uint64_t* empty = ready + kRingM;
-    uint64_t* tfull = empty + kRingM;
+    uint64_t* tail = empty + kRingM;
+    uint64_t* tfull = tail + kRingM;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -184,6 +462,7 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
         for (int s = 0; s < kRingM; ++s) {
             mbar_init(ready + s, 1 + 2 * kGroupWarps);
             mbar_init(empty + s, 1);
+            mbar_init(tail + s, 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull + a, 1);
@@ -207,13 +486,33 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
     pdl_trigger();
     pdl_wait();
 
+    Experts* ex = reinterpret_cast<Experts*>(smem + Cfg::EXPERTS_OFFSET);
+    if (L.a.offsets && L.a.groups <= kSortGroups) {
+        for (int g = threadIdx.x; g < L.a.groups; g += kWgThreads) {
+            long long b, e;
+            expert_range(L.a, g, &b, &e);
+            ex->begin[g] = (int)b, ex->end[g] = (int)e;
+        }
+        __syncthreads();
+        for (int g = threadIdx.x; g < L.a.groups; g += kWgThreads) {
+            const int n = ex->end[g] - ex->begin[g];
+            int rank = 0;
+            for (int h = 0; h < L.a.groups; ++h) {
+                const int o = ex->end[h] - ex->begin[h];
+                rank += o > n || (o == n && h < g);
+            }
+            ex->order[rank] = (uint16_t)g;
+        }
+        __syncthreads();
+    }
+
     if (warp == 0) {
         if (lane == 0) {
             // ---------------- TMA of x
             uint32_t it = 0;
             bool ok = true;
             for (int u = first; ok && u < L.units; u += stride) {
-                const Unit w = decode_unit(L, u);
+                const Unit w = decode_unit(L, ex, u);
                 const int steps = unit_steps(w);
                 const int xn = w.n0 + 128 * (int)q;
                 for (int k = 0; k < steps; ++k, ++it) {
@@ -245,7 +544,7 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
             uint32_t slot = 0, ph = 1;
             bool ok = true;
             for (int u = first; ok && u < L.units; u += stride) {
-                const Unit w = decode_unit(L, u);
+                const Unit w = decode_unit(L, ex, u);
                 const int steps = unit_steps(w);
                 const int ym = w.m0 + 128 * (int)q;
                 for (int k = 0; k < steps; ++k) {
@@ -254,10 +553,17 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
                         break;
                     }
                     const long long t0 = w.begin + (long long)k * kWgStepT;
-                    if (!TMA_Y || t0 + kWgStepT > w.end) {   // filled by the conversion warps
+                    uint8_t* sa = smem + slot * Cfg::SLOT_BYTES;
+                    if (!TMA_Y || t0 + kWgStepT > w.end) {
+                        // the conversion warps fill it, or first see it land (tail) and zero the rows that
+                        // belong to other experts
+                        if (TMA_Y) {
+                            mbar_arrive_expect_tx(tail + slot, Cfg::A_BYTES);
+                            tma_load_2d(sa, &L.map_y, tail + slot, ym, (int)t0);
+                            tma_load_2d(sa + Cfg::CHUNK_BYTES, &L.map_y, tail + slot, ym + 64, (int)t0);
+                        }
                         if (leader) mbar_arrive(ready + slot);
                     } else {
-                        uint8_t* sa = smem + slot * Cfg::SLOT_BYTES;
                         const uint32_t fb = mapa_shared(smem_u32(ready + slot), 0);
                         if (leader) mbar_arrive_expect_tx(ready + slot, 2 * Cfg::A_BYTES);
                         tma_load_2d_pair(sa, &L.map_y, fb, ym, (int)t0);
@@ -273,19 +579,21 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
-            // ---------------- MMA issue.  The tensor cores queue few instructions, so what this thread
-            // does between two steps' MMAs is time they may idle: the next step's barrier is tested
-            // before the step's last MMA is issued.
+        if (leader) {
+            // ---------------- MMA issue.  The tensor cores queue few instructions, so what this warp
+            // does between two steps' MMAs is time they may idle: the whole warp runs the loop, so that
+            // addresses stay in uniform registers, one elected lane issues, and the next step's barrier
+            // is tested before the step's last MMA is issued.
+            const bool one = elect_one();
             uint32_t slot = 0, ph = 0;
             int local = 0;
             bool ok = true, next = false;
             constexpr uint32_t idesc = idesc_make(true, 256, 256, true, true);
-            constexpr uint64_t kSlot = Cfg::SLOT_BYTES >> 4, kStep = 16 * 128 >> 4;   // of the address field
+            constexpr uint32_t kSlot = Cfg::SLOT_BYTES >> 4, kStep = 16 * 128 >> 4;   // of the address field
             const uint64_t ad0 = sdesc_sw128(smem_u32(smem), Cfg::CHUNK_BYTES, 1024);
             const uint64_t bd0 = sdesc_sw128(smem_u32(smem) + Cfg::A_BYTES, Cfg::CHUNK_BYTES, 1024);
             for (int u = first; ok && u < L.units; u += stride) {
-                const Unit w = decode_unit(L, u);
+                const Unit w = decode_unit(L, ex, u);
                 const int steps = unit_steps(w), chain = L.chain / kWgStepT;
                 const int last = ((int)(w.end - w.begin - 1) & (kWgStepT - 1)) / 16 + 1;   // MMAs of the last step
                 for (int k0 = 0; ok && k0 < steps; k0 += chain, ++local) {
@@ -298,6 +606,7 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
                     tc_fence_after();
                     const uint32_t d = tmem_base + acc * 256;
                     const int k1 = min(steps, k0 + chain);
+                    const int whole = k1 == steps && last < 4 ? k1 - 1 : k1;
                     for (int k = k0; k < k1; ++k) {
                         if (!next && !mbar_wait(ready + slot, ph, abort_flag, L.a.status, kStatusTimeoutMma)) {
                             ok = false;
@@ -306,28 +615,42 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
                         tc_fence_after();
                         const uint64_t ad = ad0 + slot * kSlot, bd = bd0 + slot * kSlot;
                         uint64_t* done = empty + slot;
-                        const int n = k == steps - 1 ? last : 4;
-                        mma_f16kind_pair(d, ad, bd, idesc, k != k0);
-                        for (int kk = 1; kk < n - 1; ++kk) mma_f16kind_pair(d, ad + kk * kStep, bd + kk * kStep, idesc, 1);
                         if (++slot == kRingM) slot = 0, ph ^= 1u;
-                        next = mbar_test_wait(ready + slot, ph);
-                        if (n > 1) mma_f16kind_pair(d, ad + (n - 1) * kStep, bd + (n - 1) * kStep, idesc, 1);
-                        mma_commit_pair(done, 0x3);
+                        if (k < whole) {
+                            if (one) {
+                                mma_f16kind_pair(d, ad, bd, idesc, k != k0);
+                                mma_f16kind_pair(d, ad + kStep, bd + kStep, idesc, 1);
+                                mma_f16kind_pair(d, ad + 2 * kStep, bd + 2 * kStep, idesc, 1);
+                            }
+                            next = mbar_test_wait(ready + slot, ph);
+                            if (one) {
+                                mma_f16kind_pair(d, ad + 3 * kStep, bd + 3 * kStep, idesc, 1);
+                                mma_commit_pair(done, 0x3);
+                            }
+                        } else {
+                            if (one) {
+                                for (int kk = 0; kk < last; ++kk)
+                                    mma_f16kind_pair(d, ad + kk * kStep, bd + kk * kStep, idesc, (k - k0) | kk);
+                                mma_commit_pair(done, 0x3);
+                            }
+                            next = false;
+                        }
                     }
-                    if (ok) mma_commit_pair(tfull + acc, 0x3);
+                    if (ok && one) mma_commit_pair(tfull + acc, 0x3);
                 }
             }
-            mma_commit_pair(drain, 0x1);
+            if (one) mma_commit_pair(drain, 0x1);
             const unsigned long long t0 = globaltimer_ns();
             while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
             }
+            __syncwarp();
         }
     } else if (warp < kEpiFirst) {
         // ---------------- conversion: warp cw of the kGroupWarps that take every kConvGroups-th step
         const int cw = (warp - kConvFirst) % kGroupWarps;
         const uint32_t cg = (warp - kConvFirst) / kGroupWarps;
         const uint32_t ready_lead = mapa_shared(smem_u32(ready), 0);
-        uint32_t it = 0;
+        uint32_t it = 0, tail_ph = 0;   // tail_ph: phase bit of each slot's tail barrier
         bool ok = true;
         // A pass of a warp takes eight token rows: lane l the row p of l / 8, or p ^ 5 for the upper
         // four of its eight lanes, and 16 codes (16-byte piece l & 3) of either 64-column half.
@@ -340,15 +663,14 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
         const uint32_t dst0 = row0 * 128 + (((2 * pc) ^ prow) << 4);       // its second piece: ^ 16
         const uint32_t sel = 0x0404u + 0x1010u * (pc >> 1);                // its scale byte in bytes 1 and 3
         for (int u = first; ok && u < L.units; u += stride) {
-            const Unit w = decode_unit(L, u);
+            const Unit w = decode_unit(L, ex, u);
             const int steps = unit_steps(w);
             const int off = ((w.n0 + 128 * (int)q) >> 5) & 15;   // the CTA's four of the 16 loaded scales
             for (int k = 0; k < steps; ++k, ++it) {
                 const int left = (int)min((long long)kWgStepT, w.end - w.begin - (long long)k * kWgStepT);
-                const bool plain = !TMA_Y || left < kWgStepT;
                 if (it % kConvGroups != cg) continue;
                 const uint32_t r = it % kRingR, b = it % kRingM;
-                const uint8_t* sr = smem + Cfg::R_OFFSET + r * Cfg::R_BYTES;
+                const uint32_t sr = smem_u32(smem + Cfg::R_OFFSET + r * Cfg::R_BYTES);
                 const uint32_t sa = smem_u32(smem + b * Cfg::SLOT_BYTES), sb = sa + Cfg::A_BYTES;
                 if (!mbar_wait_idle(full_r + r, it / kRingR & 1u, abort_flag, L.a.status, kStatusTimeoutProducer,
                                     false)) {
@@ -359,9 +681,9 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
                 uint32_t sc[kRows / 8];
 #pragma unroll
                 for (int i = 0; i < kRows / 8; ++i) {
-                    raw[2 * i] = *reinterpret_cast<const uint4*>(sr + i * 1024 + src0);
-                    raw[2 * i + 1] = *reinterpret_cast<const uint4*>(sr + i * 1024 + (src0 ^ 64));
-                    sc[i] = *reinterpret_cast<const uint32_t*>(sr + Cfg::RAW_BYTES + (row0 + 8 * i) * 16 + off);
+                    raw[2 * i] = lds128(sr + i * 1024 + src0);
+                    raw[2 * i + 1] = lds128(sr + i * 1024 + (src0 ^ 64));
+                    sc[i] = lds32(sr + Cfg::RAW_BYTES + (row0 + 8 * i) * 16 + off);
                 }
                 if (left < kWgStepT) {
 #pragma unroll
@@ -382,17 +704,21 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
                     sts128(to + dst0, make_uint4(a.x, a.y, d.x, d.y));
                     sts128(to + (dst0 ^ 16), make_uint4(e.x, e.y, f.x, f.y));
                 }
-                if (plain) {   // dy: the warp's token rows, columns 2 lane, 2 lane + 1 of both halves
-                    const int ym = w.m0 + 128 * (int)q + 2 * lane;
-#pragma unroll 16
-                    for (int i = 0; i < 2 * kRows; ++i) {
-                        const int t = cw * kRows + (i >> 1), col = ym + 64 * (i & 1);
-                        const uint16_t* p = static_cast<const uint16_t*>(L.a.dy) +
-                                            (w.begin + (long long)k * kWgStepT + t) * L.a.lddy + col;
-                        const uint32_t y0 = t < left && col < L.a.m ? p[0] : 0;
-                        const uint32_t y1 = t < left && col + 1 < L.a.m ? p[1] : 0;
-                        sts32(sa + (i & 1) * Cfg::CHUNK_BYTES + t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4,
-                              y0 | y1 << 16);
+                if (!TMA_Y) {
+                    const long long t0 = w.begin + (long long)k * kWgStepT;
+                    for (int b0 = 0; b0 < kRows / 2; b0 += 4)
+                        copy_rows(L.a, t0, left, w.m0 + 128 * (int)q, cw * kRows + 2 * b0, sa, lane);
+                } else if (left < kWgStepT) {
+                    // the rows that follow belong to other experts: zero, whatever they hold
+                    if (!mbar_wait_idle(tail + b, tail_ph >> b & 1u, abort_flag, L.a.status, kStatusTimeoutProducer,
+                                        false)) {
+                        ok = false;
+                        break;
+                    }
+                    tail_ph ^= 1u << b;
+                    for (int t = max(left, cw * kRows); t < (cw + 1) * kRows; ++t) {
+                        sts32(sa + t * 128 + lane * 4, 0);
+                        sts32(sa + Cfg::CHUNK_BYTES + t * 128 + lane * 4, 0);
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // writes visible to the MMAs
@@ -411,102 +737,19 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
             }
         }
     } else {
-        // ---------------- epilogue: TMEM lane quarter = warp % 4.  Each 32 x 32 block goes through
-        // shared memory, so that a warp reads and writes grad in 128-byte row pieces: four rows at a
-        // time, four columns per lane, where the rows are aligned, else one row, a column per lane.
-        const int wq = warp & 3;
-        const uint32_t tempty_lead = mapa_shared(smem_u32(tempty), 0);
-        float* blk = reinterpret_cast<float*>(smem + Cfg::OUT_OFFSET + (warp - kEpiFirst) * Cfg::OUT_WARP);
-        const int rl = lane >> 3, cl = 4 * (lane & 7);
-        int local = 0;
-        bool ok = true;
-        for (int u = first; ok && u < L.units; u += stride) {
-            const Unit w = decode_unit(L, u);
-            const int chains = (int)((w.end - w.begin + L.chain - 1) / L.chain);
-            const int r0 = w.m0 + 128 * (int)q + 32 * wq;
-            const int rows = min(32, L.a.m - r0);
-            const long long gbase = ((long long)w.group * L.a.m + r0) * L.a.n;
-            if (chains == 0 && L.a.accumulate) continue;
-            for (int ch = 0; ch < max(chains, 1); ++ch) {
-                const bool any = chains > 0;
-                const bool add = L.a.accumulate || ch > 0;   // a later chain of tokens adds to what this warp wrote
-                const uint32_t acc = local & 1;
-                if (any && !mbar_wait_idle(tfull + acc, local >> 1 & 1u, abort_flag, L.a.status,
-                                           kStatusTimeoutEpilogue, true)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t tbase = tmem_base + acc * 256 + (static_cast<uint32_t>(wq * 32) << 16);
-                for (int c0 = 0; c0 < 256 && w.n0 + c0 < L.a.n && rows > 0; c0 += 32) {
-                    const bool wide = L.wide && w.n0 + c0 + 32 <= L.a.n;
-                    float4 g[8];
-                    if (wide) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + rl;
-                            g[i] = add && r < rows ? load_four<BF16>(L.a.grad, gbase + (long long)r * L.a.n + w.n0 + c0 + cl)
-                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-                        }
-                    }
-                    if (any) {
-                        uint32_t v[32];
-                        tmem_ld32(tbase + c0, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4)   // undoes the operand's column order
-                            *reinterpret_cast<uint4*>(blk + lane * Cfg::OUT_LD + j) =
-                                make_uint4(v[j], v[j + 2], v[j + 1], v[j + 3]);
-                        __syncwarp();
-                    }
-                    if (wide) {
-                        float4 cs = make_float4(1.f, 1.f, 1.f, 1.f);
-                        if (L.a.col_scale) {
-                            const float* p = L.a.col_scale + w.n0 + c0 + cl;
-                            cs = make_float4(p[0], p[1], p[2], p[3]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + rl;
-                            if (any) {
-                                const float4 v = *reinterpret_cast<const float4*>(blk + r * Cfg::OUT_LD + cl);
-                                g[i].x = fmaf(v.x, cs.x, g[i].x), g[i].y = fmaf(v.y, cs.y, g[i].y);
-                                g[i].z = fmaf(v.z, cs.z, g[i].z), g[i].w = fmaf(v.w, cs.w, g[i].w);
-                            }
-                            if (r < rows)
-                                store_four<BF16>(L.a.grad, gbase + (long long)r * L.a.n + w.n0 + c0 + cl, g[i]);
-                        }
-                    } else if (w.n0 + c0 + lane < L.a.n) {
-                        const int col = w.n0 + c0 + lane;
-                        const float cs = L.a.col_scale ? L.a.col_scale[col] : 1.f;
-                        for (int rb = 0; rb < rows; rb += 8) {
-                            float v[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                v[i] = add && rb + i < rows ? load_one<BF16>(L.a.grad, gbase + (long long)(rb + i) * L.a.n + col)
-                                                            : 0.f;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                if (any) v[i] = fmaf(blk[(rb + i) * Cfg::OUT_LD + lane], cs, v[i]);
-                                if (rb + i < rows) store_one<BF16>(L.a.grad, gbase + (long long)(rb + i) * L.a.n + col, v[i]);
-                            }
-                        }
-                    }
-                    __syncwarp();
-                }
-                if (any) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (leader)
-                            mbar_arrive(tempty + acc);
-                        else
-                            mbar_arrive_remote(tempty_lead + acc * 8);
-                    }
-                    ++local;
-                }
-            }
-        }
+        // ---------------- epilogue
+        EpilogueArgs e;
+        e.ex = ex;
+        e.tmem_base = tmem_base;
+        e.tfull = tfull;
+        e.tempty_lead = mapa_shared(smem_u32(tempty), 0);
+        e.blk = smem_u32(smem + Cfg::OUT_OFFSET + (warp - kEpiFirst) * Cfg::OUT_WARP);
+        e.abort_flag = abort_flag;
+        e.first = first, e.stride = stride, e.q = (int)q, e.wq = warp & 3, e.lane = lane;
+        if (L.wide)
+            epilogue<BF16, true>(L, e);
+        else
+            epilogue<BF16, false>(L, e);
     }
 
     tc_fence_before();
@@ -562,7 +805,23 @@ cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaS
     L.tiles_n = (a.n + 255) / 256;
     const long long units = (long long)a.groups * L.tiles_m * L.tiles_n;
     if (units >= (1ll << 31)) return cudaErrorInvalidValue;
-    L.units = (int)units;
+    const int pairs = sm_count / 2;
+    L.whole = (int)units;
+    L.parts = 1;
+    if (!a.offsets) {
+        // The tiles of the last, incomplete turn (all tiles, when they are fewer than the CTA
+        // pairs) are split along the tokens into the number of parts that is estimated fastest:
+        // 0.3 us per step of 64 tokens, and joining about 5 us for each part.
+        const int rest = (int)(units % pairs);
+        const long long steps = (a.tokens + kWgStepT - 1) / kWgStepT;
+        double best = 0.3 * steps;
+        for (int p = 2; rest > 0 && p <= 8 && rest * p <= kMaxParts && p <= steps; ++p) {
+            const double t = 0.3 * (double)((rest * p + pairs - 1) / pairs) * (double)((steps + p - 1) / p) + 5.0 * p;
+            if (t < best) best = t, L.parts = p;
+        }
+        if (L.parts > 1) L.whole = (int)units - rest;
+    }
+    L.units = L.whole + ((int)units - L.whole) * L.parts;
     // The tensor cores' adds truncate: the sum of one accumulator drifts by about 1.1e-5 of
     // itself over 16384 tokens of random data, in proportion to their number.  An fp32 gradient
     // keeps that below 6e-6 by adding up partial sums of 8192 tokens in the epilogue.
@@ -574,8 +833,7 @@ cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaS
         !map_2d(&L.map_x, a.x.codes, true, a.n, a.tokens, a.x.ldq, 128, true) ||
         !map_2d(&L.map_s, a.x.scales, true, (a.n + kActGroup - 1) / kActGroup, a.tokens, a.x.lds, 16, false))
         return cudaErrorInvalidValue;
-    const unsigned pairs = (unsigned)std::min<long long>(units, sm_count / 2);
-    return launch_pdl_cluster(pick(a.x.format, tma_y, bf16_grad), dim3(2 * pairs), dim3(kWgThreads), WgCfg::SMEM_BYTES,
+        return launch_pdl_cluster(pick(a.x.format, tma_y, bf16_grad), dim3(2 * std::min(L.units, pairs)), dim3(kWgThreads), WgCfg::SMEM_BYTES,
                               s, 2u, L);
 }
 
