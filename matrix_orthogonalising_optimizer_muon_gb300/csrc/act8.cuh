@@ -39,28 +39,56 @@ __device__ __forceinline__ void store_one(void* p, long long i, float v) {
         static_cast<float*>(p)[i] = v;
 }
 
-// The segment's values of row pointer p (already at the row), columns c0 .. c0 + 255;
-// zero at and beyond `cols`.
+// A lane's eight values of a segment as loaded: bf16 in pairs (VEC), else fp32.  Loading and
+// widening are apart so that several segments' loads can be in flight in few registers.
+template <bool BF16, bool VEC>
+struct Raw {
+    static constexpr bool kPairs = BF16 && VEC;
+    uint32_t r[kPairs ? 4 : 8];
+
+    // Columns c0 .. c0 + 255 of the row at p; zero at and beyond `cols`.
+    __device__ __forceinline__ void load(const void* p, int c0, int cols, int lane) {
+        if (VEC && c0 + 8 * lane + 8 <= cols) {
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + (long long)(c0 + 8 * lane) * (BF16 ? 2 : 4));
+            const uint4 a = q[0];
+            r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
+            if constexpr (!kPairs) {
+                const uint4 b = q[1];
+                r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+            }
+            return;
+        }
+        if constexpr (kPairs) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = c0 + 8 * lane + 2 * j;
+                const uint16_t* q = static_cast<const uint16_t*>(p) + c;
+                r[j] = (c < cols ? q[0] : 0u) | (c + 1 < cols ? (uint32_t)q[1] << 16 : 0u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = c0 + seg_col<VEC>(lane, j);
+                r[j] = c < cols ? __float_as_uint(load_one<BF16>(p, c)) : 0u;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if constexpr (kPairs)
+                v[j] = j & 1 ? bf16_hi(r[j >> 1]) : bf16_lo(r[j >> 1]);
+            else
+                v[j] = __uint_as_float(r[j]);
+    }
+};
+
+// The segment's values of row pointer p, columns c0 .. c0 + 255; zero at and beyond `cols`.
 template <bool BF16, bool VEC>
 __device__ __forceinline__ void seg_load(const void* p, int c0, int cols, int lane, float (&v)[8]) {
-    if (VEC && c0 + 8 * lane + 8 <= cols) {
-        const long long e = c0 + 8 * lane;
-        if (BF16) {
-            const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + e);
-            v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
-            v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
-        } else {
-            const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
-            const float4 a = f[0], b = f[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int c = c0 + seg_col<VEC>(lane, j);
-        v[j] = c < cols ? load_one<BF16>(p, c) : 0.f;
-    }
+    Raw<BF16, VEC> raw;
+    raw.load(p, c0, cols, lane);
+    raw.get(v);
 }
 
 template <bool BF16, bool VEC>
@@ -88,9 +116,10 @@ __device__ __forceinline__ void seg_store(void* p, int c0, int cols, int lane, c
 // smallest biased exponent with a <= L 2^e, L = 448 = 1.75 2^8 or 127 = 1.984375 2^6.
 // Adding 2^23 - 1 - mantissa(L) carries into the exponent exactly when the mantissa of a
 // exceeds that of L.  An infinity or NaN gives 255.
-__device__ __forceinline__ uint32_t act_scale_byte(uint32_t a, int format) {
-    const int e = format == kE4M3 ? (int)((a + 0x1fffffu) >> 23) - 8 : (int)((a + 0x01ffffu) >> 23) - 6;
-    const int top = format == kE4M3 ? 127 + 119 : 127 + 121;
+template <int FMT>
+__device__ __forceinline__ uint32_t act_scale_byte(uint32_t a) {
+    const int e = FMT == kE4M3 ? (int)((a + 0x1fffffu) >> 23) - 8 : (int)((a + 0x01ffffu) >> 23) - 6;
+    const int top = FMT == kE4M3 ? 127 + 119 : 127 + 121;
     return a >= 0x7f800000u ? 255u : (uint32_t)min(max(e, 127 - 110), top);
 }
 // 2^-e of a scale byte (17 .. 248); zero for a group that is not finite, so its codes are zero.
@@ -103,29 +132,39 @@ __device__ __forceinline__ float act_scale(uint32_t byte) {
 }
 
 // Two values already divided by their scale -> two codes (low byte first).
-__device__ __forceinline__ uint32_t act_code2(float a, float b, int format) {
-    if (format == kE4M3) {
+template <int FMT>
+__device__ __forceinline__ uint32_t act_code2(float a, float b) {
+    if (FMT == kE4M3) {
         uint16_t r;   // round to nearest even, saturating at 448; b goes to the low byte
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
         return r;
     }
-    // groups clamped at the largest scale may exceed 127
-    const int x = __float2int_rn(fminf(fmaxf(a, -127.f), 127.f)), y = __float2int_rn(fminf(fmaxf(b, -127.f), 127.f));
-    return (uint32_t)(x & 0xff) | ((uint32_t)(y & 0xff) << 8);
+    // groups clamped at the largest scale may exceed 127; 1.5 * 2^23 rounds to a whole number in
+    // the low bits, ties to even
+    const uint32_t x = __float_as_uint(fminf(fmaxf(a, -127.f), 127.f) + 12582912.f);
+    const uint32_t y = __float_as_uint(fminf(fmaxf(b, -127.f), 127.f) + 12582912.f);
+    return __byte_perm(x, y, 0x7740) & 0xffffu;
 }
-// Two codes (low byte first) -> their numbers.
-__device__ __forceinline__ float2 act_number2(uint32_t q, int format) {
-    if (format == kE4M3) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)q));
-        return __half22float2(*reinterpret_cast<__half2*>(&h));
+// Four codes (low byte first) -> their numbers.
+template <int FMT>
+__device__ __forceinline__ void act_number4(uint32_t w, float* v) {
+    if (FMT == kE4M3) {
+        uint32_t h[2];
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[0]) : "h"((uint16_t)(w & 0xffff)));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[1]) : "h"((uint16_t)(w >> 16)));
+        const float2 a = __half22float2(*reinterpret_cast<__half2*>(h));
+        const float2 b = __half22float2(*reinterpret_cast<__half2*>(h + 1));
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+        return;
     }
-    return make_float2((float)(int8_t)(q & 0xff), (float)(int8_t)((q >> 8) & 0xff));
+    const uint32_t u = w ^ 0x80808080u;   // code + 128, then 2^23 + that, as the bits of a float
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 | j)) - 8388736.f;
 }
 
 // Writes the segment in 8 bits at row `row`.  Values beyond `cols` must be zero; lanes of
 // a partly filled last group take part with those zeros.
-template <bool VEC>
+template <int FMT, bool VEC>
 __device__ __forceinline__ void seg_quant(const Act8& q, long long row, int c0, int cols, int lane,
                                           const float (&v)[8]) {
     uint8_t* codes = q.codes + row * q.ldq + c0;
@@ -134,17 +173,14 @@ __device__ __forceinline__ void seg_quant(const Act8& q, long long row, int c0, 
 #pragma unroll
     for (int j = 0; j < 8; ++j) m[j] = __float_as_uint(v[j]) & 0x7fffffffu;
     if (VEC) {
-        uint32_t a = max(max(max(m[0], m[1]), max(m[2], m[3])), max(max(m[4], m[5]), max(m[6], m[7])));
+        uint32_t a = __vimax3_u32(__vimax3_u32(m[0], m[1], m[2]), __vimax3_u32(m[3], m[4], m[5]), max(m[6], m[7]));
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-        const uint32_t byte = act_scale_byte(a, q.format);
+        const uint32_t byte = act_scale_byte<FMT>(a);
         const float inv = act_inverse(byte);
-        float w[8];
-        // inv = 0 marks a group that is not finite: its codes are zero (0 * inf would be NaN)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = inv == 0.f ? 0.f : v[j] * inv;
-        const uint32_t lo = act_code2(w[0], w[1], q.format) | act_code2(w[2], w[3], q.format) << 16;
-        const uint32_t hi = act_code2(w[4], w[5], q.format) | act_code2(w[6], w[7], q.format) << 16;
+        uint32_t lo = act_code2<FMT>(v[0] * inv, v[1] * inv) | act_code2<FMT>(v[2] * inv, v[3] * inv) << 16;
+        uint32_t hi = act_code2<FMT>(v[4] * inv, v[5] * inv) | act_code2<FMT>(v[6] * inv, v[7] * inv) << 16;
+        if (byte == 255u) lo = hi = 0;   // a group that is not finite
         // row pitches are multiples of 16: the eight bytes lie within the row's padding
         if (c0 + 8 * lane < cols) {
             *reinterpret_cast<uint2*>(codes + 8 * lane) = make_uint2(lo, hi);
@@ -154,44 +190,79 @@ __device__ __forceinline__ void seg_quant(const Act8& q, long long row, int c0, 
         uint32_t mine = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t byte = act_scale_byte(__reduce_max_sync(0xffffffffu, m[j]), q.format);
+            const uint32_t byte = act_scale_byte<FMT>(__reduce_max_sync(0xffffffffu, m[j]));
             if (lane == j) mine = byte;
-            const float inv = act_inverse(byte);
-            const float w = inv == 0.f ? 0.f : v[j] * inv;
-            if (c0 + 32 * j + lane < cols) codes[32 * j + lane] = (uint8_t)act_code2(w, 0.f, q.format);
+            const uint32_t code = byte == 255u ? 0u : act_code2<FMT>(v[j] * act_inverse(byte), 0.f);
+            if (c0 + 32 * j + lane < cols) codes[32 * j + lane] = (uint8_t)code;
         }
         if (lane < 8 && c0 + 32 * lane < cols) scales[lane] = (uint8_t)mine;
     }
 }
-
-// Reads the segment of row `row` back; zero at and beyond `cols`.
+// The same, the format chosen at run time (uniform over the launch).
 template <bool VEC>
-__device__ __forceinline__ void seg_dequant(const Act8& q, long long row, int c0, int cols, int lane, float (&v)[8]) {
-    const uint8_t* codes = q.codes + row * q.ldq + c0;
-    const uint8_t* scales = q.scales + row * q.lds + (c0 >> 5);
-    if (VEC) {
-        uint2 w = make_uint2(0, 0);
-        float s = 0.f;
-        if (c0 + 8 * lane < cols) {   // the row's padding completes the eight bytes
-            w = *reinterpret_cast<const uint2*>(codes + 8 * lane);
-            s = act_scale(scales[lane >> 2]);
-        }
-        const float2 a = act_number2(w.x & 0xffff, q.format), b = act_number2(w.x >> 16, q.format);
-        const float2 c = act_number2(w.y & 0xffff, q.format), d = act_number2(w.y >> 16, q.format);
-        v[0] = a.x * s, v[1] = a.y * s, v[2] = b.x * s, v[3] = b.y * s;
-        v[4] = c.x * s, v[5] = c.y * s, v[6] = d.x * s, v[7] = d.y * s;
-        if (c0 + 8 * lane + 8 > cols) {
+__device__ __forceinline__ void seg_quant(const Act8& q, long long row, int c0, int cols, int lane,
+                                          const float (&v)[8]) {
+    if (q.format == kE4M3)
+        seg_quant<kE4M3, VEC>(q, row, c0, cols, lane, v);
+    else
+        seg_quant<kInt8, VEC>(q, row, c0, cols, lane, v);
+}
+
+// A lane's share of a segment in 8 bits as loaded: eight codes and their scale byte (VEC), else
+// eight codes, each with its group's byte above it.
+template <bool VEC>
+struct Raw8 {
+    uint32_t r[VEC ? 3 : 8];
+
+    // The segment of row `row`; reads as zero at and beyond `cols`.
+    __device__ __forceinline__ void load(const Act8& q, long long row, int c0, int cols, int lane) {
+        load(q.codes + row * q.ldq, q.scales + row * q.lds, c0, cols, lane);
+    }
+    __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int c0, int cols, int lane) {
+        codes += c0, scales += c0 >> 5;
+        if constexpr (VEC) {
+            r[0] = r[1] = r[2] = 0;
+            if (c0 + 8 * lane < cols) {   // the row's padding completes the eight bytes
+                const uint2 w = *reinterpret_cast<const uint2*>(codes + 8 * lane);
+                r[0] = w.x, r[1] = w.y, r[2] = scales[lane >> 2];
+                const int left = cols - c0 - 8 * lane;
+                if (left < 8) {   // padding: whatever it holds
+                    r[0] &= left >= 4 ? 0xffffffffu : (1u << 8 * left) - 1u;
+                    r[1] &= left <= 4 ? 0u : (1u << 8 * (left - 4)) - 1u;
+                }
+            }
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c0 + 8 * lane + j >= cols) v[j] = 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = 32 * j + lane;
-            v[j] = c0 + c < cols ? act_number2(codes[c], q.format).x * act_scale(scales[j]) : 0.f;
+            for (int j = 0; j < 8; ++j) {
+                const int c = 32 * j + lane;
+                r[j] = c0 + c < cols ? codes[c] | (uint32_t)scales[j] << 8 : 0u;
+            }
         }
     }
-}
+    template <int FMT>
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (VEC) {
+            const float s = act_scale(r[2]);
+            act_number4<FMT>(r[0], v);
+            act_number4<FMT>(r[1], v + 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= s;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t w = r[j];
+                float n[4];
+                act_number4<FMT>(w & 0xffu, n);
+                v[j] = n[0] * act_scale(w >> 8);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int format, float (&v)[8]) const {
+        if (format == kE4M3)
+            get<kE4M3>(v);
+        else
+            get<kInt8>(v);
+    }
+};
 
 }  // namespace muon

@@ -244,6 +244,7 @@ muon_status muon_grad_plan_create(muon_grad_plan* out) {
         }
     }
     if (st == MUON_OK) st = cuda_status(wgrad_prepare());
+    if (st == MUON_OK) st = cuda_status(rmsnorm_prepare());
     if (st == MUON_OK) st = cuda_status(cudaMemset(p->ws, 0, kWsHeader));
     if (st == MUON_OK) st = cuda_status(cudaDeviceSynchronize());
     if (st != MUON_OK) {
@@ -295,6 +296,7 @@ muon_status muon_rmsnorm_backward(muon_grad_plan p, const void* dy, int64_t lddy
     MUON_CALL(check_grad_plan(p));
     a.weight = weight, a.rstd = rstd, a.dweight = dweight, a.accumulate = accumulate != 0;
     a.partial = dweight ? p->partial : nullptr;
+    a.status = p->status;
     a.rows = rows, a.cols = (int)cols;
     const bool vec = c.vec && aligned16(weight, 0);
     return cuda_status(

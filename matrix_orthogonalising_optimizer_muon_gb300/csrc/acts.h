@@ -59,6 +59,7 @@ struct NormBwdArgs {
     float* partial;      // per block, cols sums of dy xhat; null: dweight not wanted
     float* dweight;
     int accumulate;
+    int* status;
     long long rows;
     int cols;
 };
@@ -86,6 +87,7 @@ cudaError_t launch_act_unpack(const PackArgs& a, bool bf16, bool vec, cudaStream
 cudaError_t launch_swiglu_forward(const SwigluArgs& a, bool bf16, bool vec, cudaStream_t s);
 cudaError_t launch_swiglu_backward(const SwigluArgs& a, bool bf16, bool vec, cudaStream_t s);
 cudaError_t launch_rmsnorm_forward(const NormArgs& a, bool bf16, bool vec, cudaStream_t s);
+cudaError_t rmsnorm_prepare();   // once per device, before the first backward launch
 // Blocks of the backward kernel for these sizes (its partial sums: blocks x cols floats).
 int rmsnorm_backward_blocks(long long rows, int cols, int sm_count);
 constexpr long long kNormPartialFloats = 8ll << 20;   // bound on blocks x cols

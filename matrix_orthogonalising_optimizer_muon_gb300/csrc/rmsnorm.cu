@@ -2,6 +2,8 @@
 //
 // One block per row; warp w of the block holds segments w, w + W, ... of the row (256
 // values each, eight per lane) in registers, so every value crosses HBM once each way.
+#include <algorithm>
+
 #include "act8.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -10,33 +12,47 @@ namespace muon {
 namespace {
 
 constexpr int kMaxThreads = 512;   // 128 registers per thread: up to eight segments per warp
+// Least segments per warp.  Forward: with two a row's block is small enough for many to share an SM,
+// one reducing while others load (16384 x 3584 bf16: 88 us, 99 with one, 97 with four).
+constexpr int kFwdSegs = 2, kBwdSegs = 1;
+// Backward: warps per SM (the same: 83 us; 88 with 14 warps of two segments, 99 with 42 of one).
+constexpr int kBwdWarps = 28;
+constexpr int kRingRoom = 216 * 1024;   // backward: shared memory of an SM for rows on their way
 
 template <bool BF16>
 __device__ __forceinline__ void* row_ptr(const Mat& m, long long row) {
     return static_cast<char*>(m.p) + row * m.ld * (BF16 ? 2 : 4);
 }
 
-// Sum over the block, the same in every thread.  Fixed order: lanes by butterfly, warps in
-// sequence.  `red` has room for one float per warp; two barriers allow its reuse.
+// Sum over the block, the same in every thread, in a fixed order: lanes by butterfly, warps in
+// sequence.  `red` has room for one float per warp; consecutive calls alternate between two
+// such rows, so one barrier each is enough.
+template <bool ALWAYS>   // a barrier even for a single warp
 __device__ __forceinline__ float block_sum(float x, float* red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     const int warps = blockDim.x >> 5;
-    if (warps == 1) return x;
+    if (warps == 1) {
+        if (ALWAYS) __syncthreads();
+        return x;
+    }
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
     __syncthreads();
-    float t = 0.f;
-    for (int w = 0; w < warps; ++w) t += red[w];
-    __syncthreads();
-    return t;
+    // 16 warps at most: four 16-byte reads, absent warps read as the zeros stored at the start
+    const float4* r = reinterpret_cast<const float4*>(red);
+    const float4 a = r[0], b = r[1], c = r[2], d = r[3];
+    return (((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w))) +
+           (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
 }
 
 // S segments per warp.
 template <bool BF16, bool VEC, int S>
 __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_forward(const NormArgs a) {
-    __shared__ float red[32];
+    __shared__ __align__(16) float red[16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     pdl_trigger();
+    if (threadIdx.x < 16) red[threadIdx.x] = 0.f;
+    __syncthreads();
     pdl_wait();
     const long long row = blockIdx.x;
     float h[S][8];
@@ -55,7 +71,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_forward(const NormArgs 
         for (int j = 0; j < 8; ++j) sum += h[k][j] * h[k][j];
         if (a.h.p && c0 < a.cols) seg_store<BF16, VEC>(row_ptr<BF16>(a.h, row), c0, a.cols, lane, h[k]);
     }
-    const float rstd = 1.f / sqrtf(block_sum(sum, red) / (float)a.cols + a.eps);
+    const float rstd = 1.f / sqrtf(block_sum<false>(sum, red) / (float)a.cols + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     if (!a.y.p && !a.saved.codes) return;
 #pragma unroll
@@ -79,32 +95,105 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_forward(const NormArgs 
     }
 }
 
-// Blocks stride over the rows; each keeps its threads' columns of dweight in registers and
-// leaves one row of partial sums, which k_dweight adds up in block order.
+// One row's operands of a thread, as loaded.
 template <bool BF16, bool VEC, int S>
-__global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdArgs a) {
-    __shared__ float red[32];
+struct RowIn {
+    Raw<BF16, VEC> dy[S], dres[S];
+    union Xhat {
+        Raw<BF16, VEC> h;
+        Raw8<VEC> q;
+        __device__ Xhat() {}
+    } x[S];
+    __device__ __forceinline__ void load(const NormBwdArgs& a, const void* dyp, const void* hp, const uint8_t* codes,
+                                         const uint8_t* scales, const void* dresp, int warp, int warps, int lane) {
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+            const int c0 = (warp + k * warps) * kSeg;
+            dy[k].load(dyp, c0, a.cols, lane);
+            if (a.saved.codes)
+                x[k].q.load(codes, scales, c0, a.cols, lane);
+            else
+                x[k].h.load(hp, c0, a.cols, lane);
+            if (a.dres.p) dres[k].load(dresp, c0, a.cols, lane);
+        }
+    }
+};
+
+// Shared memory of the ring: rows as they lie in HBM, each part rounded up to 16 bytes.
+struct RingShape {
+    int dy, x, scales, dres, slot;   // bytes of one row's parts, and of a slot
+    int depth;                       // slots; 0: the rows are read directly
+};
+constexpr int kRingMost = 4;
+
+// The gradients.  Blocks stride over the rows; each keeps its threads' columns of dweight in
+// registers and leaves one row of partial sums, which k_dweight adds up in block order.
+// RING (16-byte aligned rows that fit): the next rows are on their way into shared memory by
+// bulk copies while one is reduced, so that HBM stays busy across the reduction's barrier
+// with registers for one row only.
+template <bool BF16, bool VEC, int S, bool RING>
+__global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdArgs a, const RingShape ring) {
+    extern __shared__ __align__(128) uint8_t slots[];
+    __shared__ __align__(16) float red[2][16];
+    __shared__ uint64_t full[kRingMost];
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     pdl_trigger();
+    if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.f;
+    if (RING && threadIdx.x == 0) {
+        for (int s = 0; s < ring.depth; ++s) mbar_init(full + s, 1);
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
     pdl_wait();
+    const long long first = blockIdx.x, stride = gridDim.x;
+    auto fetch = [&](long long row, int s) {   // one thread
+        uint8_t* to = slots + s * ring.slot;
+        mbar_arrive_expect_tx(full + s, ring.slot);
+        bulk_load(to, row_ptr<BF16>(a.dy, row), ring.dy, full + s);
+        if (a.saved.codes) {
+            bulk_load(to + ring.dy, a.saved.codes + row * a.saved.ldq, ring.x, full + s);
+            bulk_load(to + ring.dy + ring.x, a.saved.scales + row * a.saved.lds, ring.scales, full + s);
+        } else {
+            bulk_load(to + ring.dy, row_ptr<BF16>(a.h, row), ring.x, full + s);
+        }
+        if (a.dres.p) bulk_load(to + ring.dy + ring.x + ring.scales, row_ptr<BF16>(a.dres, row), ring.dres, full + s);
+    };
+    if (RING && threadIdx.x == 0)
+        for (int s = 0; s < ring.depth && first + s * stride < a.rows; ++s) fetch(first + s * stride, s);
+
     float dw[S][8];
 #pragma unroll
     for (int k = 0; k < S; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    int slot = 0, phase = 0, turn = 0;
+    for (long long row = first; row < a.rows; row += stride, turn ^= 1) {
+        RowIn<BF16, VEC, S> in;
         const float rstd = a.rstd[row];
+        if (RING) {
+            // a wait that runs out raises the flag and the status word; later waits then return at once
+            mbar_wait(full + slot, phase, abort_flag, a.status, kStatusTimeoutProducer);
+            const uint8_t* at = slots + slot * ring.slot;
+            in.load(a, at, at + ring.dy, at + ring.dy, at + ring.dy + ring.x, at + ring.dy + ring.x + ring.scales, warp,
+                    warps, lane);
+        } else {
+            in.load(a, row_ptr<BF16>(a.dy, row), row_ptr<BF16>(a.h, row), a.saved.codes + row * a.saved.ldq,
+                    a.saved.scales + row * a.saved.lds, row_ptr<BF16>(a.dres, row), warp, warps, lane);
+        }
         float n[S][8], d[S][8];
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < S; ++k) {
             const int c0 = (warp + k * warps) * kSeg;
             float w[8];
-            seg_load<BF16, VEC>(row_ptr<BF16>(a.dy, row), c0, a.cols, lane, d[k]);
+            in.dy[k].get(d[k]);
             if (a.saved.codes) {
-                seg_dequant<VEC>(a.saved, row, c0, a.cols, lane, n[k]);
+                in.x[k].q.get(a.saved.format, n[k]);
             } else {
-                seg_load<BF16, VEC>(row_ptr<BF16>(a.h, row), c0, a.cols, lane, n[k]);
+                in.x[k].h.get(n[k]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) n[k][j] *= rstd;
             }
@@ -116,15 +205,19 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
                 sum += d[k][j] * n[k][j];
             }
         }
+        const float mean = block_sum<true>(sum, red[turn]) / (float)a.cols;
+        if (RING) {   // every thread has read the slot: block_sum has a barrier
+            if (threadIdx.x == 0 && row + ring.depth * stride < a.rows) fetch(row + ring.depth * stride, slot);
+            if (++slot == ring.depth) slot = 0, phase ^= 1;
+        }
         if (!a.dx.p) continue;
-        const float mean = block_sum(sum, red) / (float)a.cols;
 #pragma unroll
         for (int k = 0; k < S; ++k) {
             const int c0 = (warp + k * warps) * kSeg;
             if (c0 >= a.cols) break;
             float r[8];
             if (a.dres.p) {
-                seg_load<BF16, VEC>(row_ptr<BF16>(a.dres, row), c0, a.cols, lane, r);
+                in.dres[k].get(r);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) r[j] = 0.f;
@@ -132,6 +225,11 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
 #pragma unroll
             for (int j = 0; j < 8; ++j) r[j] += rstd * (d[k][j] - n[k][j] * mean);
             seg_store<BF16, VEC>(row_ptr<BF16>(a.dx, row), c0, a.cols, lane, r);
+        }
+    }
+    if (RING && threadIdx.x == 0 && *abort_flag) {   // give copies still in flight time to land
+        const unsigned long long t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
         }
     }
     if (!a.partial) return;
@@ -147,32 +245,59 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
     }
 }
 
-// dweight (+)= sum of the blocks' partial rows, in block order.
-__global__ void __launch_bounds__(256) k_dweight(const float* partial, int blocks, int cols, float* dweight,
-                                                 int accumulate) {
-    __shared__ float part[8][32];
+// dweight (+)= sum of the blocks' partial rows: warp w of a block takes rows w, w + 32, ... of 32
+// columns, then the warps' sums are added in order.
+__global__ void __launch_bounds__(1024) k_dweight(const float* partial, int blocks, int cols, float* dweight,
+                                                  int accumulate) {
+    __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     pdl_trigger();
     pdl_wait();
     float s = 0.f;
-    if (c < cols)
-        for (int b = warp; b < blocks; b += 8) s += partial[(long long)b * cols + c];
+    if (c < cols) {
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += 32) s += partial[(long long)b * cols + c];
+    }
     part[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < cols) {
-        float t = 0.f;
+    s = part[lane][warp];   // warp w: column w of the 32
 #pragma unroll
-        for (int w = 0; w < 8; ++w) t += part[w][lane];
-        dweight[c] = accumulate ? dweight[c] + t : t;
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int col = blockIdx.x * 32 + warp;
+    if (lane == 0 && col < cols) dweight[col] = accumulate ? dweight[col] + s : s;
 }
 
-// Warps per block and segments per warp for rows of `cols` values.
-void norm_shape(int cols, int* warps, int* segs) {
+// Segments per warp (1, 2, 4 or 8, at least `least` where the row has two warps' worth) and
+// warps per block for rows of `cols` values.
+void norm_shape(int cols, int least, int* warps, int* segs) {
     const int n = (cols + kSeg - 1) / kSeg;   // <= 128
-    *segs = n <= 16 ? 1 : n <= 32 ? 2 : n <= 64 ? 4 : 8;
-    *warps = (n + *segs - 1) / *segs;
+    int s = n <= 16 ? 1 : n <= 32 ? 2 : n <= 64 ? 4 : 8;
+    if (n >= 2 * least && s < least) s = least;
+    *segs = s;
+    *warps = (n + s - 1) / s;
+}
+
+typedef void (*BackwardKernel)(NormBwdArgs, RingShape);
+template <int S>
+BackwardKernel pick_backward(bool bf16, bool vec, bool ring) {
+    if (!vec) return bf16 ? k_rmsnorm_backward<true, false, S, false> : k_rmsnorm_backward<false, false, S, false>;
+    if (!ring) return bf16 ? k_rmsnorm_backward<true, true, S, false> : k_rmsnorm_backward<false, true, S, false>;
+    return bf16 ? k_rmsnorm_backward<true, true, S, true> : k_rmsnorm_backward<false, true, S, true>;
+}
+BackwardKernel pick_backward(bool bf16, bool vec, int segs, bool ring) {
+    return segs == 1   ? pick_backward<1>(bf16, vec, ring)
+           : segs == 2 ? pick_backward<2>(bf16, vec, ring)
+           : segs == 4 ? pick_backward<4>(bf16, vec, ring)
+                       : pick_backward<8>(bf16, vec, ring);
+}
+cudaError_t for_each_ring_kernel() {
+    cudaError_t e = cudaSuccess;
+    for (int segs = 1; segs <= 8; segs *= 2)
+        for (int bf16 = 0; bf16 < 2 && e == cudaSuccess; ++bf16)
+            e = cudaFuncSetAttribute(pick_backward(bf16 != 0, true, segs, true), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kRingRoom);
+    return e;
 }
 
 }  // namespace
@@ -188,36 +313,43 @@ cudaError_t launch_rmsnorm_forward(const NormArgs& a, bool bf16, bool vec, cudaS
                               {k_rmsnorm_forward<false, false, 8>, k_rmsnorm_forward<false, true, 8>,
                                k_rmsnorm_forward<true, false, 8>, k_rmsnorm_forward<true, true, 8>}};
     int warps, segs;
-    norm_shape(a.cols, &warps, &segs);
+    norm_shape(a.cols, kFwdSegs, &warps, &segs);
     return launch_pdl(k[segs == 8 ? 3 : segs >> 1][(bf16 ? 2 : 0) + (vec ? 1 : 0)], dim3((unsigned)a.rows), dim3(32 * warps), 0, s, a);
 }
 
 int rmsnorm_backward_blocks(long long rows, int cols, int sm_count) {
     int warps, segs;
-    norm_shape(cols, &warps, &segs);
-    long long b = (long long)sm_count * (64 / warps);
+    norm_shape(cols, kBwdSegs, &warps, &segs);
+    long long b = (long long)sm_count * std::max(kBwdWarps / warps, 1);
     if (b > kNormPartialFloats / cols) b = kNormPartialFloats / cols;
     return (int)(b < rows ? b : rows);
 }
 
+cudaError_t rmsnorm_prepare() { return for_each_ring_kernel(); }
+
 cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a, bool bf16, bool vec, int sm_count, cudaStream_t s) {
-    typedef void (*K)(NormBwdArgs);
-    static const K k[4][4] = {{k_rmsnorm_backward<false, false, 1>, k_rmsnorm_backward<false, true, 1>,
-                               k_rmsnorm_backward<true, false, 1>, k_rmsnorm_backward<true, true, 1>},
-                              {k_rmsnorm_backward<false, false, 2>, k_rmsnorm_backward<false, true, 2>,
-                               k_rmsnorm_backward<true, false, 2>, k_rmsnorm_backward<true, true, 2>},
-                              {k_rmsnorm_backward<false, false, 4>, k_rmsnorm_backward<false, true, 4>,
-                               k_rmsnorm_backward<true, false, 4>, k_rmsnorm_backward<true, true, 4>},
-                              {k_rmsnorm_backward<false, false, 8>, k_rmsnorm_backward<false, true, 8>,
-                               k_rmsnorm_backward<true, false, 8>, k_rmsnorm_backward<true, true, 8>}};
     int warps, segs;
-    norm_shape(a.cols, &warps, &segs);
+    norm_shape(a.cols, kBwdSegs, &warps, &segs);
     const int blocks = rmsnorm_backward_blocks(a.rows, a.cols, sm_count);
     cudaError_t e = cudaSuccess;
-    if (blocks > 0)
-        e = launch_pdl(k[segs == 8 ? 3 : segs >> 1][(bf16 ? 2 : 0) + (vec ? 1 : 0)], dim3(blocks), dim3(32 * warps), 0, s, a);
+    if (blocks > 0) {
+        RingShape r{};
+        auto up16 = [](int n) { return (n + 15) / 16 * 16; };
+        const int esz = bf16 ? 2 : 4;
+        r.dy = up16(a.cols * esz);
+        r.x = a.saved.codes ? up16(a.cols) : r.dy;
+        r.scales = a.saved.codes ? up16((a.cols + kActGroup - 1) / kActGroup) : 0;
+        r.dres = a.dres.p ? r.dy : 0;
+        r.slot = r.dy + r.x + r.scales + r.dres;
+        // the blocks of an SM share its shared memory; a block that gets two rows or more uses the ring
+        const int room = kRingRoom / std::max(kBwdWarps / warps, 1) - 1024;
+        r.depth = vec ? std::min(room / r.slot, kRingMost) : 0;
+        if (r.depth < 2) r.depth = 0;
+        e = launch_pdl(pick_backward(bf16, vec, segs, r.depth > 0), dim3(blocks), dim3(32 * warps),
+                       (size_t)r.depth * r.slot, s, a, r);
+    }
     if (e == cudaSuccess && a.dweight)
-        e = launch_pdl(k_dweight, dim3((a.cols + 31) / 32), dim3(256), 0, s, (const float*)a.partial, blocks, a.cols,
+        e = launch_pdl(k_dweight, dim3((a.cols + 31) / 32), dim3(1024), 0, s, (const float*)a.partial, blocks, a.cols,
                        a.dweight, a.accumulate);
     return e;
 }

@@ -12,7 +12,7 @@
 //   0      TMA of x: per step of 64 tokens its 128 columns' codes (8 KB) and scales (1 KB)
 //   1      MMA issue (one thread of the even CTA) and TMEM allocation
 //   2      TMA of dy: its 128 columns (16 KB per step)
-//   3-10   conversion of x into a 16 KB bf16 operand per step
+//   3-10   conversion of x into a 16 KB bf16 operand per step, four steps at a time
 //   11-14  epilogue: column scale, addition to grad, stores
 // Two rings: x as it arrives (full_r by TMA, empty_r by the conversion), and the operands (dy
 // and converted x; ready, on the even CTA, by both CTAs' conversion warps and dy's TMA bytes,
@@ -28,17 +28,11 @@
 namespace muon {
 namespace {
 
-#ifndef W_NB
-#define W_NB 4
-#define W_NR 8
-#define W_CW 8
-#define W_CG 4
-#endif
 constexpr int kWgStepT = 64;            // tokens per step
-constexpr int kRingM = W_NB;            // steps of MMA operands
-constexpr int kRingR = W_NR;            // steps of x as it arrives
-constexpr int kConvWarps = W_CW;
-constexpr int kConvGroups = W_CG;       // steps in conversion at a time
+constexpr int kRingM = 4;               // steps of MMA operands
+constexpr int kRingR = 8;               // steps of x as it arrives
+constexpr int kConvWarps = 8;
+constexpr int kConvGroups = 4;          // steps in conversion at a time
 constexpr int kGroupWarps = kConvWarps / kConvGroups;
 constexpr int kRows = kWgStepT / kGroupWarps;   // token rows per conversion warp and step
 constexpr int kConvFirst = 3;           // first conversion warp
