@@ -172,6 +172,15 @@ __device__ __forceinline__ void store_four(char* p, const float* v) {
     else
         *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
+// Adds to fp32 in global memory, without an answer.
+__device__ __forceinline__ void red_four(void* p, const float* v) {
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3])
+                 : "memory");
+}
+__device__ __forceinline__ void red_one(void* p, float v) {
+    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+}
 // A lane's 32 sums of a block of a part, 32 rows of 256 floats: as OutTile holds them.
 template <bool WIDE>
 __device__ __forceinline__ void part_load(const float* p, float (&f)[32]) {
@@ -186,14 +195,22 @@ __device__ __forceinline__ void part_load(const float* p, float (&f)[32]) {
         }
 }
 template <bool WIDE>
-__device__ __forceinline__ void part_store(float* p, const float (&f)[32]) {
+__device__ __forceinline__ void part_store(float* p, const float (&f)[32], bool more) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (WIDE) {
-            *reinterpret_cast<float4*>(p + i * 1024) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+            if (more)
+                red_four(p + i * 1024, f + 4 * i);
+            else
+                store_four<false>(reinterpret_cast<char*>(p + i * 1024), f + 4 * i);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p[(4 * i + j) * 256] = f[4 * i + j];
+            for (int j = 0; j < 4; ++j) {
+                if (more)
+                    red_one(p + (4 * i + j) * 256, f[4 * i + j]);
+                else
+                    p[(4 * i + j) * 256] = f[4 * i + j];
+            }
         }
 }
 
@@ -220,12 +237,13 @@ struct OutTile {
     }
 
     // f: the sums of the block at column c0 of the tile; times the column scale, and added to what
-    // is there when the call accumulates or `more`.  Every load comes before the first store.
+    // is there when the call accumulates or `more`.  fp32 is added by reductions in L2: the only
+    // thread that writes an element issues them in program order, so the bits do not vary, and
+    // no value travels to the SM and back (16384 x 18944 x 3584: 1614 -> 1541 us).
     __device__ __forceinline__ void put(float (&f)[32], int c0, bool more) const {
         if (c0 >= cols) return;
         more = more || add;
         char* to = p + c0 * kSize;
-        const char* from = to;
         if (WIDE) {   // n % 4 == 0: the four columns exist together
             if (scale) {
                 const float s[4] = {scale[c0], scale[c0 + 1], scale[c0 + 2], scale[c0 + 3]};
@@ -233,12 +251,21 @@ struct OutTile {
                 for (int i = 0; i < 32; ++i) f[i] *= s[i & 3];
             }
             if (more) {
-                float4 g[8];
+                if (BF16) {   // every load before the first store
+                    float4 g[8];
+                    const char* from = to;
 #pragma unroll
-                for (int i = 0; i < 8; ++i, from += step)
-                    if (i < rows) g[i] = load_four<BF16>(from);
+                    for (int i = 0; i < 8; ++i, from += step)
+                        if (i < rows) g[i] = load_four<BF16>(from);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[4 * i] += g[i].x, f[4 * i + 1] += g[i].y, f[4 * i + 2] += g[i].z, f[4 * i + 3] += g[i].w;
+                    for (int i = 0; i < 8; ++i)
+                        f[4 * i] += g[i].x, f[4 * i + 1] += g[i].y, f[4 * i + 2] += g[i].z, f[4 * i + 3] += g[i].w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i, to += step)
+                        if (i < rows) red_four(to, f + 4 * i);
+                    return;
+                }
             }
             if (rows == 8) {
 #pragma unroll
@@ -251,15 +278,22 @@ struct OutTile {
             return;
         }
         const float s = scale ? scale[c0] : 1.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] *= s;
         if (more) {
-            float g[32];
+            if (BF16) {
+                float g[32];
+                const char* from = to;
 #pragma unroll
-            for (int i = 0; i < 32; ++i, from += step) g[i] = i < rows ? load_one<BF16>(from, 0) : 0.f;
+                for (int i = 0; i < 32; ++i, from += step) g[i] = i < rows ? load_one<BF16>(from, 0) : 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = fmaf(f[i], s, g[i]);
-        } else {
+                for (int i = 0; i < 32; ++i) f[i] += g[i];
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] *= s;
+                for (int i = 0; i < 32; ++i, to += step)
+                    if (i < rows) red_one(to, f[i]);
+                return;
+            }
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i, to += step)
@@ -386,14 +420,7 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
                 if (part == nullptr) {
                     out.put(f, c0, ch > 0);   // a later chain of tokens adds to what this warp wrote
                 } else {
-                    float* to = part + w.part * 8192 + c0;
-                    if (ch > 0) {
-                        float g[32];
-                        part_load<WIDE>(to, g);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) f[i] += g[i];
-                    }
-                    part_store<WIDE>(to, f);
+                    part_store<WIDE>(part + w.part * 8192 + c0, f, ch > 0);
                 }
             }
             tc_fence_before();
@@ -816,10 +843,12 @@ cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaS
         if (L.parts > 1) L.whole = (int)units - rest;
     }
     L.units = L.whole + ((int)units - L.whole) * L.parts;
-    // The tensor cores' adds truncate: the sum of one accumulator drifts by about 1.1e-5 of
-    // itself over 16384 tokens of random data, in proportion to their number.  An fp32 gradient
-    // keeps that below 6e-6 by adding up partial sums of 8192 tokens in the epilogue.
-    L.chain = bf16_grad ? 1 << 30 : 8192;
+    // The tensor cores' adds truncate: the sum in one accumulator drifts in proportion to the
+    // number of tokens, by 1.1e-5 of itself over 16384 tokens of random data.  An fp32 gradient
+    // adds up partial sums of 2048 tokens in the epilogue instead, which leaves 8.4e-7 (an fp32
+    // product on the CUDA cores: 6.9e-7) and costs 7 % (16384 x 18944 x 3584: 1437 -> 1541 us;
+    // 4096 tokens: 2e-6, 1470 us).  A bf16 gradient's own rounding, 1.7e-3, hides the drift.
+    L.chain = bf16_grad ? 1 << 30 : 2048;
     L.wide = a.n % 4 == 0 && (reinterpret_cast<uintptr_t>(a.grad) & (bf16_grad ? 7 : 15)) == 0;
     // TMA needs 16-byte aligned rows; x has them by its format
     const bool tma_y = ((reinterpret_cast<uintptr_t>(a.dy) | (uintptr_t)(a.lddy * 2)) & 15) == 0;
