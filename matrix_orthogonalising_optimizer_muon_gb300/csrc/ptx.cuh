@@ -275,6 +275,10 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_saddr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr) : "memory");
 }
+// The same without ordering memory (a hand-over of TMEM, whose reads are complete).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_saddr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr) : "memory");
+}
 // The same with release at CTA scope.
 __device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_saddr) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr) : "memory");

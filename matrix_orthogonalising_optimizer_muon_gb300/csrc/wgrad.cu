@@ -61,14 +61,33 @@ struct WgCfg {
 };
 static_assert(WgCfg::SMEM_BYTES <= 232448, "weight-gradient kernel exceeds the shared memory of one CTA");
 
+// Division of whole numbers below 2^31 by a divisor known at launch: with 2^(32 + s) / d rounded
+// up to the 33 bits 2^32 + m, n / d = (n + floor(n m / 2^32)) / 2^s (Granlund and Montgomery,
+// "Division by invariant integers using multiplication").  A tile's decoding is a chain of them.
+struct Divisor {
+    uint32_t d, m;
+    int s;
+    __host__ void set(uint32_t divisor) {
+        d = divisor;
+        s = 0;
+        while ((1ull << s) < d) ++s;
+        m = (uint32_t)(((((1ull << s) - d) << 32) / d) + 1);
+    }
+    __device__ __forceinline__ int div(int n) const {
+        return (int)(((unsigned long long)(uint32_t)n + __umulhi((uint32_t)n, m)) >> s);
+    }
+};
+
 struct WgradLaunch {
     CUtensorMap map_y, map_x, map_s;
     WgradArgs a;
     int tiles_m, tiles_n;
+    Divisor tiles, band, wide_band, last_band, part;   // by tiles of a weight, of a band, bands' widths, parts
     int units;                     // whole tiles of all groups, then parts of split tiles
     int whole, parts;              // units below `whole` are tiles, the others one of `parts` of a tile
-    int chain;                     // tokens one accumulator takes
+    int chain_log;                 // log2 of the tokens one accumulator takes
     int wide;                      // rows of grad are aligned to four elements
+    int sectors;                   // rows of a bf16 grad are aligned to 32 bytes
 };
 
 // Experts by decreasing number of tokens, built by every CTA when there are several (at most
@@ -85,30 +104,44 @@ struct Unit {
     int group, tile, part;  // part < 0: the whole tile
 };
 
+// The units of this CTA pair, one per turn.  Experts are dealt out by length: every other turn
+// runs backwards, so that no pair gets the longest of each.
+struct Turns {
+    int unit, base, pair, pairs;
+    bool back, snake;
+    __device__ __forceinline__ explicit Turns(const WgradLaunch& L)
+        : unit(blockIdx.x >> 1), base(0), pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), back(false), snake(L.a.offsets != nullptr) {}
+    __device__ __forceinline__ void next() {
+        base += pairs;
+        back = snake && !back;
+        unit = base + (back ? pairs - 1 - pair : pair);
+    }
+};
+
 __device__ __forceinline__ void expert_range(const WgradArgs& a, int g, long long* begin, long long* end) {
     *begin = min(max((long long)a.offsets[g], 0ll), a.tokens);
     *end = min(max((long long)a.offsets[g + 1], *begin), a.tokens);
 }
 
 __device__ __forceinline__ Unit decode_unit(const WgradLaunch& L, const Experts* ex, int u) {
-    const int per = L.tiles_m * L.tiles_n;
     Unit r;
     r.part = -1;
     if (u >= L.whole) {
-        const int v = u - L.whole;
-        u = L.whole + v / L.parts;
-        r.part = v % L.parts;
+        const int v = u - L.whole, t = L.part.div(v);
+        u = L.whole + t;
+        r.part = v - t * L.parts;
     }
     r.tile = u;
-    r.group = u / per;
-    int t = u - r.group * per;
+    r.group = L.tiles.div(u);
+    int t = u - r.group * (int)L.tiles.d;
     // bands of kBandM tiles along m, within a band along n: the tiles that run together share
     // both operands' columns in L2
-    const int band = t / (kBandM * L.tiles_n);
-    t -= band * kBandM * L.tiles_n;
-    const int wide = min(kBandM, L.tiles_m - band * kBandM);
-    r.m0 = (band * kBandM + t % wide) * 256;
-    r.n0 = t / wide * 256;
+    const int band = L.band.div(t);
+    t -= band * (int)L.band.d;
+    const bool full = (band + 1) * kBandM <= L.tiles_m;
+    const int col = full ? L.wide_band.div(t) : L.last_band.div(t);
+    r.m0 = (band * kBandM + t - col * (full ? kBandM : (int)L.last_band.d)) * 256;
+    r.n0 = col * 256;
     r.begin = 0, r.end = L.a.tokens;
     if (L.a.offsets) {
         if (L.a.groups <= kSortGroups) {
@@ -124,7 +157,7 @@ __device__ __forceinline__ Unit decode_unit(const WgradLaunch& L, const Experts*
     }
     return r;
 }
-__device__ __forceinline__ int unit_steps(const Unit& u) { return (int)((u.end - u.begin + kWgStepT - 1) / kWgStepT); }
+__device__ __forceinline__ int unit_steps(const Unit& u) { return (int)((uint32_t)(u.end - u.begin + kWgStepT - 1) / kWgStepT); }
 
 __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -361,8 +394,56 @@ struct EpilogueArgs {
     uint32_t tmem_base, tempty_lead, blk;   // blk: this warp's staging block in shared memory
     uint64_t* tfull;
     volatile int* abort_flag;
-    int first, stride, q, wq, lane;
+    int q, wq, lane;
 };
+
+// Hands accumulator `acc` back to the MMA warp once this warp's last load from it is complete.  The
+// arrival orders no memory: behind a release it would wait for the stores of grad.
+__device__ __forceinline__ void release_tmem(const EpilogueArgs& e, uint32_t acc) {
+    tc_fence_before();
+    __syncwarp();
+    if (e.lane == 0) mbar_arrive_remote_relaxed(e.tempty_lead + acc * 8);
+}
+
+// 32 aligned bytes: a whole sector from one lane.
+__device__ __forceinline__ void store_sector(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// A bf16 tile that is only written, whole, to rows of 32-byte aligned sectors: each lane stores its
+// TMEM lane's row, 32 columns at a time, without a detour through shared memory (32 experts of
+// 1024 x 2048: 83 -> 73 us; the same through shared memory and TMA stores 78 us).
+__device__ __forceinline__ void store_rows(const WgradLaunch& L, const Unit& w, const EpilogueArgs& e, uint32_t tbase,
+                                           uint32_t acc) {
+    const int row = w.m0 + 128 * e.q + 32 * e.wq + e.lane;
+    char* to = static_cast<char*>(L.a.grad) + (((long long)w.group * L.a.m + row) * L.a.n + w.n0) * 2;
+    const float* scale = L.a.col_scale ? L.a.col_scale + w.n0 : nullptr;
+    uint32_t v[2][32];
+    tmem_ld32(tbase, v[0]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        tmem_ld_wait();
+        if (c < 7)
+            tmem_ld32(tbase + 32 * (c + 1), v[(c + 1) & 1]);
+        else
+            release_tmem(e, acc);
+        uint32_t o[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {   // undoes the operand's column order
+            float f[4] = {__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 2]), __uint_as_float(v[c & 1][j + 1]),
+                          __uint_as_float(v[c & 1][j + 3])};
+            if (scale) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[k] *= scale[32 * c + j + k];
+            }
+            o[j / 2] = bf16_pair(f[0], f[1]), o[j / 2 + 1] = bf16_pair(f[2], f[3]);
+        }
+        store_sector(to + 64 * c, o);
+        store_sector(to + 64 * c + 32, o + 8);
+    }
+}
 
 // One epilogue warp: TMEM lane quarter wq, 32 rows of the tile, each 32 x 32 block through
 // shared memory into the layout of OutTile.
@@ -371,11 +452,12 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
     const int rl = e.lane >> 3, cl = 4 * (e.lane & 7);
     int local = 0;
     bool ok = true;
-    for (int u = e.first; ok && u < L.units; u += e.stride) {
-        const Unit w = decode_unit(L, e.ex, u);
-        const int chains = (int)((w.end - w.begin + L.chain - 1) / L.chain);
-        const OutTile<BF16, WIDE> out(L, w, w.m0 + 128 * e.q + 32 * e.wq, e.lane);
+    for (Turns u(L); ok && u.unit < L.units; u.next()) {
+        const Unit w = decode_unit(L, e.ex, u.unit);
+        const int chains = (int)((w.end - w.begin + (1ll << L.chain_log) - 1) >> L.chain_log);
+        const int r0 = w.m0 + 128 * e.q + 32 * e.wq;
         if (chains == 0) {   // an expert without tokens
+            const OutTile<BF16, WIDE> out(L, w, r0, e.lane);
             for (int c0 = 0; c0 < 256 && !L.a.accumulate; c0 += 32) {
                 float f[32] = {};
                 out.put(f, c0, false);
@@ -396,10 +478,18 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
             }
             tc_fence_after();
             const uint32_t tbase = e.tmem_base + acc * 256 + (static_cast<uint32_t>(e.wq * 32) << 16);
+            if (BF16 && WIDE && L.sectors && part == nullptr && !L.a.accumulate && w.n0 + 256 <= L.a.n &&
+                r0 + 32 <= L.a.m) {
+                store_rows(L, w, e, tbase, acc);
+                ++local;
+                continue;
+            }
+            const OutTile<BF16, WIDE> out(L, w, r0, e.lane);
             for (int c0 = 0; c0 < 256; c0 += 32) {
                 uint32_t v[32];
                 tmem_ld32(tbase + c0, v);
                 tmem_ld_wait();
+                if (c0 == 256 - 32) release_tmem(e, acc);
 #pragma unroll
                 for (int j = 0; j < 32; j += 4)   // undoes the operand's column order
                     sts128(e.blk + e.lane * WgCfg::OUT_LD + j * 4, make_uint4(v[j], v[j + 2], v[j + 1], v[j + 3]));
@@ -423,9 +513,6 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
                     part_store<WIDE>(part + w.part * 8192 + c0, f, ch > 0);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (e.lane == 0) mbar_arrive_remote_cta(e.tempty_lead + acc * 8);   // TMEM alone changes hands
             ++local;
         }
         if (part != nullptr && ok) {   // the warp that comes last adds up all parts, in their order
@@ -437,6 +524,7 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
             if (__shfl_sync(0xffffffffu, seen, 0) == L.parts - 1) {
                 if (e.lane == 0) *count = 0;   // for the next call
                 __threadfence();
+                const OutTile<BF16, WIDE> out(L, w, r0, e.lane);
                 for (int c0 = 0; c0 < 256; c0 += 32) {
                     float f[32];
                     part_load<WIDE>(part + c0, f);
@@ -473,8 +561,6 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t q = cluster_ctarank() & 1u;
     const bool leader = q == 0;
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRingR; ++s) {
             mbar_init(full_r + s, 1);
@@ -532,8 +618,8 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
             // ---------------- TMA of x
             uint32_t it = 0;
             bool ok = true;
-            for (int u = first; ok && u < L.units; u += stride) {
-                const Unit w = decode_unit(L, ex, u);
+            for (Turns u(L); ok && u.unit < L.units; u.next()) {
+                const Unit w = decode_unit(L, ex, u.unit);
                 const int steps = unit_steps(w);
                 const int xn = w.n0 + 128 * (int)q;
                 for (int k = 0; k < steps; ++k, ++it) {
@@ -564,8 +650,8 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
             // ---------------- TMA of dy, completion on the even CTA's barrier
             uint32_t slot = 0, ph = 1;
             bool ok = true;
-            for (int u = first; ok && u < L.units; u += stride) {
-                const Unit w = decode_unit(L, ex, u);
+            for (Turns u(L); ok && u.unit < L.units; u.next()) {
+                const Unit w = decode_unit(L, ex, u.unit);
                 const int steps = unit_steps(w);
                 const int ym = w.m0 + 128 * (int)q;
                 for (int k = 0; k < steps; ++k) {
@@ -613,9 +699,9 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
             constexpr uint32_t kSlot = Cfg::SLOT_BYTES >> 4, kStep = 16 * 128 >> 4;   // of the address field
             const uint64_t ad0 = sdesc_sw128(smem_u32(smem), Cfg::CHUNK_BYTES, 1024);
             const uint64_t bd0 = sdesc_sw128(smem_u32(smem) + Cfg::A_BYTES, Cfg::CHUNK_BYTES, 1024);
-            for (int u = first; ok && u < L.units; u += stride) {
-                const Unit w = decode_unit(L, ex, u);
-                const int steps = unit_steps(w), chain = L.chain / kWgStepT;
+            for (Turns u(L); ok && u.unit < L.units; u.next()) {
+                const Unit w = decode_unit(L, ex, u.unit);
+                const int steps = unit_steps(w), chain = 1 << (L.chain_log - 6);
                 const int last = ((int)(w.end - w.begin - 1) & (kWgStepT - 1)) / 16 + 1;   // MMAs of the last step
                 for (int k0 = 0; ok && k0 < steps; k0 += chain, ++local) {
                     const uint32_t acc = local & 1;
@@ -683,8 +769,8 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
         const uint32_t src0 = row0 * 128 + ((pc ^ prow) << 4);             // half 0; half 1: ^ 64
         const uint32_t dst0 = row0 * 128 + (((2 * pc) ^ prow) << 4);       // its second piece: ^ 16
         const uint32_t sel = 0x0404u + 0x1010u * (pc >> 1);                // its scale byte in bytes 1 and 3
-        for (int u = first; ok && u < L.units; u += stride) {
-            const Unit w = decode_unit(L, ex, u);
+        for (Turns u(L); ok && u.unit < L.units; u.next()) {
+            const Unit w = decode_unit(L, ex, u.unit);
             const int steps = unit_steps(w);
             const int off = ((w.n0 + 128 * (int)q) >> 5) & 15;   // the CTA's four of the 16 loaded scales
             for (int k = 0; k < steps; ++k, ++it) {
@@ -766,7 +852,7 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
         e.tempty_lead = mapa_shared(smem_u32(tempty), 0);
         e.blk = smem_u32(smem + Cfg::OUT_OFFSET + (warp - kEpiFirst) * Cfg::OUT_WARP);
         e.abort_flag = abort_flag;
-        e.first = first, e.stride = stride, e.q = (int)q, e.wq = warp & 3, e.lane = lane;
+        e.q = (int)q, e.wq = warp & 3, e.lane = lane;
         if (L.wide)
             epilogue<BF16, true>(L, e);
         else
@@ -843,13 +929,19 @@ cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaS
         if (L.parts > 1) L.whole = (int)units - rest;
     }
     L.units = L.whole + ((int)units - L.whole) * L.parts;
+    L.tiles.set(L.tiles_m * L.tiles_n);
+    L.band.set(kBandM * L.tiles_n);
+    L.wide_band.set(kBandM);
+    L.last_band.set(std::max(L.tiles_m % kBandM, 1));
+    L.part.set(L.parts);
     // The tensor cores' adds truncate: the sum in one accumulator drifts in proportion to the
     // number of tokens, by 1.1e-5 of itself over 16384 tokens of random data.  An fp32 gradient
     // adds up partial sums of 2048 tokens in the epilogue instead, which leaves 8.4e-7 (an fp32
     // product on the CUDA cores: 6.9e-7) and costs 7 % (16384 x 18944 x 3584: 1437 -> 1541 us;
     // 4096 tokens: 2e-6, 1470 us).  A bf16 gradient's own rounding, 1.7e-3, hides the drift.
-    L.chain = bf16_grad ? 1 << 30 : 2048;
+    L.chain_log = bf16_grad ? 30 : 11;
     L.wide = a.n % 4 == 0 && (reinterpret_cast<uintptr_t>(a.grad) & (bf16_grad ? 7 : 15)) == 0;
+    L.sectors = bf16_grad && a.n % 16 == 0 && (reinterpret_cast<uintptr_t>(a.grad) & 31) == 0;
     // TMA needs 16-byte aligned rows; x has them by its format
     const bool tma_y = ((reinterpret_cast<uintptr_t>(a.dy) | (uintptr_t)(a.lddy * 2)) & 15) == 0;
     if ((tma_y && !map_2d(&L.map_y, a.dy, false, a.m, a.tokens, a.lddy * 2, 64, true)) ||
