@@ -45,6 +45,19 @@ __device__ __forceinline__ float block_sum(float x, float* red) {
            (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
 }
 
+// 1 / sqrt(sum / cols + eps) to about half an ulp: the mean in two floats, then one Newton step with
+// its residual 1 - v y^2 in two floats.  The rounding of each step alone would move a few more
+// 8-bit codes across a rounding boundary.
+__device__ __forceinline__ float inverse_rms(float sum, float cols, float eps) {
+    const float inv = 1.f / cols, inv_lo = fmaf(-inv, cols, 1.f) * inv;   // 1 / cols
+    const float q = sum * inv, q_lo = fmaf(sum, inv, -q) + sum * inv_lo;
+    const float v = q + eps, b = v - q, v_lo = (q - (v - b)) + (eps - b) + q_lo;
+    const float y = rsqrtf(v);
+    const float h = y * y, h_lo = fmaf(y, y, -h);
+    const float res = fmaf(-v, h, 1.f) - fmaf(v, h_lo, v_lo * h);
+    return isfinite(res) ? fmaf(0.5f * y, res, y) : y;   // sum infinite or NaN
+}
+
 // S segments per warp.
 template <bool BF16, bool VEC, int S>
 __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_forward(const NormArgs a) {
@@ -71,7 +84,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_forward(const NormArgs 
         for (int j = 0; j < 8; ++j) sum += h[k][j] * h[k][j];
         if (a.h.p && c0 < a.cols) seg_store<BF16, VEC>(row_ptr<BF16>(a.h, row), c0, a.cols, lane, h[k]);
     }
-    const float rstd = 1.f / sqrtf(block_sum<false>(sum, red) / (float)a.cols + a.eps);
+    const float rstd = inverse_rms(block_sum<false>(sum, red), (float)a.cols, a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     if (!a.y.p && !a.saved.codes) return;
 #pragma unroll
