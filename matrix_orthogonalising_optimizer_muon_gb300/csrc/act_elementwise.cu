@@ -10,23 +10,30 @@ namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocks = 152 * 16;   // two full SMs' worth of warps on each SM
+// Blocks that fit an SM (by registers), and launched blocks: about four times as many, which evens
+// out the SMs' ends.  SwiGLU backward, 8192 x 18944 bf16: 306 us with six (40 registers), 329 with
+// four; forward 222 with four (64 registers), 233 with five.  Packing: 73 us with eight, 77 with six.
+constexpr int kFit = 8, kFitForward = 4, kFitBackward = 6;
+constexpr int kSms = 152;
 // Segments in flight per warp (SwiGLU forward, 8192 x 18944 bf16: 222 us; 250 with one, 277 with
-// four, whose registers leave too few warps).
-constexpr int kUnroll = 2;
+// four, whose registers leave too few warps); one where rows are loaded element by element.
+template <bool VEC>
+constexpr int kUnroll = VEC ? 2 : 1;
 
 // Units of this warp: row and first column of each, in steps of the launch's warps without a
 // division per step.
+template <bool VEC>
 struct Walk {
+    static constexpr int kWidth = kUnroll<VEC> * kSeg;
     long long row, drow;
     int col, dcol, width;
     __device__ __forceinline__ Walk(int cols) {
-        const int units = (cols + kUnroll * kSeg - 1) / (kUnroll * kSeg);
+        const int units = (cols + kWidth - 1) / kWidth;
         const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
         const long long n = (long long)gridDim.x * (kThreads / 32);
-        row = w / units, col = (int)(w - row * units) * (kUnroll * kSeg);
-        drow = n / units, dcol = (int)(n - drow * units) * (kUnroll * kSeg);
-        width = units * (kUnroll * kSeg);
+        row = w / units, col = (int)(w - row * units) * kWidth;
+        drow = n / units, dcol = (int)(n - drow * units) * kWidth;
+        width = units * kWidth;
     }
     __device__ __forceinline__ void next() {
         row += drow, col += dcol;
@@ -40,17 +47,17 @@ __device__ __forceinline__ void* row_ptr(const Mat& m, long long row) {
 }
 
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_act_pack(const PackArgs a) {
+__global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_pack(const PackArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    for (Walk w(a.cols); w.row < a.rows; w.next()) {
+    for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
         const void* x = row_ptr<BF16>(a.x, w.row);
-        Raw<BF16, VEC> raw[kUnroll];
+        Raw<BF16, VEC> raw[kUnroll<VEC>];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) raw[k].load(x, w.col + k * kSeg, a.cols, lane);
+        for (int k = 0; k < kUnroll<VEC>; ++k) raw[k].load(x, w.col + k * kSeg, a.cols, lane);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
+        for (int k = 0; k < kUnroll<VEC>; ++k) {
             float v[8];
             raw[k].get(v);
             seg_quant<VEC>(a.q, w.row, w.col + k * kSeg, a.cols, lane, v);
@@ -59,17 +66,17 @@ __global__ void __launch_bounds__(kThreads) k_act_pack(const PackArgs a) {
 }
 
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_act_unpack(const PackArgs a) {
+__global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_unpack(const PackArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    for (Walk w(a.cols); w.row < a.rows; w.next()) {
+    for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
         void* y = row_ptr<BF16>(a.x, w.row);
-        Raw8<VEC> raw[kUnroll];
+        Raw8<VEC> raw[kUnroll<VEC>];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) raw[k].load(a.q, w.row, w.col + k * kSeg, a.cols, lane);
+        for (int k = 0; k < kUnroll<VEC>; ++k) raw[k].load(a.q, w.row, w.col + k * kSeg, a.cols, lane);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
+        for (int k = 0; k < kUnroll<VEC>; ++k) {
             float v[8];
             raw[k].get(a.q.format, v);
             seg_store<BF16, VEC>(y, w.col + k * kSeg, a.cols, lane, v);
@@ -81,20 +88,20 @@ __global__ void __launch_bounds__(kThreads) k_act_unpack(const PackArgs a) {
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
 
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_swiglu_forward(const SwigluArgs a) {
+__global__ void __launch_bounds__(kThreads, kFitForward) k_swiglu_forward(const SwigluArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    for (Walk w(a.cols); w.row < a.rows; w.next()) {
+    for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
         const void *gate = row_ptr<BF16>(a.gate, w.row), *up = row_ptr<BF16>(a.up, w.row);
-        Raw<BF16, VEC> gr[kUnroll], ur[kUnroll];
+        Raw<BF16, VEC> gr[kUnroll<VEC>], ur[kUnroll<VEC>];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
+        for (int k = 0; k < kUnroll<VEC>; ++k) {
             gr[k].load(gate, w.col + k * kSeg, a.cols, lane);
             ur[k].load(up, w.col + k * kSeg, a.cols, lane);
         }
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
+        for (int k = 0; k < kUnroll<VEC>; ++k) {
             const int c0 = w.col + k * kSeg;
             float g[8], u[8], o[8];
             gr[k].get(g);
@@ -110,22 +117,22 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_forward(const SwigluArgs a)
 }
 
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_swiglu_backward(const SwigluArgs a) {
+__global__ void __launch_bounds__(kThreads, BF16 && VEC ? kFitBackward : 4) k_swiglu_backward(const SwigluArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    for (Walk w(a.cols); w.row < a.rows; w.next()) {
+    for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
         const void* da = row_ptr<BF16>(a.a, w.row);
-        Raw<BF16, VEC> dr[kUnroll];
-        Raw8<VEC> gr[kUnroll], ur[kUnroll];
+        Raw<BF16, VEC> dr[kUnroll<VEC>];
+        Raw8<VEC> gr[kUnroll<VEC>], ur[kUnroll<VEC>];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
+        for (int k = 0; k < kUnroll<VEC>; ++k) {
             dr[k].load(da, w.col + k * kSeg, a.cols, lane);
             gr[k].load(a.gate8, w.row, w.col + k * kSeg, a.cols, lane);
             ur[k].load(a.up8, w.row, w.col + k * kSeg, a.cols, lane);
         }
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
+        for (int k = 0; k < kUnroll<VEC>; ++k) {
             const int c0 = w.col + k * kSeg;
             float g[8], u[8], d[8], o[8];
             dr[k].get(d);
@@ -146,16 +153,17 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_backward(const SwigluArgs a
     }
 }
 
-// Blocks for all units, at most kBlocks (the kernels stride over what is left).
-unsigned blocks_for(long long rows, int cols) {
-    const long long units = rows * ((cols + kUnroll * kSeg - 1) / (kUnroll * kSeg));
+// Blocks for all units, at most four times what fits (the kernels stride over what is left).
+unsigned blocks_for(long long rows, int cols, int fit, bool vec) {
+    const int width = vec ? Walk<true>::kWidth : Walk<false>::kWidth;
+    const long long units = rows * ((cols + width - 1) / width);
     const long long b = (units + kThreads / 32 - 1) / (kThreads / 32);
-    return (unsigned)(b < kBlocks ? b : kBlocks);
+    return (unsigned)(b < 4 * fit * kSms ? b : 4 * fit * kSms);
 }
 
 template <typename Args>
-cudaError_t launch(void (*const (&k)[4])(Args), const Args& a, bool bf16, bool vec, cudaStream_t s) {
-    return launch_pdl(k[(bf16 ? 2 : 0) + (vec ? 1 : 0)], dim3(blocks_for(a.rows, a.cols)), dim3(kThreads), 0,
+cudaError_t launch(void (*const (&k)[4])(Args), const Args& a, int fit, bool bf16, bool vec, cudaStream_t s) {
+    return launch_pdl(k[(bf16 ? 2 : 0) + (vec ? 1 : 0)], dim3(blocks_for(a.rows, a.cols, fit, vec)), dim3(kThreads), 0,
                       s, a);
 }
 
@@ -164,22 +172,22 @@ cudaError_t launch(void (*const (&k)[4])(Args), const Args& a, bool bf16, bool v
 cudaError_t launch_act_pack(const PackArgs& a, bool bf16, bool vec, cudaStream_t s) {
     static void (*const k[4])(PackArgs) = {k_act_pack<false, false>, k_act_pack<false, true>, k_act_pack<true, false>,
                                            k_act_pack<true, true>};
-    return launch(k, a, bf16, vec, s);
+    return launch(k, a, kFit, bf16, vec, s);
 }
 cudaError_t launch_act_unpack(const PackArgs& a, bool bf16, bool vec, cudaStream_t s) {
     static void (*const k[4])(PackArgs) = {k_act_unpack<false, false>, k_act_unpack<false, true>,
                                            k_act_unpack<true, false>, k_act_unpack<true, true>};
-    return launch(k, a, bf16, vec, s);
+    return launch(k, a, kFit, bf16, vec, s);
 }
 cudaError_t launch_swiglu_forward(const SwigluArgs& a, bool bf16, bool vec, cudaStream_t s) {
     static void (*const k[4])(SwigluArgs) = {k_swiglu_forward<false, false>, k_swiglu_forward<false, true>,
                                              k_swiglu_forward<true, false>, k_swiglu_forward<true, true>};
-    return launch(k, a, bf16, vec, s);
+    return launch(k, a, kFitForward, bf16, vec, s);
 }
 cudaError_t launch_swiglu_backward(const SwigluArgs& a, bool bf16, bool vec, cudaStream_t s) {
     static void (*const k[4])(SwigluArgs) = {k_swiglu_backward<false, false>, k_swiglu_backward<false, true>,
                                              k_swiglu_backward<true, false>, k_swiglu_backward<true, true>};
-    return launch(k, a, bf16, vec, s);
+    return launch(k, a, kFitBackward, bf16, vec, s);
 }
 
 }  // namespace muon
