@@ -132,16 +132,17 @@ struct RowIn {
     }
 };
 
-// Shared memory of the ring: rows as they lie in HBM, each part rounded up to 16 bytes.
+// Shared memory of the ring: rows as they lie in HBM, in whole 16-byte pieces.  A row that is not
+// aligned keeps its offset within its first piece; every piece copied holds some of the row.
 struct RingShape {
-    int dy, x, scales, dres, slot;   // bytes of one row's parts, and of a slot
+    int dy, x, scales, dres, slot;   // room of one row's parts, and of a slot
     int depth;                       // slots; 0: the rows are read directly
 };
 constexpr int kRingMost = 4;
 
 // The gradients.  Blocks stride over the rows; each keeps its threads' columns of dweight in
 // registers and leaves one row of partial sums, which k_dweight adds up in block order.
-// RING (16-byte aligned rows that fit): the next rows are on their way into shared memory by
+// RING (rows that fit): the next rows are on their way into shared memory by
 // bulk copies while one is reduced, so that HBM stays busy across the reduction's barrier
 // with registers for one row only.
 template <bool BF16, bool VEC, int S, bool RING>
@@ -162,17 +163,23 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
     __syncthreads();
     pdl_wait();
     const long long first = blockIdx.x, stride = gridDim.x;
+    constexpr int kSize = BF16 ? 2 : 4;
+    auto offset = [](const void* p) { return VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15); };
+    auto pieces = [&](const void* p) { return (offset(p) + a.cols * kSize + 15) & ~15; };
     auto fetch = [&](long long row, int s) {   // one thread
         uint8_t* to = slots + s * ring.slot;
-        mbar_arrive_expect_tx(full + s, ring.slot);
-        bulk_load(to, row_ptr<BF16>(a.dy, row), ring.dy, full + s);
+        const char *y = static_cast<const char*>(row_ptr<BF16>(a.dy, row)), *h = static_cast<const char*>(row_ptr<BF16>(a.h, row)),
+                   *r = static_cast<const char*>(row_ptr<BF16>(a.dres, row));
+        const int ny = pieces(y), nx = a.saved.codes ? ring.x : pieces(h), nr = a.dres.p ? pieces(r) : 0;
+        mbar_arrive_expect_tx(full + s, ny + nx + ring.scales + nr);
+        bulk_load(to, y - offset(y), ny, full + s);
         if (a.saved.codes) {
-            bulk_load(to + ring.dy, a.saved.codes + row * a.saved.ldq, ring.x, full + s);
+            bulk_load(to + ring.dy, a.saved.codes + row * a.saved.ldq, nx, full + s);
             bulk_load(to + ring.dy + ring.x, a.saved.scales + row * a.saved.lds, ring.scales, full + s);
         } else {
-            bulk_load(to + ring.dy, row_ptr<BF16>(a.h, row), ring.x, full + s);
+            bulk_load(to + ring.dy, h - offset(h), nx, full + s);
         }
-        if (a.dres.p) bulk_load(to + ring.dy + ring.x + ring.scales, row_ptr<BF16>(a.dres, row), ring.dres, full + s);
+        if (nr) bulk_load(to + ring.dy + ring.x + ring.scales, r - offset(r), nr, full + s);
     };
     if (RING && threadIdx.x == 0)
         for (int s = 0; s < ring.depth && first + s * stride < a.rows; ++s) fetch(first + s * stride, s);
@@ -190,8 +197,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
             // a wait that runs out raises the flag and the status word; later waits then return at once
             mbar_wait(full + slot, phase, abort_flag, a.status, kStatusTimeoutProducer);
             const uint8_t* at = slots + slot * ring.slot;
-            in.load(a, at, at + ring.dy, at + ring.dy, at + ring.dy + ring.x, at + ring.dy + ring.x + ring.scales, warp,
-                    warps, lane);
+            const uint8_t *x = at + ring.dy, *r = x + ring.x + ring.scales;
+            in.load(a, at + offset(row_ptr<BF16>(a.dy, row)), x + offset(row_ptr<BF16>(a.h, row)), x, x + ring.x,
+                    r + offset(row_ptr<BF16>(a.dres, row)), warp, warps, lane);
         } else {
             in.load(a, row_ptr<BF16>(a.dy, row), row_ptr<BF16>(a.h, row), a.saved.codes + row * a.saved.ldq,
                     a.saved.scales + row * a.saved.lds, row_ptr<BF16>(a.dres, row), warp, warps, lane);
@@ -294,7 +302,10 @@ void norm_shape(int cols, int least, int* warps, int* segs) {
 typedef void (*BackwardKernel)(NormBwdArgs, RingShape);
 template <int S>
 BackwardKernel pick_backward(bool bf16, bool vec, bool ring) {
-    if (!vec) return bf16 ? k_rmsnorm_backward<true, false, S, false> : k_rmsnorm_backward<false, false, S, false>;
+    if (!vec) {
+        if (!ring) return bf16 ? k_rmsnorm_backward<true, false, S, false> : k_rmsnorm_backward<false, false, S, false>;
+        return bf16 ? k_rmsnorm_backward<true, false, S, true> : k_rmsnorm_backward<false, false, S, true>;
+    }
     if (!ring) return bf16 ? k_rmsnorm_backward<true, true, S, false> : k_rmsnorm_backward<false, true, S, false>;
     return bf16 ? k_rmsnorm_backward<true, true, S, true> : k_rmsnorm_backward<false, true, S, true>;
 }
@@ -307,8 +318,8 @@ BackwardKernel pick_backward(bool bf16, bool vec, int segs, bool ring) {
 cudaError_t for_each_ring_kernel() {
     cudaError_t e = cudaSuccess;
     for (int segs = 1; segs <= 8; segs *= 2)
-        for (int bf16 = 0; bf16 < 2 && e == cudaSuccess; ++bf16)
-            e = cudaFuncSetAttribute(pick_backward(bf16 != 0, true, segs, true), cudaFuncAttributeMaxDynamicSharedMemorySize,
+        for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+            e = cudaFuncSetAttribute(pick_backward(i & 1, i >> 1, segs, true), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kRingRoom);
     return e;
 }
@@ -349,14 +360,14 @@ cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a, bool bf16, bool vec, i
         RingShape r{};
         auto up16 = [](int n) { return (n + 15) / 16 * 16; };
         const int esz = bf16 ? 2 : 4;
-        r.dy = up16(a.cols * esz);
+        r.dy = up16(a.cols * esz) + (vec ? 0 : 16);
         r.x = a.saved.codes ? up16(a.cols) : r.dy;
         r.scales = a.saved.codes ? up16((a.cols + kActGroup - 1) / kActGroup) : 0;
         r.dres = a.dres.p ? r.dy : 0;
         r.slot = r.dy + r.x + r.scales + r.dres;
         // the blocks of an SM share its shared memory; a block that gets two rows or more uses the ring
         const int room = kRingRoom / std::max(kBwdWarps / warps, 1) - 1024;
-        r.depth = vec ? std::min(room / r.slot, kRingMost) : 0;
+        r.depth = std::min(room / r.slot, kRingMost);
         if (r.depth < 2) r.depth = 0;
         e = launch_pdl(pick_backward(bf16, vec, segs, r.depth > 0), dim3(blocks), dim3(32 * warps),
                        (size_t)r.depth * r.slot, s, a, r);
