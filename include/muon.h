@@ -460,7 +460,7 @@ muon_status muon_stage_times(muon_plan p, float* ms, double* flops, int32_t n_st
  * the step reads, from activations held in 8 bits between the forward and the
  * backward pass.  The conventions above hold, except that each call takes its
  * tensors themselves (one matrix per argument, a pointer and a row pitch `ld`
- * in elements, ld >= cols; rows need no alignment, aligned rows are faster)
+ * in elements, ld >= cols, below 2^32 bytes; rows need no alignment, 16-byte aligned rows are faster)
  * and that nothing but muon_wgrad and muon_rmsnorm_backward needs a plan.
  * Values of a NULL optional argument are not computed.  Outputs must not
  * overlap inputs or one another unless a call says so; tensors that interleave
@@ -476,10 +476,11 @@ typedef enum { MUON_ACT_E4M3 = 0, MUON_ACT_INT8 = 1 } muon_act_format;
  *           mantissa bits, largest 448), or two's-complement whole numbers -127 .. 127.
  *   scales  row-major bytes, row pitch lds: byte g of a row belongs to columns
  *           32 g .. 32 g + 31 and stands for 2^(byte - 127); 255 marks a group that
- *           held an infinity or a NaN and reads back as NaN.
+ *           held an infinity or a NaN: its codes are 0 and it reads back as NaN.
  * value = code * 2^(byte - 127).  Both pointers and both pitches are multiples of 16,
  * ldq >= cols, lds >= ceil(cols / 32); bytes that pad a row may be overwritten and are
- * never used.  Every writer picks the smallest 2^e that brings the group's largest
+ * never used.  The e4m3 codes 0x7f and 0xff (NaN), the whole number -128 and scale bytes outside 17 .. 248
+ * and 255 are never written; what a reader makes of them is unspecified.  Every writer picks the smallest 2^e that brings the group's largest
  * magnitude within the codes' range (448 or 127), with -110 <= e <= 119 (e4m3) or
  * 121 (int8), and rounds value / 2^e to the nearest code, ties to even, saturating at
  * the largest.  Within that range of e every value is exact in bf16 (at most 8

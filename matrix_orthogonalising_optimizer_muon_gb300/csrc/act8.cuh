@@ -27,6 +27,9 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&h);
 }
+__device__ __forceinline__ char* row_ptr(const Mat& m, uint32_t row) {
+    return static_cast<char*>(m.p) + (uint64_t)row * m.pitch;
+}
 template <bool BF16>
 __device__ __forceinline__ float load_one(const void* p, long long i) {
     return BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
@@ -165,10 +168,10 @@ __device__ __forceinline__ void act_number4(uint32_t w, float* v) {
 // Writes the segment in 8 bits at row `row`.  Values beyond `cols` must be zero; lanes of
 // a partly filled last group take part with those zeros.
 template <int FMT, bool VEC>
-__device__ __forceinline__ void seg_quant(const Act8& q, long long row, int c0, int cols, int lane,
+__device__ __forceinline__ void seg_quant(const Act8& q, uint32_t row, int c0, int cols, int lane,
                                           const float (&v)[8]) {
-    uint8_t* codes = q.codes + row * q.ldq + c0;
-    uint8_t* scales = q.scales + row * q.lds + (c0 >> 5);
+    uint8_t* codes = q.codes + (uint64_t)row * q.ldq + c0;
+    uint8_t* scales = q.scales + (uint64_t)row * q.lds + (c0 >> 5);
     uint32_t m[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) m[j] = __float_as_uint(v[j]) & 0x7fffffffu;
@@ -200,7 +203,7 @@ __device__ __forceinline__ void seg_quant(const Act8& q, long long row, int c0, 
 }
 // The same, the format chosen at run time (uniform over the launch).
 template <bool VEC>
-__device__ __forceinline__ void seg_quant(const Act8& q, long long row, int c0, int cols, int lane,
+__device__ __forceinline__ void seg_quant(const Act8& q, uint32_t row, int c0, int cols, int lane,
                                           const float (&v)[8]) {
     if (q.format == kE4M3)
         seg_quant<kE4M3, VEC>(q, row, c0, cols, lane, v);
@@ -215,8 +218,8 @@ struct Raw8 {
     uint32_t r[VEC ? 3 : 8];
 
     // The segment of row `row`; reads as zero at and beyond `cols`.
-    __device__ __forceinline__ void load(const Act8& q, long long row, int c0, int cols, int lane) {
-        load(q.codes + row * q.ldq, q.scales + row * q.lds, c0, cols, lane);
+    __device__ __forceinline__ void load(const Act8& q, uint32_t row, int c0, int cols, int lane) {
+        load(q.codes + (uint64_t)row * q.ldq, q.scales + (uint64_t)row * q.lds, c0, cols, lane);
     }
     __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int c0, int cols, int lane) {
         codes += c0, scales += c0 >> 5;

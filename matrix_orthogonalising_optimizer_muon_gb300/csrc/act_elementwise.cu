@@ -10,13 +10,14 @@ namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
-// Blocks that fit an SM (by registers), and launched blocks: about four times as many, which evens
-// out the SMs' ends.  SwiGLU backward, 8192 x 18944 bf16: 306 us with six (40 registers), 329 with
-// four; forward 222 with four (64 registers), 233 with five.  Packing: 73 us with eight, 77 with six.
-constexpr int kFit = 8, kFitForward = 4, kFitBackward = 6;
+// Blocks that fit an SM (by registers); about four times as many are launched, which evens out the
+// SMs' ends.  8192 x 18944 bf16: SwiGLU forward 207 us with five (48 registers; 209 with four),
+// backward 278 us with five (287 with six, 296 with four).  Packing: 71 us with eight, 77 with six.
+constexpr int kFit = 8, kFitForward = 5, kFitBackward = 5;
 constexpr int kSms = 152;
-// Segments in flight per warp (SwiGLU forward, 8192 x 18944 bf16: 222 us; 250 with one, 277 with
-// four, whose registers leave too few warps); one where rows are loaded element by element.
+// Segments in flight per warp: with one the loads do not cover HBM's latency (an earlier forward kernel
+// took 250 us, 222 with two), with four the registers leave too few warps (277); one where rows are
+// loaded element by element.
 template <bool VEC>
 constexpr int kUnroll = VEC ? 2 : 1;
 
@@ -25,12 +26,12 @@ constexpr int kUnroll = VEC ? 2 : 1;
 template <bool VEC>
 struct Walk {
     static constexpr int kWidth = kUnroll<VEC> * kSeg;
-    long long row, drow;
+    uint32_t row, drow;   // below 2^31 each
     int col, dcol, width;
     __device__ __forceinline__ Walk(int cols) {
         const int units = (cols + kWidth - 1) / kWidth;
-        const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-        const long long n = (long long)gridDim.x * (kThreads / 32);
+        const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+        const uint32_t n = gridDim.x * (kThreads / 32);
         row = w / units, col = (int)(w - row * units) * kWidth;
         drow = n / units, dcol = (int)(n - drow * units) * kWidth;
         width = units * kWidth;
@@ -41,18 +42,13 @@ struct Walk {
     }
 };
 
-template <bool BF16>
-__device__ __forceinline__ void* row_ptr(const Mat& m, long long row) {
-    return static_cast<char*>(m.p) + row * m.ld * (BF16 ? 2 : 4);
-}
-
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_pack(const PackArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
     for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        const void* x = row_ptr<BF16>(a.x, w.row);
+        const void* x = row_ptr(a.x, w.row);
         Raw<BF16, VEC> raw[kUnroll<VEC>];
 #pragma unroll
         for (int k = 0; k < kUnroll<VEC>; ++k) raw[k].load(x, w.col + k * kSeg, a.cols, lane);
@@ -71,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_unpack(const P
     pdl_trigger();
     pdl_wait();
     for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        void* y = row_ptr<BF16>(a.x, w.row);
+        void* y = row_ptr(a.x, w.row);
         Raw8<VEC> raw[kUnroll<VEC>];
 #pragma unroll
         for (int k = 0; k < kUnroll<VEC>; ++k) raw[k].load(a.q, w.row, w.col + k * kSeg, a.cols, lane);
@@ -84,8 +80,19 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_unpack(const P
     }
 }
 
-// 1 / (1 + e^-z); the quotient by the approximate reciprocal (1 ulp; 0 where e^-z overflows).
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + expf(-z)); }
+// 1 / (1 + e^-z).  e^-z = 2^t 2^d with t = -z log2 e rounded and d, what the rounding left, by the
+// first term of its series: a relative error of about 3 ulp in the exponential and 1 in the
+// reciprocal (expf and a division: 217 us forward, 304 backward).  Zero below -87.3, where it leaves
+// the normal range (so that -infinity times it is a NaN, as in z / (1 + e^-z)).
+__device__ __forceinline__ float sigmoid(float z) {
+    const float c = fminf(z, 80.f);
+    const float t = c * -1.44269504f, d = fmaf(c, -1.44269504f, -t);
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = fmaf(e, d * 0.693147181f, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return z < -87.3f ? 0.f : r;
+}
 
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads, kFitForward) k_swiglu_forward(const SwigluArgs a) {
@@ -93,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, kFitForward) k_swiglu_forward(const 
     pdl_trigger();
     pdl_wait();
     for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        const void *gate = row_ptr<BF16>(a.gate, w.row), *up = row_ptr<BF16>(a.up, w.row);
+        const void *gate = row_ptr(a.gate, w.row), *up = row_ptr(a.up, w.row);
         Raw<BF16, VEC> gr[kUnroll<VEC>], ur[kUnroll<VEC>];
 #pragma unroll
         for (int k = 0; k < kUnroll<VEC>; ++k) {
@@ -108,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, kFitForward) k_swiglu_forward(const 
             ur[k].get(u);
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid(g[j]) * u[j];
-            if (a.a.p) seg_store<BF16, VEC>(row_ptr<BF16>(a.a, w.row), c0, a.cols, lane, o);
+            if (a.a.p) seg_store<BF16, VEC>(row_ptr(a.a, w.row), c0, a.cols, lane, o);
             if (a.gate8.codes) seg_quant<VEC>(a.gate8, w.row, c0, a.cols, lane, g);
             if (a.up8.codes) seg_quant<VEC>(a.up8, w.row, c0, a.cols, lane, u);
             if (a.a8.codes) seg_quant<VEC>(a.a8, w.row, c0, a.cols, lane, o);
@@ -122,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && VEC ? kFitBackward : 4) k_sw
     pdl_trigger();
     pdl_wait();
     for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        const void* da = row_ptr<BF16>(a.a, w.row);
+        const void* da = row_ptr(a.a, w.row);
         Raw<BF16, VEC> dr[kUnroll<VEC>];
         Raw8<VEC> gr[kUnroll<VEC>], ur[kUnroll<VEC>];
 #pragma unroll
@@ -146,8 +153,8 @@ __global__ void __launch_bounds__(kThreads, BF16 && VEC ? kFitBackward : 4) k_sw
                 g[j] = d[j] * u[j] * (s + silu * (1.f - s));   // dgate
                 u[j] = d[j] * silu;                            // dup
             }
-            seg_store<BF16, VEC>(row_ptr<BF16>(a.gate, w.row), c0, a.cols, lane, g);
-            seg_store<BF16, VEC>(row_ptr<BF16>(a.up, w.row), c0, a.cols, lane, u);
+            seg_store<BF16, VEC>(row_ptr(a.gate, w.row), c0, a.cols, lane, g);
+            seg_store<BF16, VEC>(row_ptr(a.up, w.row), c0, a.cols, lane, u);
             if (a.a8.codes) seg_quant<VEC>(a.a8, w.row, c0, a.cols, lane, o);
         }
     }

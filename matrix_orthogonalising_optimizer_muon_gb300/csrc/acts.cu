@@ -19,6 +19,8 @@ constexpr size_t kWsHeader = 256 + kMaxParts * 4 * sizeof(int);   // status word
 constexpr int64_t kGradWorkspace = (int64_t)kWsHeader + kPartialFloats * 4;
 static_assert(kWsHeader % 256 == 0, "the partial sums are aligned");
 
+constexpr int64_t kMostPitch = 1ll << 32;   // bytes from row to row
+
 // A strided range of device memory: `rows` rows of `width` bytes, `pitch` bytes apart.
 struct Range {
     uintptr_t p;
@@ -78,12 +80,13 @@ struct Call {
 
     int mat(Mat* m, const void* p, int64_t ld, bool output, bool optional, int may_alias = 0) {
         m->p = const_cast<void*>(p);
-        m->ld = ld;
+        m->pitch = 0;
         if (!p) {
             ok = ok && optional;
             return ops.add(nullptr, 0, 0, 0, output);
         }
-        ok = ok && ld >= cols && ld <= (1ll << 40) && (reinterpret_cast<uintptr_t>(p) & (esz - 1)) == 0;
+        ok = ok && ld >= cols && ld < kMostPitch / esz && (reinterpret_cast<uintptr_t>(p) & (esz - 1)) == 0;
+        m->pitch = ok ? (uint32_t)(ld * esz) : 0;
         vec = vec && aligned16(p, ld * esz);
         return ops.add(p, rows, cols * esz, ld * esz, output, may_alias);
     }
@@ -99,10 +102,11 @@ struct Call {
         }
         ok = ok && ((a->codes && a->scales) || rows == 0) && (a->format == MUON_ACT_E4M3 || a->format == MUON_ACT_INT8) &&
              a->reserved == 0 && a->ldq >= cols && a->lds >= (cols + kActGroup - 1) / kActGroup &&
-             a->ldq <= (1ll << 40) && a->lds <= (1ll << 40) && aligned16(a->codes, a->ldq) &&
+             a->ldq < kMostPitch && a->lds < kMostPitch && aligned16(a->codes, a->ldq) &&
              aligned16(a->scales, a->lds);
         if (!ok) return;
-        *q = Act8{static_cast<uint8_t*>(a->codes), static_cast<uint8_t*>(a->scales), a->ldq, a->lds, a->format};
+        *q = Act8{static_cast<uint8_t*>(a->codes), static_cast<uint8_t*>(a->scales), (uint32_t)a->ldq, (uint32_t)a->lds,
+                  a->format};
         // the padding belongs to the tensor: writers may touch it
         ops.add(a->codes, rows, round_up(cols, 16), a->ldq, output);
         ops.add(a->scales, rows, round_up((cols + kActGroup - 1) / kActGroup, 16), a->lds, output);
@@ -146,7 +150,7 @@ muon_status muon_act_pack(const void* x, int64_t rows, int64_t cols, int64_t ldx
     c.act(&a.q, out, true, false);
     MUON_CALL(c.status());
     if (rows == 0) return MUON_OK;
-    a.rows = rows, a.cols = (int)cols;
+    a.rows = (uint32_t)rows, a.cols = (int)cols;
     return cuda_status(launch_act_pack(a, dtype == MUON_BF16, c.vec, static_cast<cudaStream_t>(stream)));
 }
 
@@ -159,7 +163,7 @@ muon_status muon_act_unpack(const muon_act8* in, int64_t rows, int64_t cols, voi
     c.mat(&a.x, y, ldy, true, rows == 0);
     MUON_CALL(c.status());
     if (rows == 0) return MUON_OK;
-    a.rows = rows, a.cols = (int)cols;
+    a.rows = (uint32_t)rows, a.cols = (int)cols;
     return cuda_status(launch_act_unpack(a, dtype == MUON_BF16, c.vec, static_cast<cudaStream_t>(stream)));
 }
 
@@ -199,7 +203,7 @@ muon_status muon_swiglu_forward(const void* gate, int64_t ldg, const void* up, i
     c.act(&a.a8, saved_out, true, true);
     MUON_CALL(c.status());
     if (rows == 0) return MUON_OK;
-    a.rows = rows, a.cols = (int)cols;
+    a.rows = (uint32_t)rows, a.cols = (int)cols;
     return cuda_status(launch_swiglu_forward(a, dtype == MUON_BF16, c.vec, static_cast<cudaStream_t>(stream)));
 }
 
@@ -217,7 +221,7 @@ muon_status muon_swiglu_backward(const void* da, int64_t ldda, const muon_act8* 
     c.act(&a.a8, saved_out, true, true);
     MUON_CALL(c.status());
     if (rows == 0) return MUON_OK;
-    a.rows = rows, a.cols = (int)cols;
+    a.rows = (uint32_t)rows, a.cols = (int)cols;
     return cuda_status(launch_swiglu_backward(a, dtype == MUON_BF16, c.vec, static_cast<cudaStream_t>(stream)));
 }
 
@@ -297,7 +301,7 @@ muon_status muon_rmsnorm_backward(muon_grad_plan p, const void* dy, int64_t lddy
     a.weight = weight, a.rstd = rstd, a.dweight = dweight, a.accumulate = accumulate != 0;
     a.partial = dweight ? p->partial : nullptr;
     a.status = p->status;
-    a.rows = rows, a.cols = (int)cols;
+    a.rows = (uint32_t)rows, a.cols = (int)cols;
     const bool vec = c.vec && aligned16(weight, 0);
     return cuda_status(
         launch_rmsnorm_backward(a, dtype == MUON_BF16, vec, p->sm_count, static_cast<cudaStream_t>(stream)));

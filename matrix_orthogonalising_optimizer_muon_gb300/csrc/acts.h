@@ -16,27 +16,28 @@ enum ActFormat : int { kE4M3 = 0, kInt8 = 1 };
 struct Act8 {
     uint8_t* codes;
     uint8_t* scales;
-    long long ldq, lds;
+    uint32_t ldq, lds;
     int format;
 };
 
-// One rows x cols tensor of fp32 or bf16; p null: not wanted.
+// One rows x cols tensor of fp32 or bf16, row pitch in bytes; p null: not wanted.  Rows and pitches
+// are 32-bit numbers, so the address of a row is one multiplication with a 64-bit result.
 struct Mat {
     void* p;
-    long long ld;
+    uint32_t pitch;
 };
 
 struct PackArgs {
     Mat x;      // pack: input; unpack: output
     Act8 q;
-    long long rows;
+    uint32_t rows;
     int cols;
 };
 
 struct SwigluArgs {
     Mat gate, up, a;     // backward: dgate, dup, da
     Act8 gate8, up8, a8;
-    long long rows;
+    uint32_t rows;
     int cols;
 };
 

@@ -19,11 +19,6 @@ constexpr int kFwdSegs = 2, kBwdSegs = 1;
 constexpr int kBwdWarps = 28;
 constexpr int kRingRoom = 216 * 1024;   // backward: shared memory of an SM for rows on their way
 
-template <bool BF16>
-__device__ __forceinline__ void* row_ptr(const Mat& m, long long row) {
-    return static_cast<char*>(m.p) + row * m.ld * (BF16 ? 2 : 4);
-}
-
 // Sum over the block, the same in every thread, in a fixed order: lanes by butterfly, warps in
 // sequence.  `red` has room for one float per warp; consecutive calls alternate between two
 // such rows, so one barrier each is enough.
@@ -67,22 +62,22 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_forward(const NormArgs 
     if (threadIdx.x < 16) red[threadIdx.x] = 0.f;
     __syncthreads();
     pdl_wait();
-    const long long row = blockIdx.x;
+    const uint32_t row = blockIdx.x;
     float h[S][8];
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < S; ++k) {
         const int c0 = (warp + k * warps) * kSeg;
-        seg_load<BF16, VEC>(row_ptr<BF16>(a.x, row), c0, a.cols, lane, h[k]);
+        seg_load<BF16, VEC>(row_ptr(a.x, row), c0, a.cols, lane, h[k]);
         if (a.residual.p) {
             float r[8];
-            seg_load<BF16, VEC>(row_ptr<BF16>(a.residual, row), c0, a.cols, lane, r);
+            seg_load<BF16, VEC>(row_ptr(a.residual, row), c0, a.cols, lane, r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[k][j] += r[j];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum += h[k][j] * h[k][j];
-        if (a.h.p && c0 < a.cols) seg_store<BF16, VEC>(row_ptr<BF16>(a.h, row), c0, a.cols, lane, h[k]);
+        if (a.h.p && c0 < a.cols) seg_store<BF16, VEC>(row_ptr(a.h, row), c0, a.cols, lane, h[k]);
     }
     const float rstd = inverse_rms(block_sum<false>(sum, red), (float)a.cols, a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
@@ -98,7 +93,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_forward(const NormArgs 
             h[k][j] *= rstd;
             y[j] = h[k][j] * w[j];
         }
-        if (a.y.p) seg_store<BF16, VEC>(row_ptr<BF16>(a.y, row), c0, a.cols, lane, y);
+        if (a.y.p) seg_store<BF16, VEC>(row_ptr(a.y, row), c0, a.cols, lane, y);
         if (a.saved.codes) {
             if (a.saved_weighted)
                 seg_quant<VEC>(a.saved, row, c0, a.cols, lane, y);
@@ -162,27 +157,27 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
     }
     __syncthreads();
     pdl_wait();
-    const long long first = blockIdx.x, stride = gridDim.x;
+    const uint32_t first = blockIdx.x, stride = gridDim.x, rows = (uint32_t)a.rows;   // below 2^31
     constexpr int kSize = BF16 ? 2 : 4;
     auto offset = [](const void* p) { return VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15); };
     auto pieces = [&](const void* p) { return (offset(p) + a.cols * kSize + 15) & ~15; };
-    auto fetch = [&](long long row, int s) {   // one thread
+    auto fetch = [&](uint32_t row, int s) {   // one thread
         uint8_t* to = slots + s * ring.slot;
-        const char *y = static_cast<const char*>(row_ptr<BF16>(a.dy, row)), *h = static_cast<const char*>(row_ptr<BF16>(a.h, row)),
-                   *r = static_cast<const char*>(row_ptr<BF16>(a.dres, row));
+        const char *y = row_ptr(a.dy, row), *h = row_ptr(a.h, row),
+                   *r = row_ptr(a.dres, row);
         const int ny = pieces(y), nx = a.saved.codes ? ring.x : pieces(h), nr = a.dres.p ? pieces(r) : 0;
         mbar_arrive_expect_tx(full + s, ny + nx + ring.scales + nr);
         bulk_load(to, y - offset(y), ny, full + s);
         if (a.saved.codes) {
-            bulk_load(to + ring.dy, a.saved.codes + row * a.saved.ldq, nx, full + s);
-            bulk_load(to + ring.dy + ring.x, a.saved.scales + row * a.saved.lds, ring.scales, full + s);
+            bulk_load(to + ring.dy, a.saved.codes + (uint64_t)row * a.saved.ldq, nx, full + s);
+            bulk_load(to + ring.dy + ring.x, a.saved.scales + (uint64_t)row * a.saved.lds, ring.scales, full + s);
         } else {
             bulk_load(to + ring.dy, h - offset(h), nx, full + s);
         }
         if (nr) bulk_load(to + ring.dy + ring.x + ring.scales, r - offset(r), nr, full + s);
     };
     if (RING && threadIdx.x == 0)
-        for (int s = 0; s < ring.depth && first + s * stride < a.rows; ++s) fetch(first + s * stride, s);
+        for (int s = 0; s < ring.depth && first + s * stride < rows; ++s) fetch(first + s * stride, s);
 
     float dw[S][8];
 #pragma unroll
@@ -190,7 +185,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
     int slot = 0, phase = 0, turn = 0;
-    for (long long row = first; row < a.rows; row += stride, turn ^= 1) {
+    for (uint32_t row = first; row < rows; row += stride, turn ^= 1) {
         RowIn<BF16, VEC, S> in;
         const float rstd = a.rstd[row];
         if (RING) {
@@ -198,11 +193,11 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
             mbar_wait(full + slot, phase, abort_flag, a.status, kStatusTimeoutProducer);
             const uint8_t* at = slots + slot * ring.slot;
             const uint8_t *x = at + ring.dy, *r = x + ring.x + ring.scales;
-            in.load(a, at + offset(row_ptr<BF16>(a.dy, row)), x + offset(row_ptr<BF16>(a.h, row)), x, x + ring.x,
-                    r + offset(row_ptr<BF16>(a.dres, row)), warp, warps, lane);
+            in.load(a, at + offset(row_ptr(a.dy, row)), x + offset(row_ptr(a.h, row)), x, x + ring.x,
+                    r + offset(row_ptr(a.dres, row)), warp, warps, lane);
         } else {
-            in.load(a, row_ptr<BF16>(a.dy, row), row_ptr<BF16>(a.h, row), a.saved.codes + row * a.saved.ldq,
-                    a.saved.scales + row * a.saved.lds, row_ptr<BF16>(a.dres, row), warp, warps, lane);
+            in.load(a, row_ptr(a.dy, row), row_ptr(a.h, row), a.saved.codes + (uint64_t)row * a.saved.ldq,
+                    a.saved.scales + (uint64_t)row * a.saved.lds, row_ptr(a.dres, row), warp, warps, lane);
         }
         float n[S][8], d[S][8];
         float sum = 0.f;
@@ -228,7 +223,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
         }
         const float mean = block_sum<true>(sum, red[turn]) / (float)a.cols;
         if (RING) {   // every thread has read the slot: block_sum has a barrier
-            if (threadIdx.x == 0 && row + ring.depth * stride < a.rows) fetch(row + ring.depth * stride, slot);
+            if (threadIdx.x == 0 && row + ring.depth * stride < rows) fetch(row + ring.depth * stride, slot);
             if (++slot == ring.depth) slot = 0, phase ^= 1;
         }
         if (!a.dx.p) continue;
@@ -245,7 +240,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) r[j] += rstd * (d[k][j] - n[k][j] * mean);
-            seg_store<BF16, VEC>(row_ptr<BF16>(a.dx, row), c0, a.cols, lane, r);
+            seg_store<BF16, VEC>(row_ptr(a.dx, row), c0, a.cols, lane, r);
         }
     }
     if (RING && threadIdx.x == 0 && *abort_flag) {   // give copies still in flight time to land
