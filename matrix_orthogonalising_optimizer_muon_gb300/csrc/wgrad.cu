@@ -41,6 +41,7 @@ constexpr int kWgEpiWarps = 4;
 constexpr int kWgThreads = 32 * (kEpiFirst + kWgEpiWarps);
 constexpr int kBandM = 8;               // tiles along m whose columns of dy are in flight together
 constexpr int kSortGroups = 256;        // experts that are dealt out by their number of tokens
+constexpr int kTurnTable = 96;          // turns decoded at the start
 // A ring slot is always converted by the same warps, which so see every phase of its barriers.
 static_assert(kRingR % kConvGroups == 0 && kRingM % kConvGroups == 0 && kRows % 8 == 0, "ring sizes");
 
@@ -57,7 +58,8 @@ struct WgCfg {
     static constexpr int OUT_WARP = 32 * OUT_LD;
     static constexpr int BAR_OFFSET = OUT_OFFSET + kWgEpiWarps * OUT_WARP;
     static constexpr int EXPERTS_OFFSET = BAR_OFFSET + 512;
-    static constexpr int SMEM_BYTES = EXPERTS_OFFSET + kSortGroups * 10 + 1024;
+    static constexpr int TABLE_OFFSET = EXPERTS_OFFSET + kSortGroups * 10;
+    static constexpr int SMEM_BYTES = TABLE_OFFSET + kTurnTable * 32 + 1024;
 };
 static_assert(WgCfg::SMEM_BYTES <= 232448, "weight-gradient kernel exceeds the shared memory of one CTA");
 
@@ -98,29 +100,15 @@ struct Experts {
     uint16_t order[kSortGroups];
 };
 
-struct Unit {
+struct __align__(16) Unit {
     int m0, n0;
-    long long begin, end;   // tokens
-    int group, tile, part;  // part < 0: the whole tile
+    int begin, end;             // tokens
+    int group, tile, part, pad; // part < 0: the whole tile
 };
 
-// The units of this CTA pair, one per turn.  Experts are dealt out by length: every other turn
-// runs backwards, so that no pair gets the longest of each.
-struct Turns {
-    int unit, base, pair, pairs;
-    bool back, snake;
-    __device__ __forceinline__ explicit Turns(const WgradLaunch& L)
-        : unit(blockIdx.x >> 1), base(0), pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), back(false), snake(L.a.offsets != nullptr) {}
-    __device__ __forceinline__ void next() {
-        base += pairs;
-        back = snake && !back;
-        unit = base + (back ? pairs - 1 - pair : pair);
-    }
-};
-
-__device__ __forceinline__ void expert_range(const WgradArgs& a, int g, long long* begin, long long* end) {
-    *begin = min(max((long long)a.offsets[g], 0ll), a.tokens);
-    *end = min(max((long long)a.offsets[g + 1], *begin), a.tokens);
+__device__ __forceinline__ void expert_range(const WgradArgs& a, int g, int* begin, int* end) {   // tokens < 2^31
+    *begin = min(max(a.offsets[g], 0), (int)a.tokens);
+    *end = min(max(a.offsets[g + 1], *begin), (int)a.tokens);
 }
 
 __device__ __forceinline__ Unit decode_unit(const WgradLaunch& L, const Experts* ex, int u) {
@@ -142,7 +130,7 @@ __device__ __forceinline__ Unit decode_unit(const WgradLaunch& L, const Experts*
     const int col = full ? L.wide_band.div(t) : L.last_band.div(t);
     r.m0 = (band * kBandM + t - col * (full ? kBandM : (int)L.last_band.d)) * 256;
     r.n0 = col * 256;
-    r.begin = 0, r.end = L.a.tokens;
+    r.begin = 0, r.end = (int)L.a.tokens;
     if (L.a.offsets) {
         if (L.a.groups <= kSortGroups) {
             r.group = ex->order[r.group];
@@ -152,11 +140,33 @@ __device__ __forceinline__ Unit decode_unit(const WgradLaunch& L, const Experts*
         }
     } else if (r.part >= 0) {
         const long long steps = (L.a.tokens + kWgStepT - 1) / kWgStepT;
-        r.begin = steps * r.part / L.parts * kWgStepT;
-        r.end = min(steps * (r.part + 1) / L.parts * kWgStepT, L.a.tokens);
+        r.begin = (int)(steps * r.part / L.parts * kWgStepT);
+        r.end = (int)min(steps * (r.part + 1) / L.parts * kWgStepT, L.a.tokens);
     }
     return r;
 }
+// The units of this CTA pair, one per turn.  Experts are dealt out by length: every other turn
+// runs backwards, so that no pair gets the longest of each.  The first kTurnTable turns are decoded
+// once, by all threads at the kernel's start: decoded by each role at each tile, they cost a tile
+// of few tokens more than its product (about 1000 cycles, one after another).
+struct Turns {
+    int pair, pairs, count;
+    bool snake;
+    __device__ __forceinline__ explicit Turns(const WgradLaunch& L)
+        : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), snake(L.a.offsets != nullptr) {
+        count = L.units / pairs;
+        count += unit(count) < L.units;
+    }
+    __device__ __forceinline__ int unit(int turn) const { return turn * pairs + (snake && (turn & 1) ? pairs - 1 - pair : pair); }
+    __device__ __forceinline__ Unit get(const WgradLaunch& L, const Experts* ex, uint32_t table, int turn) const {
+        if (turn >= kTurnTable) return decode_unit(L, ex, unit(turn));
+        Unit u;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.m0), "=r"(u.n0), "=r"(u.begin), "=r"(u.end) : "r"(table + turn * 32));
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.group), "=r"(u.tile), "=r"(u.part), "=r"(u.pad) : "r"(table + turn * 32 + 16));
+        return u;
+    }
+};
+
 __device__ __forceinline__ int unit_steps(const Unit& u) { return (int)((uint32_t)(u.end - u.begin + kWgStepT - 1) / kWgStepT); }
 
 __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
@@ -391,6 +401,8 @@ __device__ __forceinline__ void copy_rows(const WgradArgs& a, long long t0, int 
 
 struct EpilogueArgs {
     const Experts* ex;
+    Turns turns;
+    uint32_t table;
     uint32_t tmem_base, tempty_lead, blk;   // blk: this warp's staging block in shared memory
     uint64_t* tfull;
     volatile int* abort_flag;
@@ -452,9 +464,9 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
     const int rl = e.lane >> 3, cl = 4 * (e.lane & 7);
     int local = 0;
     bool ok = true;
-    for (Turns u(L); ok && u.unit < L.units; u.next()) {
-        const Unit w = decode_unit(L, e.ex, u.unit);
-        const int chains = (int)((w.end - w.begin + (1ll << L.chain_log) - 1) >> L.chain_log);
+    for (int turn = 0; ok && turn < e.turns.count; ++turn) {
+        const Unit w = e.turns.get(L, e.ex, e.table, turn);
+        const int chains = (int)(((uint32_t)(w.end - w.begin) + (1u << L.chain_log) - 1) >> L.chain_log);
         const int r0 = w.m0 + 128 * e.q + 32 * e.wq;
         if (chains == 0) {   // an expert without tokens
             const OutTile<BF16, WIDE> out(L, w, r0, e.lane);
@@ -596,9 +608,7 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
     Experts* ex = reinterpret_cast<Experts*>(smem + Cfg::EXPERTS_OFFSET);
     if (L.a.offsets && L.a.groups <= kSortGroups) {
         for (int g = threadIdx.x; g < L.a.groups; g += kWgThreads) {
-            long long b, e;
-            expert_range(L.a, g, &b, &e);
-            ex->begin[g] = (int)b, ex->end[g] = (int)e;
+            expert_range(L.a, g, &ex->begin[g], &ex->end[g]);
         }
         __syncthreads();
         for (int g = threadIdx.x; g < L.a.groups; g += kWgThreads) {
@@ -612,14 +622,19 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
         }
         __syncthreads();
     }
+    const Turns turns(L);
+    const uint32_t table = smem_u32(smem + Cfg::TABLE_OFFSET);
+    for (int t = threadIdx.x; t < min(turns.count, kTurnTable); t += kWgThreads)
+        reinterpret_cast<Unit*>(smem + Cfg::TABLE_OFFSET)[t] = decode_unit(L, ex, turns.unit(t));
+    __syncthreads();
 
     if (warp == 0) {
         if (lane == 0) {
             // ---------------- TMA of x
             uint32_t it = 0;
             bool ok = true;
-            for (Turns u(L); ok && u.unit < L.units; u.next()) {
-                const Unit w = decode_unit(L, ex, u.unit);
+            for (int turn = 0; ok && turn < turns.count; ++turn) {
+                const Unit w = turns.get(L, ex, table, turn);
                 const int steps = unit_steps(w);
                 const int xn = w.n0 + 128 * (int)q;
                 for (int k = 0; k < steps; ++k, ++it) {
@@ -630,7 +645,7 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
                         break;
                     }
                     uint8_t* sr = smem + Cfg::R_OFFSET + s * Cfg::R_BYTES;
-                    const int t0 = (int)(w.begin + (long long)k * kWgStepT);
+                    const int t0 = w.begin + k * kWgStepT;
                     mbar_arrive_expect_tx(full_r + s, Cfg::R_BYTES);
                     tma_load_2d(sr, &L.map_x, full_r + s, xn, t0);
                     tma_load_2d(sr + Cfg::RAW_BYTES, &L.map_s, full_r + s, (xn >> 5) & ~15, t0);
@@ -650,8 +665,8 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
             // ---------------- TMA of dy, completion on the even CTA's barrier
             uint32_t slot = 0, ph = 1;
             bool ok = true;
-            for (Turns u(L); ok && u.unit < L.units; u.next()) {
-                const Unit w = decode_unit(L, ex, u.unit);
+            for (int turn = 0; ok && turn < turns.count; ++turn) {
+                const Unit w = turns.get(L, ex, table, turn);
                 const int steps = unit_steps(w);
                 const int ym = w.m0 + 128 * (int)q;
                 for (int k = 0; k < steps; ++k) {
@@ -659,22 +674,22 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
                         ok = false;
                         break;
                     }
-                    const long long t0 = w.begin + (long long)k * kWgStepT;
+                    const int t0 = w.begin + k * kWgStepT;
                     uint8_t* sa = smem + slot * Cfg::SLOT_BYTES;
-                    if (!TMA_Y || t0 + kWgStepT > w.end) {
+                    if (!TMA_Y || w.end - t0 < kWgStepT) {
                         // the conversion warps fill it, or first see it land (tail) and zero the rows that
                         // belong to other experts
                         if (TMA_Y) {
                             mbar_arrive_expect_tx(tail + slot, Cfg::A_BYTES);
-                            tma_load_2d(sa, &L.map_y, tail + slot, ym, (int)t0);
-                            tma_load_2d(sa + Cfg::CHUNK_BYTES, &L.map_y, tail + slot, ym + 64, (int)t0);
+                            tma_load_2d(sa, &L.map_y, tail + slot, ym, t0);
+                            tma_load_2d(sa + Cfg::CHUNK_BYTES, &L.map_y, tail + slot, ym + 64, t0);
                         }
                         if (leader) mbar_arrive(ready + slot);
                     } else {
                         const uint32_t fb = mapa_shared(smem_u32(ready + slot), 0);
                         if (leader) mbar_arrive_expect_tx(ready + slot, 2 * Cfg::A_BYTES);
-                        tma_load_2d_pair(sa, &L.map_y, fb, ym, (int)t0);
-                        tma_load_2d_pair(sa + Cfg::CHUNK_BYTES, &L.map_y, fb, ym + 64, (int)t0);
+                        tma_load_2d_pair(sa, &L.map_y, fb, ym, t0);
+                        tma_load_2d_pair(sa + Cfg::CHUNK_BYTES, &L.map_y, fb, ym + 64, t0);
                     }
                     if (++slot == kRingM) slot = 0, ph ^= 1u;
                 }
@@ -699,10 +714,10 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
             constexpr uint32_t kSlot = Cfg::SLOT_BYTES >> 4, kStep = 16 * 128 >> 4;   // of the address field
             const uint64_t ad0 = sdesc_sw128(smem_u32(smem), Cfg::CHUNK_BYTES, 1024);
             const uint64_t bd0 = sdesc_sw128(smem_u32(smem) + Cfg::A_BYTES, Cfg::CHUNK_BYTES, 1024);
-            for (Turns u(L); ok && u.unit < L.units; u.next()) {
-                const Unit w = decode_unit(L, ex, u.unit);
+            for (int turn = 0; ok && turn < turns.count; ++turn) {
+                const Unit w = turns.get(L, ex, table, turn);
                 const int steps = unit_steps(w), chain = 1 << (L.chain_log - 6);
-                const int last = ((int)(w.end - w.begin - 1) & (kWgStepT - 1)) / 16 + 1;   // MMAs of the last step
+                const int last = ((w.end - w.begin - 1) & (kWgStepT - 1)) / 16 + 1;   // MMAs of the last step
                 for (int k0 = 0; ok && k0 < steps; k0 += chain, ++local) {
                     const uint32_t acc = local & 1;
                     if (!mbar_wait_idle(tempty + acc, (local >> 1 & 1u) ^ 1u, abort_flag, L.a.status,
@@ -769,12 +784,12 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
         const uint32_t src0 = row0 * 128 + ((pc ^ prow) << 4);             // half 0; half 1: ^ 64
         const uint32_t dst0 = row0 * 128 + (((2 * pc) ^ prow) << 4);       // its second piece: ^ 16
         const uint32_t sel = 0x0404u + 0x1010u * (pc >> 1);                // its scale byte in bytes 1 and 3
-        for (Turns u(L); ok && u.unit < L.units; u.next()) {
-            const Unit w = decode_unit(L, ex, u.unit);
+        for (int turn = 0; ok && turn < turns.count; ++turn) {
+            const Unit w = turns.get(L, ex, table, turn);
             const int steps = unit_steps(w);
             const int off = ((w.n0 + 128 * (int)q) >> 5) & 15;   // the CTA's four of the 16 loaded scales
             for (int k = 0; k < steps; ++k, ++it) {
-                const int left = (int)min((long long)kWgStepT, w.end - w.begin - (long long)k * kWgStepT);
+                const int left = min(kWgStepT, w.end - w.begin - k * kWgStepT);
                 if (it % kConvGroups != cg) continue;
                 const uint32_t r = it % kRingR, b = it % kRingM;
                 const uint32_t sr = smem_u32(smem + Cfg::R_OFFSET + r * Cfg::R_BYTES);
@@ -845,8 +860,7 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
         }
     } else {
         // ---------------- epilogue
-        EpilogueArgs e;
-        e.ex = ex;
+        EpilogueArgs e{ex, turns, table};
         e.tmem_base = tmem_base;
         e.tfull = tfull;
         e.tempty_lead = mapa_shared(smem_u32(tempty), 0);
