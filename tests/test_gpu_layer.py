@@ -345,6 +345,34 @@ def test_wgrad(mu, plan, tokens, m, n, fmt, dtype, accumulate, scaled):
     wgrad_check(mu, plan, tokens, m, n, fmt, dtype, accumulate, scaled)
 
 
+@pytest.mark.parametrize("m,n", [(300, 392), (257, 391), (64, 96)])
+@pytest.mark.parametrize("dtype,accumulate", [("f32", False), ("f32", True), ("bf16", False), ("bf16", True)])
+def test_wgrad_long(mu, plan, m, n, dtype, accumulate):
+    """Few tiles and many tokens: tiles split along the tokens and joined, fp32 sums in several chains."""
+    wgrad_check(mu, plan, 8203, m, n, "e4m3", dtype, accumulate, True)
+
+
+def test_wgrad_many_experts(mu, plan):
+    """More experts than are dealt out by length, and more tiles per CTA pair than are decoded at the start."""
+    import torch
+    e, m, n, tokens = 301, 1288, 1296, 3010            # 36 tiles each: 10836 tiles, over 96 turns of 76 pairs
+    edges = [10 * i for i in range(e)] + [tokens]
+    edges[5] = edges[4]                                # one without tokens, its neighbour with twenty
+    dy, x8 = rand((tokens, m), "bf16", 1, 0.5), filled(mu, rand((tokens, n), "f32", 2), "int8")
+    g = torch.empty((e, m, n), dtype=torch.bfloat16, device="cuda")
+    plan.wgrad(dy, x8, g, offsets=torch.tensor(edges, dtype=torch.int32, device="cuda"))
+    plan.sync()
+    d, v = f64(dy), values(x8)
+    for k in (0, 4, 5, 150, 299, 300):
+        a, b = edges[k], edges[k + 1]
+        close(g[k], d[a:b].T @ v[a:b], 60 * U * (np.abs(d[a:b]).T @ np.abs(v[a:b])) + 1e-30)
+    whole = torch.zeros((m, n), dtype=torch.float64, device="cuda")
+    for part in g.split(16):
+        whole += part.double().sum(0)
+    want = torch.from_numpy(d.T @ v).cuda()
+    assert float((whole - want).norm() / want.norm()) < 2.0 ** -8   # bf16 roundings of the parts
+
+
 @pytest.mark.parametrize("pad", [1, 4, 8])
 def test_wgrad_strided_dy(mu, plan, pad):
     wgrad_check(mu, plan, 200, 320, 288, "int8", "f32", False, True, pad)

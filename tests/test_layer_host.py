@@ -100,6 +100,22 @@ def test_rmsnorm_backward_refuses(lib, kw):
                                      a["weight"], None, 50, 4, 50, 0, a["dx"], 50, a["dweight"], 0, None) == BAD
 
 
+def test_act_layout_matches_the_header():
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "muon.h")).read()
+    body = re.search(r"typedef struct \{([^}]*)\}\s*muon_act8\s*;", re.sub(r"/\*.*?\*/", "", src, flags=re.S)).group(1)
+    names = [n.strip(" *") for decl in body.split(";") for n in decl.strip().split(" ", 1)[-1].split(",") if decl.strip()]
+    assert names == [f for f, _ in mu.MuonAct8._fields_]
+    assert ctypes.sizeof(mu.MuonAct8) == 40 and mu.MuonAct8.format.offset == 32
+
+
+@pytest.mark.parametrize("pitch", [1 << 32, (1 << 32) + 16, 1 << 40])
+def test_pitches_of_four_gigabytes_are_refused(lib, pitch):
+    assert lib.muon_act_pack(A, 4, 50, pitch // 4, 0, act(), None) == BAD
+    assert lib.muon_act_pack(A, 4, 50, 50, 0, act(codes=2 * F, scales=2 * F + (1 << 36), ldq=pitch), None) == BAD
+
+
 def test_interleaved_halves_do_not_overlap(lib):
     """dgate and dup as the halves of one (rows, 2 cols) tensor pass the overlap check; one column further they
     do not.  (A bad `da` pitch ends the accepted call before it launches.)"""
