@@ -41,21 +41,27 @@ namespace {
 constexpr int kWgStepT = 64;            // tokens per step
 constexpr int kRingM = 4;               // steps of MMA operands
 constexpr int kRingR = 8;               // steps of x as it arrives
-constexpr int kConvWarps = 8;
 // Steps in conversion at a time: the way from a landed step to its arrival at the MMA warp takes a
 // warp about 2000 cycles, four times a step's MMAs (183 us with two groups, 148 with four).
 constexpr int kConvGroups = 4;
-constexpr int kGroupWarps = kConvWarps / kConvGroups;
-constexpr int kRows = kWgStepT / kGroupWarps;   // token rows per conversion warp and step
 constexpr int kConvFirst = 3;           // first conversion warp
-constexpr int kEpiFirst = kConvFirst + kConvWarps;
 constexpr int kWgEpiWarps = 4;
-constexpr int kWgThreads = 32 * (kEpiFirst + kWgEpiWarps);
+// Warps by whether dy comes by TMA or is copied by the conversion warps, which are then twice as many
+// (8192 x 3585 x 3584: 298 us; 434 with eight).
+template <bool TMA_Y>
+struct Roles {
+    static constexpr int kConvWarps = TMA_Y ? 8 : 16;
+    static constexpr int kGroupWarps = kConvWarps / kConvGroups;
+    static constexpr int kRows = kWgStepT / kGroupWarps;   // token rows per conversion warp and step
+    static constexpr int kEpiFirst = kConvFirst + kConvWarps;
+    static constexpr int kThreads = 32 * (kEpiFirst + kWgEpiWarps);
+    static_assert(kRows % 8 == 0, "whole passes");
+};
 constexpr int kBandM = 8;               // tiles along m whose columns of dy are in flight together
 constexpr int kSortGroups = 256;        // experts that are dealt out by their number of tokens
 constexpr int kTurnTable = 96;          // turns decoded at the start
 // A ring slot is always converted by the same warps, which so see every phase of its barriers.
-static_assert(kRingR % kConvGroups == 0 && kRingM % kConvGroups == 0 && kRows % 8 == 0, "ring sizes");
+static_assert(kRingR % kConvGroups == 0 && kRingM % kConvGroups == 0, "ring sizes");
 
 struct WgCfg {
     static constexpr int A_BYTES = 128 * kWgStepT * 2;      // 128 columns of dy, or of x in bf16
@@ -306,21 +312,27 @@ struct OutTile {
                 for (int i = 0; i < 32; ++i) f[i] *= s[i & 3];
             }
             if (more) {
-                if (BF16) {   // every load before the first store
-                    float4 g[8];
-                    const char* from = to;
+                if (BF16) {   // half of the loads before their stores
 #pragma unroll
-                    for (int i = 0; i < 8; ++i, from += step)
-                        if (i < rows) g[i] = load_four<BF16>(from);
+                    for (int h = 0; h < 8; h += 4) {
+                        float4 g[4];
+                        char* from = to;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        f[4 * i] += g[i].x, f[4 * i + 1] += g[i].y, f[4 * i + 2] += g[i].z, f[4 * i + 3] += g[i].w;
+                        for (int i = 0; i < 4; ++i, from += step)
+                            if (h + i < rows) g[i] = load_four<BF16>(from);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i, to += step) {
+                            float* v = f + 4 * (h + i);
+                            v[0] += g[i].x, v[1] += g[i].y, v[2] += g[i].z, v[3] += g[i].w;
+                            if (h + i < rows) store_four<BF16>(to, v);
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i, to += step)
                         if (i < rows) red_four(to, f + 4 * i);
-                    return;
                 }
+                return;
             }
             if (rows == 8) {
 #pragma unroll
@@ -337,18 +349,22 @@ struct OutTile {
         for (int i = 0; i < 32; ++i) f[i] *= s;
         if (more) {
             if (BF16) {
-                float g[32];
-                const char* from = to;
 #pragma unroll
-                for (int i = 0; i < 32; ++i, from += step) g[i] = i < rows ? load_one<BF16>(from, 0) : 0.f;
+                for (int h = 0; h < 32; h += 8) {
+                    float g[8];
+                    char* from = to;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) f[i] += g[i];
+                    for (int i = 0; i < 8; ++i, from += step) g[i] = h + i < rows ? load_one<BF16>(from, 0) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i, to += step)
+                        if (h + i < rows) store_one<BF16>(to, 0, f[h + i] + g[i]);
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i, to += step)
                     if (i < rows) red_one(to, f[i]);
-                return;
             }
+            return;
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i, to += step)
@@ -471,7 +487,7 @@ __device__ __forceinline__ void store_rows(const WgradLaunch& L, const Unit& w, 
 
 // One epilogue warp: TMEM lane quarter wq, 32 rows of the tile, each 32 x 32 block through
 // shared memory into the layout of OutTile.
-template <bool BF16, bool WIDE>
+template <bool BF16, bool WIDE, bool DIRECT>
 __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArgs& e) {
     const int rl = e.lane >> 3, cl = 4 * (e.lane & 7);
     int local = 0;
@@ -502,7 +518,7 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
             }
             tc_fence_after();
             const uint32_t tbase = e.tmem_base + acc * 256 + (static_cast<uint32_t>(e.wq * 32) << 16);
-            if (BF16 && WIDE && L.sectors && part == nullptr && !L.a.accumulate && ch == 0 && w.n0 + 256 <= L.a.n &&
+            if (BF16 && WIDE && DIRECT && L.sectors && part == nullptr && !L.a.accumulate && ch == 0 && w.n0 + 256 <= L.a.n &&
                 r0 + 32 <= L.a.m) {
                 store_rows(L, w, e, tbase, acc);
                 ++local;
@@ -567,8 +583,10 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
 
 // TMA_Y: dy's rows are 16-byte aligned and come by TMA; else the conversion warps copy them.
 template <int FMT, bool TMA_Y, bool BF16>
-__global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ WgradLaunch L) {
+__global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_constant__ WgradLaunch L) {
     using Cfg = WgCfg;
+    using R = Roles<TMA_Y>;
+    constexpr int kGroupWarps = R::kGroupWarps, kRows = R::kRows, kEpiFirst = R::kEpiFirst, kWgThreads = R::kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full_r = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFFSET);
@@ -880,9 +898,9 @@ __global__ void __launch_bounds__(kWgThreads) k_wgrad(const __grid_constant__ Wg
         e.abort_flag = abort_flag;
         e.q = (int)q, e.wq = warp & 3, e.lane = lane;
         if (L.wide)
-            epilogue<BF16, true>(L, e);
+            epilogue<BF16, true, TMA_Y>(L, e);
         else
-            epilogue<BF16, false>(L, e);
+            epilogue<BF16, false, TMA_Y>(L, e);
     }
 
     tc_fence_before();
@@ -974,7 +992,8 @@ cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaS
         !map_2d(&L.map_x, a.x.codes, true, a.n, a.tokens, a.x.ldq, 128, true) ||
         !map_2d(&L.map_s, a.x.scales, true, (a.n + kActGroup - 1) / kActGroup, a.tokens, a.x.lds, 16, false))
         return cudaErrorInvalidValue;
-        return launch_pdl_cluster(pick(a.x.format, tma_y, bf16_grad), dim3(2 * std::min(L.units, pairs)), dim3(kWgThreads), WgCfg::SMEM_BYTES,
+        return launch_pdl_cluster(pick(a.x.format, tma_y, bf16_grad), dim3(2 * std::min(L.units, pairs)),
+                              dim3(tma_y ? Roles<true>::kThreads : Roles<false>::kThreads), WgCfg::SMEM_BYTES,
                               s, 2u, L);
 }
 
