@@ -49,9 +49,10 @@ struct Raw {
     static constexpr bool kPairs = BF16 && VEC;
     uint32_t r[kPairs ? 4 : 8];
 
-    // Columns c0 .. c0 + 255 of the row at p; zero at and beyond `cols`.
+    // Columns c0 .. c0 + 255 of the row at p; zero at and beyond `cols`.  FULL: none is.
+    template <bool FULL = false>
     __device__ __forceinline__ void load(const void* p, int c0, int cols, int lane) {
-        if (VEC && c0 + 8 * lane + 8 <= cols) {
+        if (VEC && (FULL || c0 + 8 * lane + 8 <= cols)) {
             const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + (long long)(c0 + 8 * lane) * (BF16 ? 2 : 4));
             const uint4 a = q[0];
             r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
@@ -59,9 +60,7 @@ struct Raw {
                 const uint4 b = q[1];
                 r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
             }
-            return;
-        }
-        if constexpr (kPairs) {
+        } else if constexpr (kPairs) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = c0 + 8 * lane + 2 * j;
@@ -94,9 +93,9 @@ __device__ __forceinline__ void seg_load(const void* p, int c0, int cols, int la
     raw.get(v);
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16, bool VEC, bool FULL = false>
 __device__ __forceinline__ void seg_store(void* p, int c0, int cols, int lane, const float (&v)[8]) {
-    if (VEC && c0 + 8 * lane + 8 <= cols) {
+    if (VEC && (FULL || c0 + 8 * lane + 8 <= cols)) {
         const long long e = c0 + 8 * lane;
         if (BF16) {
             *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + e) =
@@ -106,12 +105,12 @@ __device__ __forceinline__ void seg_store(void* p, int c0, int cols, int lane, c
             f[0] = make_float4(v[0], v[1], v[2], v[3]);
             f[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int c = c0 + seg_col<VEC>(lane, j);
-        if (c < cols) store_one<BF16>(p, c, v[j]);
+        for (int j = 0; j < 8; ++j) {
+            const int c = c0 + seg_col<VEC>(lane, j);
+            if (c < cols) store_one<BF16>(p, c, v[j]);
+        }
     }
 }
 
@@ -167,7 +166,7 @@ __device__ __forceinline__ void act_number4(uint32_t w, float* v) {
 
 // Writes the segment in 8 bits at row `row`.  Values beyond `cols` must be zero; lanes of
 // a partly filled last group take part with those zeros.
-template <int FMT, bool VEC>
+template <int FMT, bool VEC, bool FULL>
 __device__ __forceinline__ void seg_quant(const Act8& q, uint32_t row, int c0, int cols, int lane,
                                           const float (&v)[8]) {
     uint8_t* codes = q.codes + (uint64_t)row * q.ldq + c0;
@@ -185,7 +184,7 @@ __device__ __forceinline__ void seg_quant(const Act8& q, uint32_t row, int c0, i
         uint32_t hi = act_code2<FMT>(v[4] * inv, v[5] * inv) | act_code2<FMT>(v[6] * inv, v[7] * inv) << 16;
         if (byte == 255u) lo = hi = 0;   // a group that is not finite
         // row pitches are multiples of 16: the eight bytes lie within the row's padding
-        if (c0 + 8 * lane < cols) {
+        if (FULL || c0 + 8 * lane < cols) {
             *reinterpret_cast<uint2*>(codes + 8 * lane) = make_uint2(lo, hi);
             if ((lane & 3) == 0) scales[lane >> 2] = (uint8_t)byte;
         }
@@ -202,13 +201,13 @@ __device__ __forceinline__ void seg_quant(const Act8& q, uint32_t row, int c0, i
     }
 }
 // The same, the format chosen at run time (uniform over the launch).
-template <bool VEC>
+template <bool VEC, bool FULL = false>
 __device__ __forceinline__ void seg_quant(const Act8& q, uint32_t row, int c0, int cols, int lane,
                                           const float (&v)[8]) {
     if (q.format == kE4M3)
-        seg_quant<kE4M3, VEC>(q, row, c0, cols, lane, v);
+        seg_quant<kE4M3, VEC, FULL>(q, row, c0, cols, lane, v);
     else
-        seg_quant<kInt8, VEC>(q, row, c0, cols, lane, v);
+        seg_quant<kInt8, VEC, FULL>(q, row, c0, cols, lane, v);
 }
 
 // A lane's share of a segment in 8 bits as loaded: eight codes and their scale byte (VEC), else
@@ -217,15 +216,17 @@ template <bool VEC>
 struct Raw8 {
     uint32_t r[VEC ? 3 : 8];
 
-    // The segment of row `row`; reads as zero at and beyond `cols`.
+    // The segment of row `row`; reads as zero at and beyond `cols`.  FULL: none is.
+    template <bool FULL = false>
     __device__ __forceinline__ void load(const Act8& q, uint32_t row, int c0, int cols, int lane) {
-        load(q.codes + (uint64_t)row * q.ldq, q.scales + (uint64_t)row * q.lds, c0, cols, lane);
+        load<FULL>(q.codes + (uint64_t)row * q.ldq, q.scales + (uint64_t)row * q.lds, c0, cols, lane);
     }
+    template <bool FULL = false>
     __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int c0, int cols, int lane) {
         codes += c0, scales += c0 >> 5;
         if constexpr (VEC) {
             r[0] = r[1] = r[2] = 0;
-            if (c0 + 8 * lane < cols) {   // the row's padding completes the eight bytes
+            if (FULL || c0 + 8 * lane < cols) {   // the row's padding completes the eight bytes
                 const uint2 w = *reinterpret_cast<const uint2*>(codes + 8 * lane);
                 r[0] = w.x, r[1] = w.y, r[2] = scales[lane >> 2];
                 const int left = cols - c0 - 8 * lane;

@@ -16,7 +16,7 @@ constexpr int kThreads = 256;
 // Blocks that fit an SM (by registers); about four times as many are launched, which evens out the
 // SMs' ends.  8192 x 18944 bf16: SwiGLU forward 207 us with five (48 registers; 209 with four),
 // backward 278 us with five (287 with six, 296 with four).  Packing: 71 us with eight, 77 with six.
-constexpr int kFit = 8, kFitForward = 5, kFitBackward = 5;
+constexpr int kFit = 8, kFitForward = 4, kFitBackward = 5;
 constexpr int kSms = 152;
 // Segments in flight per warp: with one the loads do not cover HBM's latency (an earlier forward kernel
 // took 250 us, 222 with two), with four the registers leave too few warps (277); one where rows are
@@ -25,7 +25,7 @@ template <bool VEC>
 constexpr int kUnroll = VEC ? 2 : 1;
 
 // Units of this warp: row and first column of each, in steps of the launch's warps without a
-// division per step.
+// division per step.  Most lie inside the row and need no masks: they run as FULL.
 template <bool VEC>
 struct Walk {
     static constexpr int kWidth = kUnroll<VEC> * kSeg;
@@ -45,41 +45,55 @@ struct Walk {
     }
 };
 
+template <bool BF16, bool VEC, bool FULL>
+__device__ __forceinline__ void unit_act_pack(const PackArgs& a, const Walk<VEC>& w, int lane) {
+    const void* x = row_ptr(a.x, w.row);
+    Raw<BF16, VEC> raw[kUnroll<VEC>];
+#pragma unroll
+    for (int k = 0; k < kUnroll<VEC>; ++k) raw[k].template load<FULL>(x, w.col + k * kSeg, a.cols, lane);
+#pragma unroll
+    for (int k = 0; k < kUnroll<VEC>; ++k) {
+        float v[8];
+        raw[k].get(v);
+        seg_quant<VEC, FULL>(a.q, w.row, w.col + k * kSeg, a.cols, lane, v);
+    }
+}
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_pack(const PackArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
     for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        const void* x = row_ptr(a.x, w.row);
-        Raw<BF16, VEC> raw[kUnroll<VEC>];
-#pragma unroll
-        for (int k = 0; k < kUnroll<VEC>; ++k) raw[k].load(x, w.col + k * kSeg, a.cols, lane);
-#pragma unroll
-        for (int k = 0; k < kUnroll<VEC>; ++k) {
-            float v[8];
-            raw[k].get(v);
-            seg_quant<VEC>(a.q, w.row, w.col + k * kSeg, a.cols, lane, v);
-        }
+        if (VEC && w.col + Walk<VEC>::kWidth <= a.cols)
+            unit_act_pack<BF16, VEC, true>(a, w, lane);
+        else
+            unit_act_pack<BF16, VEC, false>(a, w, lane);
     }
 }
 
+template <bool BF16, bool VEC, bool FULL>
+__device__ __forceinline__ void unit_act_unpack(const PackArgs& a, const Walk<VEC>& w, int lane) {
+    void* y = row_ptr(a.x, w.row);
+    Raw8<VEC> raw[kUnroll<VEC>];
+#pragma unroll
+    for (int k = 0; k < kUnroll<VEC>; ++k) raw[k].template load<FULL>(a.q, w.row, w.col + k * kSeg, a.cols, lane);
+#pragma unroll
+    for (int k = 0; k < kUnroll<VEC>; ++k) {
+        float v[8];
+        raw[k].get(a.q.format, v);
+        seg_store<BF16, VEC, FULL>(y, w.col + k * kSeg, a.cols, lane, v);
+    }
+}
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_unpack(const PackArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
     for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        void* y = row_ptr(a.x, w.row);
-        Raw8<VEC> raw[kUnroll<VEC>];
-#pragma unroll
-        for (int k = 0; k < kUnroll<VEC>; ++k) raw[k].load(a.q, w.row, w.col + k * kSeg, a.cols, lane);
-#pragma unroll
-        for (int k = 0; k < kUnroll<VEC>; ++k) {
-            float v[8];
-            raw[k].get(a.q.format, v);
-            seg_store<BF16, VEC>(y, w.col + k * kSeg, a.cols, lane, v);
-        }
+        if (VEC && w.col + Walk<VEC>::kWidth <= a.cols)
+            unit_act_unpack<BF16, VEC, true>(a, w, lane);
+        else
+            unit_act_unpack<BF16, VEC, false>(a, w, lane);
     }
 }
 
@@ -97,69 +111,83 @@ __device__ __forceinline__ float sigmoid(float z) {
     return z < -87.3f ? 0.f : r;
 }
 
+template <bool BF16, bool VEC, bool FULL>
+__device__ __forceinline__ void unit_swiglu_forward(const SwigluArgs& a, const Walk<VEC>& w, int lane) {
+    const void *gate = row_ptr(a.gate, w.row), *up = row_ptr(a.up, w.row);
+    Raw<BF16, VEC> gr[kUnroll<VEC>], ur[kUnroll<VEC>];
+#pragma unroll
+    for (int k = 0; k < kUnroll<VEC>; ++k) {
+        gr[k].template load<FULL>(gate, w.col + k * kSeg, a.cols, lane);
+        ur[k].template load<FULL>(up, w.col + k * kSeg, a.cols, lane);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll<VEC>; ++k) {
+        const int c0 = w.col + k * kSeg;
+        float g[8], u[8], o[8];
+        gr[k].get(g);
+        ur[k].get(u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid(g[j]) * u[j];
+        if (a.a.p) seg_store<BF16, VEC, FULL>(row_ptr(a.a, w.row), c0, a.cols, lane, o);
+        if (a.gate8.codes) seg_quant<VEC, FULL>(a.gate8, w.row, c0, a.cols, lane, g);
+        if (a.up8.codes) seg_quant<VEC, FULL>(a.up8, w.row, c0, a.cols, lane, u);
+        if (a.a8.codes) seg_quant<VEC, FULL>(a.a8, w.row, c0, a.cols, lane, o);
+    }
+}
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads, kFitForward) k_swiglu_forward(const SwigluArgs a) {
+__global__ void __launch_bounds__(kThreads, VEC ? kFitForward : 5) k_swiglu_forward(const SwigluArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
     for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        const void *gate = row_ptr(a.gate, w.row), *up = row_ptr(a.up, w.row);
-        Raw<BF16, VEC> gr[kUnroll<VEC>], ur[kUnroll<VEC>];
-#pragma unroll
-        for (int k = 0; k < kUnroll<VEC>; ++k) {
-            gr[k].load(gate, w.col + k * kSeg, a.cols, lane);
-            ur[k].load(up, w.col + k * kSeg, a.cols, lane);
-        }
-#pragma unroll
-        for (int k = 0; k < kUnroll<VEC>; ++k) {
-            const int c0 = w.col + k * kSeg;
-            float g[8], u[8], o[8];
-            gr[k].get(g);
-            ur[k].get(u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid(g[j]) * u[j];
-            if (a.a.p) seg_store<BF16, VEC>(row_ptr(a.a, w.row), c0, a.cols, lane, o);
-            if (a.gate8.codes) seg_quant<VEC>(a.gate8, w.row, c0, a.cols, lane, g);
-            if (a.up8.codes) seg_quant<VEC>(a.up8, w.row, c0, a.cols, lane, u);
-            if (a.a8.codes) seg_quant<VEC>(a.a8, w.row, c0, a.cols, lane, o);
-        }
+        if (VEC && w.col + Walk<VEC>::kWidth <= a.cols)
+            unit_swiglu_forward<BF16, VEC, true>(a, w, lane);
+        else
+            unit_swiglu_forward<BF16, VEC, false>(a, w, lane);
     }
 }
 
+template <bool BF16, bool VEC, bool FULL>
+__device__ __forceinline__ void unit_swiglu_backward(const SwigluArgs& a, const Walk<VEC>& w, int lane) {
+    const void* da = row_ptr(a.a, w.row);
+    Raw<BF16, VEC> dr[kUnroll<VEC>];
+    Raw8<VEC> gr[kUnroll<VEC>], ur[kUnroll<VEC>];
+#pragma unroll
+    for (int k = 0; k < kUnroll<VEC>; ++k) {
+        dr[k].template load<FULL>(da, w.col + k * kSeg, a.cols, lane);
+        gr[k].template load<FULL>(a.gate8, w.row, w.col + k * kSeg, a.cols, lane);
+        ur[k].template load<FULL>(a.up8, w.row, w.col + k * kSeg, a.cols, lane);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll<VEC>; ++k) {
+        const int c0 = w.col + k * kSeg;
+        float g[8], u[8], d[8], o[8];
+        dr[k].get(d);
+        gr[k].get(a.gate8.format, g);
+        ur[k].get(a.up8.format, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float s = sigmoid(g[j]);
+            const float silu = g[j] * s;
+            o[j] = silu * u[j];
+            g[j] = d[j] * u[j] * (s + silu * (1.f - s));   // dgate
+            u[j] = d[j] * silu;                            // dup
+        }
+        seg_store<BF16, VEC, FULL>(row_ptr(a.gate, w.row), c0, a.cols, lane, g);
+        seg_store<BF16, VEC, FULL>(row_ptr(a.up, w.row), c0, a.cols, lane, u);
+        if (a.a8.codes) seg_quant<VEC, FULL>(a.a8, w.row, c0, a.cols, lane, o);
+    }
+}
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads, BF16 && VEC ? kFitBackward : 4) k_swiglu_backward(const SwigluArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
     for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        const void* da = row_ptr(a.a, w.row);
-        Raw<BF16, VEC> dr[kUnroll<VEC>];
-        Raw8<VEC> gr[kUnroll<VEC>], ur[kUnroll<VEC>];
-#pragma unroll
-        for (int k = 0; k < kUnroll<VEC>; ++k) {
-            dr[k].load(da, w.col + k * kSeg, a.cols, lane);
-            gr[k].load(a.gate8, w.row, w.col + k * kSeg, a.cols, lane);
-            ur[k].load(a.up8, w.row, w.col + k * kSeg, a.cols, lane);
-        }
-#pragma unroll
-        for (int k = 0; k < kUnroll<VEC>; ++k) {
-            const int c0 = w.col + k * kSeg;
-            float g[8], u[8], d[8], o[8];
-            dr[k].get(d);
-            gr[k].get(a.gate8.format, g);
-            ur[k].get(a.up8.format, u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float s = sigmoid(g[j]);
-                const float silu = g[j] * s;
-                o[j] = silu * u[j];
-                g[j] = d[j] * u[j] * (s + silu * (1.f - s));   // dgate
-                u[j] = d[j] * silu;                            // dup
-            }
-            seg_store<BF16, VEC>(row_ptr(a.gate, w.row), c0, a.cols, lane, g);
-            seg_store<BF16, VEC>(row_ptr(a.up, w.row), c0, a.cols, lane, u);
-            if (a.a8.codes) seg_quant<VEC>(a.a8, w.row, c0, a.cols, lane, o);
-        }
+        if (VEC && w.col + Walk<VEC>::kWidth <= a.cols)
+            unit_swiglu_backward<BF16, VEC, true>(a, w, lane);
+        else
+            unit_swiglu_backward<BF16, VEC, false>(a, w, lane);
     }
 }
 

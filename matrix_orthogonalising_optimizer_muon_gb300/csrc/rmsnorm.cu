@@ -2,10 +2,11 @@
 //
 // One block per row; warp w of the block holds segments w, w + W, ... of the row (256
 // values each, eight per lane) in registers, so every value crosses HBM once each way, which
-// bounds both passes.  Measured at 16384 x 3584 bf16 with the residual: forward 88 us for 530 MB
-// (6.05 TB/s, 91 % of the measured copy rate), backward from 8 bits 84 us for 413 MB (4.9 TB/s, 73 %:
+// bounds both passes.  Measured at 16384 x 3584 bf16 with the residual: forward 82 us for 530 MB
+// (6.5 TB/s, 96 % of the measured copy rate), backward from 8 bits 80 us for 413 MB (5.2 TB/s, 76 %:
 // 4 us of it are the sum of the blocks' dweight rows, the rest waits on each row's barrier).
 #include <algorithm>
+#include <type_traits>
 
 #include "act8.cuh"
 #include "kernels.h"
@@ -16,10 +17,13 @@ namespace {
 
 constexpr int kMaxThreads = 512;   // 128 registers per thread: up to eight segments per warp
 // Least segments per warp.  Forward: with two a row's block is small enough for many to share an SM,
-// one reducing while others load (16384 x 3584 bf16: 88 us, 99 with one, 97 with four).
+// one reducing while others load (16384 x 3584 bf16: 82 us, and 88 with the two segments' loads one
+// after the other; there 99 with one, 97 with four).
 constexpr int kFwdSegs = 2, kBwdSegs = 1;
-// Backward: warps per SM (the same: 83 us; 88 with 14 warps of two segments, 99 with 42 of one).
-constexpr int kBwdWarps = 28;
+// Backward: warps per SM, as many as 64 registers allow.  With 28, rows of 15 segments have one block
+// per SM instead of two (16384 x 3585 bf16: 254 us, 135 with 32; 65536 x 1024: 97 us, 88 with 32).
+// With 80 registers fewer fit: 16384 x 3584 takes 107 us, 80 with 64.
+constexpr int kBwdWarps = 32;
 constexpr int kRingRoom = 216 * 1024;   // backward: shared memory of an SM for rows on their way
 
 // Sum over the block, the same in every thread, in a fixed order: lanes by butterfly, warps in
@@ -68,19 +72,37 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_forward(const NormArgs 
     const uint32_t row = blockIdx.x;
     float h[S][8];
     float sum = 0.f;
+    constexpr int P = VEC && S > 1 ? 2 : 1;   // segments whose loads are in flight together
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-        const int c0 = (warp + k * warps) * kSeg;
-        seg_load<BF16, VEC>(row_ptr(a.x, row), c0, a.cols, lane, h[k]);
-        if (a.residual.p) {
-            float r[8];
-            seg_load<BF16, VEC>(row_ptr(a.residual, row), c0, a.cols, lane, r);
+    for (int k0 = 0; k0 < S; k0 += P) {
+        Raw<BF16, VEC> x[P], r[P];
+        auto load = [&](auto full) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[k][j] += r[j];
+            for (int k = 0; k < P; ++k) {
+                const int c0 = (warp + (k0 + k) * warps) * kSeg;
+                x[k].template load<full.value>(row_ptr(a.x, row), c0, a.cols, lane);
+                if (a.residual.p) r[k].template load<full.value>(row_ptr(a.residual, row), c0, a.cols, lane);
+            }
+        };
+        if (VEC && (warp + (k0 + P - 1) * warps + 1) * kSeg <= a.cols)
+            load(std::true_type{});
+        else
+            load(std::false_type{});
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            const int c0 = (warp + (k0 + k) * warps) * kSeg;
+            float(&v)[8] = h[k0 + k];
+            x[k].get(v);
+            if (a.residual.p) {
+                float b[8];
+                r[k].get(b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += b[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += v[j] * v[j];
+            if (a.h.p && c0 < a.cols) seg_store<BF16, VEC>(row_ptr(a.h, row), c0, a.cols, lane, v);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += h[k][j] * h[k][j];
-        if (a.h.p && c0 < a.cols) seg_store<BF16, VEC>(row_ptr(a.h, row), c0, a.cols, lane, h[k]);
     }
     const float rstd = inverse_rms(block_sum<false>(sum, red), (float)a.cols, a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
@@ -144,7 +166,7 @@ constexpr int kRingMost = 4;
 // bulk copies while one is reduced, so that HBM stays busy across the reduction's barrier
 // with registers for one row only.
 template <bool BF16, bool VEC, int S, bool RING>
-__global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdArgs a, const RingShape ring) {
+__global__ void __launch_bounds__(kMaxThreads, S == 1 ? 2 : 1) k_rmsnorm_backward(const NormBwdArgs a, const RingShape ring) {
     extern __shared__ __align__(128) uint8_t slots[];
     __shared__ __align__(16) float red[2][16];
     __shared__ uint64_t full[kRingMost];
@@ -187,6 +209,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
     for (int k = 0; k < S; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
+    // one segment per warp leaves registers for its weights (16384 x 3584 from h: 77 us, 83 without)
+    float wk[8];
+    if constexpr (S == 1) seg_load<false, VEC>(a.weight, warp * kSeg, a.cols, lane, wk);
     int slot = 0, phase = 0, turn = 0;
     for (uint32_t row = first; row < rows; row += stride, turn ^= 1) {
         RowIn<BF16, VEC, S> in;
@@ -206,8 +231,6 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < S; ++k) {
-            const int c0 = (warp + k * warps) * kSeg;
-            float w[8];
             in.dy[k].get(d[k]);
             if (a.saved.codes) {
                 in.x[k].q.get(a.saved.format, n[k]);
@@ -216,11 +239,11 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_backward(const NormBwdA
 #pragma unroll
                 for (int j = 0; j < 8; ++j) n[k][j] *= rstd;
             }
-            seg_load<false, VEC>(a.weight, c0, a.cols, lane, w);
+            if constexpr (S > 1) seg_load<false, VEC>(a.weight, (warp + k * warps) * kSeg, a.cols, lane, wk);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 dw[k][j] += d[k][j] * n[k][j];
-                d[k][j] *= w[j];
+                d[k][j] *= wk[j];
                 sum += d[k][j] * n[k][j];
             }
         }
