@@ -1,10 +1,12 @@
 // Activations to 8 bits and back, and SwiGLU with its inputs held in 8 bits.
 //
 // All four kernels read and write each value once (HBM-bound).  A warp takes units of kUnroll
-// neighbouring segments of 256 values of a row, all loads before the first store.  Beside HBM they are
-// bound by instruction issue (64-70 % of the cycles): scales, codes and the exponential come to 40 to
-// 55 instructions per value pair.  Measured at 8192 x 18944 bf16: forward 207 us (6.04 TB/s, 91 % of
-// the measured copy rate), backward 278 us (5.1 TB/s, 76 %), pack 70 us (100 %), unpack 78 us (91 %).
+// neighbouring segments of 256 values of a row, all loads before the first store.  HBM bounds
+// them once units that lie inside the row skip the per-lane masks (with masks the loads wait on one
+// another's branches: forward 207 us, backward 278).  Measured at 8192 x 18944 bf16: forward 202 us
+// (6.2 TB/s, 93 % of the measured copy rate), backward 219 us (6.4 TB/s, 96 %), pack 69 us (102 %),
+// unpack 71 us (99 %).  Rows that are not aligned go element by element, bound by instruction issue
+// (18945 columns: 369, 457, 155 and 126 us).
 #include "act8.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -14,8 +16,9 @@ namespace {
 
 constexpr int kThreads = 256;
 // Blocks that fit an SM (by registers); about four times as many are launched, which evens out the
-// SMs' ends.  8192 x 18944 bf16: SwiGLU forward 207 us with five (48 registers; 209 with four),
-// backward 278 us with five (287 with six, 296 with four).  Packing: 71 us with eight, 77 with six.
+// SMs' ends.  8192 x 18944 bf16: SwiGLU forward 202 us with four (216 with five, whose 48 registers
+// spill), backward 219 us with five (221 with six, 224 with four).  Packing: 71 us with eight, 77 with
+// six.  Element by element, 18945 columns: forward 369 us with five, 429 with four.
 constexpr int kFit = 8, kFitForward = 4, kFitBackward = 5;
 constexpr int kSms = 152;
 // Segments in flight per warp: with one the loads do not cover HBM's latency (an earlier forward kernel

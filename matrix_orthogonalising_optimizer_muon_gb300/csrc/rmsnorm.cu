@@ -3,7 +3,7 @@
 // One block per row; warp w of the block holds segments w, w + W, ... of the row (256
 // values each, eight per lane) in registers, so every value crosses HBM once each way, which
 // bounds both passes.  Measured at 16384 x 3584 bf16 with the residual: forward 82 us for 530 MB
-// (6.5 TB/s, 96 % of the measured copy rate), backward from 8 bits 80 us for 413 MB (5.2 TB/s, 76 %:
+// (6.5 TB/s, 96 % of the measured copy rate), backward from 8 bits 76 us for 413 MB (5.4 TB/s, 80 %:
 // 4 us of it are the sum of the blocks' dweight rows, the rest waits on each row's barrier).
 #include <algorithm>
 #include <type_traits>
@@ -21,8 +21,9 @@ constexpr int kMaxThreads = 512;   // 128 registers per thread: up to eight segm
 // after the other; there 99 with one, 97 with four).
 constexpr int kFwdSegs = 2, kBwdSegs = 1;
 // Backward: warps per SM, as many as 64 registers allow.  With 28, rows of 15 segments have one block
-// per SM instead of two (16384 x 3585 bf16: 254 us, 135 with 32; 65536 x 1024: 97 us, 88 with 32).
-// With 80 registers fewer fit: 16384 x 3584 takes 107 us, 80 with 64.
+// per SM instead of two (16384 x 3585 bf16: 254 us, 135 with 32; 65536 x 1024: 97 us, 88 with 32;
+// 125 and 83 since).
+// With 80 registers fewer fit: 16384 x 3584 took 107 us, 80 with 64.
 constexpr int kBwdWarps = 32;
 constexpr int kRingRoom = 216 * 1024;   // backward: shared memory of an SM for rows on their way
 
@@ -128,26 +129,42 @@ __global__ void __launch_bounds__(kMaxThreads) k_rmsnorm_forward(const NormArgs 
     }
 }
 
-// One row's operands of a thread, as loaded.
-template <bool BF16, bool VEC, int S>
+// Where one row's operands lie: in HBM, or in a slot of the ring.
+struct RowAt {
+    const void *dy, *h, *dres;
+    const uint8_t *codes, *scales;
+};
+// A thread's operands of segments warp + k0 warps, warp + (k0 + 1) warps, ... of a row, as loaded.
+template <bool BF16, bool VEC, int N>
 struct RowIn {
-    Raw<BF16, VEC> dy[S], dres[S];
+    Raw<BF16, VEC> dy[N], dres[N];
     union Xhat {
         Raw<BF16, VEC> h;
         Raw8<VEC> q;
         __device__ Xhat() {}
-    } x[S];
-    __device__ __forceinline__ void load(const NormBwdArgs& a, const void* dyp, const void* hp, const uint8_t* codes,
-                                         const uint8_t* scales, const void* dresp, int warp, int warps, int lane) {
+    } x[N];
+    __device__ __forceinline__ void load(const NormBwdArgs& a, const RowAt& at, int k0, int warp, int warps, int lane,
+                                         bool with_dres) {
 #pragma unroll
-        for (int k = 0; k < S; ++k) {
-            const int c0 = (warp + k * warps) * kSeg;
-            dy[k].load(dyp, c0, a.cols, lane);
+        for (int k = 0; k < N; ++k) {
+            const int c0 = (warp + (k0 + k) * warps) * kSeg;
+            dy[k].load(at.dy, c0, a.cols, lane);
             if (a.saved.codes)
-                x[k].q.load(codes, scales, c0, a.cols, lane);
+                x[k].q.load(at.codes, at.scales, c0, a.cols, lane);
             else
-                x[k].h.load(hp, c0, a.cols, lane);
-            if (a.dres.p) dres[k].load(dresp, c0, a.cols, lane);
+                x[k].h.load(at.h, c0, a.cols, lane);
+            if (with_dres) dres[k].load(at.dres, c0, a.cols, lane);
+        }
+    }
+    // Segment k's dy and normalised input.
+    __device__ __forceinline__ void get(const NormBwdArgs& a, float rstd, int k, float (&d)[8], float (&n)[8]) const {
+        dy[k].get(d);
+        if (a.saved.codes) {
+            x[k].q.get(a.saved.format, n);
+        } else {
+            x[k].h.get(n);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) n[j] *= rstd;
         }
     }
 };
@@ -204,6 +221,11 @@ __global__ void __launch_bounds__(kMaxThreads, S == 1 ? 2 : 1) k_rmsnorm_backwar
     if (RING && threadIdx.x == 0)
         for (int s = 0; s < ring.depth && first + s * stride < rows; ++s) fetch(first + s * stride, s);
 
+    // KEEP: the row's operands stay in registers between the sum and dx.  Else, where they would not
+    // fit, they are read again, one segment at a time (4096 x 16383 bf16: 348 us, 698 kept; 1024 x
+    // 32768 fp32: 191, 244 kept; but 4096 x 16384 bf16: 136 kept, 240 read again).
+    constexpr bool KEEP = S <= 2 || (VEC && (BF16 || S == 4));
+    constexpr int N = KEEP ? S : 1;   // segments in registers
     float dw[S][8];
 #pragma unroll
     for (int k = 0; k < S; ++k)
@@ -214,59 +236,71 @@ __global__ void __launch_bounds__(kMaxThreads, S == 1 ? 2 : 1) k_rmsnorm_backwar
     if constexpr (S == 1) seg_load<false, VEC>(a.weight, warp * kSeg, a.cols, lane, wk);
     int slot = 0, phase = 0, turn = 0;
     for (uint32_t row = first; row < rows; row += stride, turn ^= 1) {
-        RowIn<BF16, VEC, S> in;
         const float rstd = a.rstd[row];
+        RowAt at{row_ptr(a.dy, row), row_ptr(a.h, row), row_ptr(a.dres, row),
+                 a.saved.codes + (uint64_t)row * a.saved.ldq, a.saved.scales + (uint64_t)row * a.saved.lds};
         if (RING) {
             // a wait that runs out raises the flag and the status word; later waits then return at once
             mbar_wait(full + slot, phase, abort_flag, a.status, kStatusTimeoutProducer);
-            const uint8_t* at = slots + slot * ring.slot;
-            const uint8_t *x = at + ring.dy, *r = x + ring.x + ring.scales;
-            in.load(a, at + offset(row_ptr(a.dy, row)), x + offset(row_ptr(a.h, row)), x, x + ring.x,
-                    r + offset(row_ptr(a.dres, row)), warp, warps, lane);
-        } else {
-            in.load(a, row_ptr(a.dy, row), row_ptr(a.h, row), a.saved.codes + (uint64_t)row * a.saved.ldq,
-                    a.saved.scales + (uint64_t)row * a.saved.lds, row_ptr(a.dres, row), warp, warps, lane);
+            const uint8_t* p = slots + slot * ring.slot;
+            const uint8_t *x = p + ring.dy, *r = x + ring.x + ring.scales;
+            at = RowAt{p + offset(at.dy), x + offset(at.h), r + offset(at.dres), x, x + ring.x};
         }
-        float n[S][8], d[S][8];
+        RowIn<BF16, VEC, N> in;
+        float n[N][8], d[N][8];
         float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < S; ++k) {
-            in.dy[k].get(d[k]);
-            if (a.saved.codes) {
-                in.x[k].q.get(a.saved.format, n[k]);
-            } else {
-                in.x[k].h.get(n[k]);
+        for (int k0 = 0; k0 < S; k0 += N) {
+            in.load(a, at, k0, warp, warps, lane, KEEP && a.dres.p);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) n[k][j] *= rstd;
-            }
-            if constexpr (S > 1) seg_load<false, VEC>(a.weight, (warp + k * warps) * kSeg, a.cols, lane, wk);
+            for (int k = 0; k < N; ++k) {
+                in.get(a, rstd, k, d[k], n[k]);
+                if constexpr (S > 1) seg_load<false, VEC>(a.weight, (warp + (k0 + k) * warps) * kSeg, a.cols, lane, wk);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dw[k][j] += d[k][j] * n[k][j];
-                d[k][j] *= wk[j];
-                sum += d[k][j] * n[k][j];
+                for (int j = 0; j < 8; ++j) {
+                    dw[k0 + k][j] += d[k][j] * n[k][j];
+                    d[k][j] *= wk[j];
+                    sum += d[k][j] * n[k][j];
+                }
             }
         }
         const float mean = block_sum<true>(sum, red[turn]) / (float)a.cols;
-        if (RING) {   // every thread has read the slot: block_sum has a barrier
+        // every thread has read the slot once block_sum's barrier, or with !KEEP the one below, is passed
+        auto refill = [&] {
             if (threadIdx.x == 0 && row + ring.depth * stride < rows) fetch(row + ring.depth * stride, slot);
             if (++slot == ring.depth) slot = 0, phase ^= 1;
-        }
-        if (!a.dx.p) continue;
+        };
+        if (RING && KEEP) refill();
+        if (a.dx.p) {
 #pragma unroll
-        for (int k = 0; k < S; ++k) {
-            const int c0 = (warp + k * warps) * kSeg;
-            if (c0 >= a.cols) break;
-            float r[8];
-            if (a.dres.p) {
-                in.dres[k].get(r);
-            } else {
+            for (int k0 = 0; k0 < S; k0 += N) {
+                if (!KEEP) in.load(a, at, k0, warp, warps, lane, a.dres.p);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) r[j] = 0.f;
+                for (int k = 0; k < N; ++k) {
+                    const int c0 = (warp + (k0 + k) * warps) * kSeg;
+                    if (c0 >= a.cols) break;
+                    if constexpr (!KEEP) {
+                        in.get(a, rstd, k, d[k], n[k]);
+                        seg_load<false, VEC>(a.weight, c0, a.cols, lane, wk);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) d[k][j] *= wk[j];
+                    }
+                    float r[8];
+                    if (a.dres.p) {
+                        in.dres[k].get(r);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) r[j] = 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) r[j] += rstd * (d[k][j] - n[k][j] * mean);
+                    seg_store<BF16, VEC>(row_ptr(a.dx, row), c0, a.cols, lane, r);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] += rstd * (d[k][j] - n[k][j] * mean);
-            seg_store<BF16, VEC>(row_ptr(a.dx, row), c0, a.cols, lane, r);
+        }
+        if (RING && !KEEP) {
+            __syncthreads();
+            refill();
         }
     }
     if (RING && threadIdx.x == 0 && *abort_flag) {   // give copies still in flight time to land
