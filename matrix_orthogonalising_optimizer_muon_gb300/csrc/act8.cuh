@@ -1,11 +1,16 @@
 // Device side of the 8-bit activation format, in units of one warp's segment: 256
 // neighbouring values of a row, eight per lane.
 //
-// Two layouts of a segment over the lanes, chosen per launch:
-//  VEC   lane l holds values 8 l .. 8 l + 7: one 16-byte load (bf16) or two (fp32) per
-//        lane; four lanes share a scale group.  Needs 16-byte aligned rows.
-//  else  lane l holds values 32 j + l, j = 0 .. 7: element loads, coalesced whatever the
-//        alignment; value j of all lanes is one scale group.
+// How a segment lies over the lanes and is moved, chosen per launch:
+//  kAligned  lane l holds values 8 l .. 8 l + 7: one 16-byte load (bf16) or two (fp32) per lane; four
+//            lanes share a scale group.  Needs 16-byte aligned rows.
+//  kShifted  the same on rows that are not aligned: the lanes load and store the aligned pieces that
+//            hold their values and shift them into place.  The elementwise kernels use it.
+//  kByValue  lane l holds values 32 j + l, j = 0 .. 7: element loads, coalesced whatever the alignment;
+//            value j of all lanes is one scale group.  The norms use it: their rows' loads and stores are
+//            a smaller part beside the barrier (forward 127 us, 151 shifted, at 16384 x 3585 bf16), while
+//            SwiGLU and packing gain (8192 x 18945: 369, 457, 155, 126 us by value, 295, 337, 85, 96
+//            shifted).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -15,6 +20,7 @@
 namespace muon {
 
 constexpr int kSeg = 256;
+enum { kByValue = 0, kAligned = 1, kShifted = 2 };   // the first two convert from `rows are aligned`
 
 template <bool VEC>
 __device__ __forceinline__ int seg_col(int lane, int j) {
@@ -42,37 +48,73 @@ __device__ __forceinline__ void store_one(void* p, long long i, float v) {
         static_cast<float*>(p)[i] = v;
 }
 
-// A lane's eight values of a segment as loaded: bf16 in pairs (VEC), else fp32.  Loading and
+// Words moved down by `shift` bytes (0 to 15, whole values); the last four are left undefined.
+template <bool BF16, int N>
+__device__ __forceinline__ void words_down(uint32_t (&w)[N], int shift) {
+#pragma unroll
+    for (int i = 0; i + 2 < N; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+    if (BF16) {
+#pragma unroll
+        for (int i = 0; i + 1 < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 2) * 8);
+    }
+}
+
+// A lane's eight values of a segment as loaded: bf16 in pairs (not by value), else fp32.  Loading and
 // widening are apart so that several segments' loads can be in flight in few registers.
-template <bool BF16, bool VEC>
+template <bool BF16, int MODE>
 struct Raw {
-    static constexpr bool kPairs = BF16 && VEC;
-    uint32_t r[kPairs ? 4 : 8];
+    static constexpr bool VEC = MODE == kAligned, kPairs = BF16 && MODE != kByValue;
+    static constexpr int kWords = kPairs ? 4 : 8, kSize = BF16 ? 2 : 4;
+    uint32_t r[kWords];
 
     // Columns c0 .. c0 + 255 of the row at p; zero at and beyond `cols`.  FULL: none is.
     template <bool FULL = false>
     __device__ __forceinline__ void load(const void* p, int c0, int cols, int lane) {
-        if (VEC && (FULL || c0 + 8 * lane + 8 <= cols)) {
-            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + (long long)(c0 + 8 * lane) * (BF16 ? 2 : 4));
-            const uint4 a = q[0];
-            r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
-            if constexpr (!kPairs) {
-                const uint4 b = q[1];
-                r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
-            }
-        } else if constexpr (kPairs) {
+        if constexpr (MODE == kByValue) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = c0 + 8 * lane + 2 * j;
-                const uint16_t* q = static_cast<const uint16_t*>(p) + c;
-                r[j] = (c < cols ? q[0] : 0u) | (c + 1 < cols ? (uint32_t)q[1] << 16 : 0u);
+            for (int j = 0; j < 8; ++j) {
+                const int c = c0 + seg_col<false>(lane, j);
+                r[j] = c < cols ? __float_as_uint(load_one<BF16>(p, c)) : 0u;
+            }
+        } else {
+            load_pieces<FULL>(p, c0, cols, lane);
+        }
+    }
+    template <bool FULL>
+    __device__ __forceinline__ void load_pieces(const void* p, int c0, int cols, int lane) {
+        if (!VEC && !FULL && c0 + kSeg <= cols) return load_pieces<true>(p, c0, cols, lane);
+        const int left = cols - c0 - 8 * lane;
+        const char* at = static_cast<const char*>(p) + (long long)(c0 + 8 * lane) * kSize;
+        if (VEC && (FULL || left >= 8)) {
+            const uint4* q = reinterpret_cast<const uint4*>(at);
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 a = q[i];
+                r[4 * i] = a.x, r[4 * i + 1] = a.y, r[4 * i + 2] = a.z, r[4 * i + 3] = a.w;
+            }
+        } else if (FULL || left > 0) {
+            // the aligned pieces that hold the values; the last one again where there are fewer
+            constexpr int kPieces = kWords / 4 + (VEC ? 0 : 1);
+            const int shift = VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(at) & 15);
+            const int last = (shift + (FULL ? 8 : min(left, 8)) * kSize - 1) & ~15;
+            uint32_t w[4 * kPieces];
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const uint4 a = *reinterpret_cast<const uint4*>(at - shift + min(16 * i, last));
+                w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+            }
+            if (!VEC) words_down<BF16>(w, shift);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                r[i] = w[i];
+                if (!FULL && BF16) r[i] &= left > 2 * i + 1 ? 0xffffffffu : left > 2 * i ? 0xffffu : 0u;
+                if (!FULL && !BF16 && left <= i) r[i] = 0u;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = c0 + seg_col<VEC>(lane, j);
-                r[j] = c < cols ? __float_as_uint(load_one<BF16>(p, c)) : 0u;
-            }
+            for (int i = 0; i < kWords; ++i) r[i] = 0u;
         }
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -93,24 +135,77 @@ __device__ __forceinline__ void seg_load(const void* p, int c0, int cols, int la
     raw.get(v);
 }
 
-template <bool BF16, bool VEC, bool FULL = false>
+// Stores the segment's values below `cols`.  Every lane of the warp takes part.  Shifted: a lane stores the aligned piece (fp32: two) that begins in the lane below it, with the
+// values that reach into it from there; the segment's ragged ends go value by value.
+template <bool BF16, int MODE, bool FULL = false>
 __device__ __forceinline__ void seg_store(void* p, int c0, int cols, int lane, const float (&v)[8]) {
-    if (VEC && (FULL || c0 + 8 * lane + 8 <= cols)) {
-        const long long e = c0 + 8 * lane;
-        if (BF16) {
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + e) =
-                make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
-        } else {
-            float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + e);
-            f[0] = make_float4(v[0], v[1], v[2], v[3]);
-            f[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
-    } else {
+    if constexpr (MODE == kByValue) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = c0 + seg_col<VEC>(lane, j);
+            const int c = c0 + seg_col<false>(lane, j);
             if (c < cols) store_one<BF16>(p, c, v[j]);
         }
+        return;
+    }
+    if (MODE == kShifted && !FULL && c0 + kSeg <= cols) return seg_store<BF16, MODE, true>(p, c0, cols, lane, v);
+    constexpr int kWords = BF16 ? 4 : 8, kSize = BF16 ? 2 : 4;
+    uint32_t own[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) own[i] = BF16 ? bf16_pair(v[2 * i], v[2 * i + 1]) : __float_as_uint(v[i]);
+    const int c = c0 + 8 * lane;
+    char* at = static_cast<char*>(p) + (long long)c * kSize;
+    auto one = [&](char* to, uint32_t word, int j) {
+        if (BF16)
+            *reinterpret_cast<uint16_t*>(to + 2 * j) = (uint16_t)(j & 1 ? word >> 16 : word);
+        else
+            *reinterpret_cast<uint32_t*>(to + 4 * j) = word;
+    };
+    if (MODE == kAligned) {
+        if (FULL || c + 8 <= cols) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i)
+                reinterpret_cast<uint4*>(at)[i] = make_uint4(own[4 * i], own[4 * i + 1], own[4 * i + 2], own[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < cols) one(at, own[BF16 ? j >> 1 : j], j);
+        }
+        return;
+    }
+    const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15);   // of every lane's values
+    const int back = shift / kSize;   // values of the lane below in this lane's pieces
+    uint32_t w[kWords + 4];           // the lane below's last 16 bytes, then this one's
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, own[kWords - 4 + i], 1);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[4 + i] = own[i];
+    // the pieces begin 16 - shift bytes into w; for 0 they are this lane's own
+    words_down<BF16>(w, shift ? 16 - shift : 0);
+    if (shift == 0) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = own[i];
+    }
+    const bool whole = (lane > 0 || shift == 0) && (FULL || c - back + 8 <= cols);
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i)
+            reinterpret_cast<uint4*>(at - shift)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    // the values outside those pieces: lane 0's first 8 - back and lane 31's last, one per lane
+    const int from = lane < 8 - back ? 0 : 31;
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        const uint32_t x = __shfl_sync(0xffffffffu, own[i], from);
+        if ((BF16 ? lane >> 1 : lane) == i) word = x;
+    }
+    const int e = c0 + 8 * from + lane;
+    if (lane < 8 && shift != 0 && (FULL || e < cols))
+        one(static_cast<char*>(p) + (long long)(e - lane) * kSize, word, lane);
+    if (!FULL && !whole && (lane > 0 || shift == 0)) {   // the piece that holds the row's end
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c - back + j < cols) one(at - shift, w[BF16 ? j >> 1 : j], j);
     }
 }
 

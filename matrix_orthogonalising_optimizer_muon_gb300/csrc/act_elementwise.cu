@@ -5,8 +5,8 @@
 // them once units that lie inside the row skip the per-lane masks (with masks the loads wait on one
 // another's branches: forward 207 us, backward 278).  Measured at 8192 x 18944 bf16: forward 202 us
 // (6.2 TB/s, 93 % of the measured copy rate), backward 219 us (6.4 TB/s, 96 %), pack 69 us (102 %),
-// unpack 71 us (99 %).  Rows that are not aligned go element by element, bound by instruction issue
-// (18945 columns: 369, 457, 155 and 126 us).
+// unpack 71 us (99 %).  Rows that are not aligned are loaded and stored in shifted
+// pieces, bound by instruction issue (18945 columns: 295, 337, 85 and 96 us).
 #include "act8.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -18,20 +18,20 @@ constexpr int kThreads = 256;
 // Blocks that fit an SM (by registers); about four times as many are launched, which evens out the
 // SMs' ends.  8192 x 18944 bf16: SwiGLU forward 202 us with four (216 with five, whose 48 registers
 // spill), backward 219 us with five (221 with six, 224 with four).  Packing: 71 us with eight, 77 with
-// six.  Element by element, 18945 columns: forward 369 us with five, 429 with four.
+// six.  The shifted kernels need more registers: 18945 columns, unpacking 96 us with six (106 with
+// eight), SwiGLU backward 337 us with four (376 with five).
 constexpr int kFit = 8, kFitForward = 4, kFitBackward = 5;
 constexpr int kSms = 152;
 // Segments in flight per warp: with one the loads do not cover HBM's latency (an earlier forward kernel
-// took 250 us, 222 with two), with four the registers leave too few warps (277); one where rows are
-// loaded element by element.
+// took 250 us, 222 with two), with four the registers leave too few warps (277).
+constexpr int kUnroll = 2;
 template <bool VEC>
-constexpr int kUnroll = VEC ? 2 : 1;
+constexpr int kMode = VEC ? kAligned : kShifted;
 
 // Units of this warp: row and first column of each, in steps of the launch's warps without a
 // division per step.  Most lie inside the row and need no masks: they run as FULL.
-template <bool VEC>
 struct Walk {
-    static constexpr int kWidth = kUnroll<VEC> * kSeg;
+    static constexpr int kWidth = kUnroll * kSeg;
     uint32_t row, drow;   // below 2^31 each
     int col, dcol, width;
     __device__ __forceinline__ Walk(int cols) {
@@ -49,16 +49,16 @@ struct Walk {
 };
 
 template <bool BF16, bool VEC, bool FULL>
-__device__ __forceinline__ void unit_act_pack(const PackArgs& a, const Walk<VEC>& w, int lane) {
+__device__ __forceinline__ void unit_act_pack(const PackArgs& a, const Walk& w, int lane) {
     const void* x = row_ptr(a.x, w.row);
-    Raw<BF16, VEC> raw[kUnroll<VEC>];
+    Raw<BF16, kMode<VEC>> raw[kUnroll];
 #pragma unroll
-    for (int k = 0; k < kUnroll<VEC>; ++k) raw[k].template load<FULL>(x, w.col + k * kSeg, a.cols, lane);
+    for (int k = 0; k < kUnroll; ++k) raw[k].template load<FULL>(x, w.col + k * kSeg, a.cols, lane);
 #pragma unroll
-    for (int k = 0; k < kUnroll<VEC>; ++k) {
+    for (int k = 0; k < kUnroll; ++k) {
         float v[8];
         raw[k].get(v);
-        seg_quant<VEC, FULL>(a.q, w.row, w.col + k * kSeg, a.cols, lane, v);
+        seg_quant<true, FULL>(a.q, w.row, w.col + k * kSeg, a.cols, lane, v);
     }
 }
 template <bool BF16, bool VEC>
@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_pack(const Pac
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        if (VEC && w.col + Walk<VEC>::kWidth <= a.cols)
+    for (Walk w(a.cols); w.row < a.rows; w.next()) {
+        if (w.col + Walk::kWidth <= a.cols)
             unit_act_pack<BF16, VEC, true>(a, w, lane);
         else
             unit_act_pack<BF16, VEC, false>(a, w, lane);
@@ -75,16 +75,16 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_pack(const Pac
 }
 
 template <bool BF16, bool VEC, bool FULL>
-__device__ __forceinline__ void unit_act_unpack(const PackArgs& a, const Walk<VEC>& w, int lane) {
+__device__ __forceinline__ void unit_act_unpack(const PackArgs& a, const Walk& w, int lane) {
     void* y = row_ptr(a.x, w.row);
-    Raw8<VEC> raw[kUnroll<VEC>];
+    Raw8<true> raw[kUnroll];
 #pragma unroll
-    for (int k = 0; k < kUnroll<VEC>; ++k) raw[k].template load<FULL>(a.q, w.row, w.col + k * kSeg, a.cols, lane);
+    for (int k = 0; k < kUnroll; ++k) raw[k].template load<FULL>(a.q, w.row, w.col + k * kSeg, a.cols, lane);
 #pragma unroll
-    for (int k = 0; k < kUnroll<VEC>; ++k) {
+    for (int k = 0; k < kUnroll; ++k) {
         float v[8];
         raw[k].get(a.q.format, v);
-        seg_store<BF16, VEC, FULL>(y, w.col + k * kSeg, a.cols, lane, v);
+        seg_store<BF16, kMode<VEC>, FULL>(y, w.col + k * kSeg, a.cols, lane, v);
     }
 }
 template <bool BF16, bool VEC>
@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_unpack(const P
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        if (VEC && w.col + Walk<VEC>::kWidth <= a.cols)
+    for (Walk w(a.cols); w.row < a.rows; w.next()) {
+        if (w.col + Walk::kWidth <= a.cols)
             unit_act_unpack<BF16, VEC, true>(a, w, lane);
         else
             unit_act_unpack<BF16, VEC, false>(a, w, lane);
@@ -115,35 +115,35 @@ __device__ __forceinline__ float sigmoid(float z) {
 }
 
 template <bool BF16, bool VEC, bool FULL>
-__device__ __forceinline__ void unit_swiglu_forward(const SwigluArgs& a, const Walk<VEC>& w, int lane) {
+__device__ __forceinline__ void unit_swiglu_forward(const SwigluArgs& a, const Walk& w, int lane) {
     const void *gate = row_ptr(a.gate, w.row), *up = row_ptr(a.up, w.row);
-    Raw<BF16, VEC> gr[kUnroll<VEC>], ur[kUnroll<VEC>];
+    Raw<BF16, kMode<VEC>> gr[kUnroll], ur[kUnroll];
 #pragma unroll
-    for (int k = 0; k < kUnroll<VEC>; ++k) {
+    for (int k = 0; k < kUnroll; ++k) {
         gr[k].template load<FULL>(gate, w.col + k * kSeg, a.cols, lane);
         ur[k].template load<FULL>(up, w.col + k * kSeg, a.cols, lane);
     }
 #pragma unroll
-    for (int k = 0; k < kUnroll<VEC>; ++k) {
+    for (int k = 0; k < kUnroll; ++k) {
         const int c0 = w.col + k * kSeg;
         float g[8], u[8], o[8];
         gr[k].get(g);
         ur[k].get(u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid(g[j]) * u[j];
-        if (a.a.p) seg_store<BF16, VEC, FULL>(row_ptr(a.a, w.row), c0, a.cols, lane, o);
-        if (a.gate8.codes) seg_quant<VEC, FULL>(a.gate8, w.row, c0, a.cols, lane, g);
-        if (a.up8.codes) seg_quant<VEC, FULL>(a.up8, w.row, c0, a.cols, lane, u);
-        if (a.a8.codes) seg_quant<VEC, FULL>(a.a8, w.row, c0, a.cols, lane, o);
+        if (a.a.p) seg_store<BF16, kMode<VEC>, FULL>(row_ptr(a.a, w.row), c0, a.cols, lane, o);
+        if (a.gate8.codes) seg_quant<true, FULL>(a.gate8, w.row, c0, a.cols, lane, g);
+        if (a.up8.codes) seg_quant<true, FULL>(a.up8, w.row, c0, a.cols, lane, u);
+        if (a.a8.codes) seg_quant<true, FULL>(a.a8, w.row, c0, a.cols, lane, o);
     }
 }
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads, VEC ? kFitForward : 5) k_swiglu_forward(const SwigluArgs a) {
+__global__ void __launch_bounds__(kThreads, kFitForward) k_swiglu_forward(const SwigluArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        if (VEC && w.col + Walk<VEC>::kWidth <= a.cols)
+    for (Walk w(a.cols); w.row < a.rows; w.next()) {
+        if (w.col + Walk::kWidth <= a.cols)
             unit_swiglu_forward<BF16, VEC, true>(a, w, lane);
         else
             unit_swiglu_forward<BF16, VEC, false>(a, w, lane);
@@ -151,18 +151,18 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFitForward : 5) k_swiglu_forw
 }
 
 template <bool BF16, bool VEC, bool FULL>
-__device__ __forceinline__ void unit_swiglu_backward(const SwigluArgs& a, const Walk<VEC>& w, int lane) {
+__device__ __forceinline__ void unit_swiglu_backward(const SwigluArgs& a, const Walk& w, int lane) {
     const void* da = row_ptr(a.a, w.row);
-    Raw<BF16, VEC> dr[kUnroll<VEC>];
-    Raw8<VEC> gr[kUnroll<VEC>], ur[kUnroll<VEC>];
+    Raw<BF16, kMode<VEC>> dr[kUnroll];
+    Raw8<true> gr[kUnroll], ur[kUnroll];
 #pragma unroll
-    for (int k = 0; k < kUnroll<VEC>; ++k) {
+    for (int k = 0; k < kUnroll; ++k) {
         dr[k].template load<FULL>(da, w.col + k * kSeg, a.cols, lane);
         gr[k].template load<FULL>(a.gate8, w.row, w.col + k * kSeg, a.cols, lane);
         ur[k].template load<FULL>(a.up8, w.row, w.col + k * kSeg, a.cols, lane);
     }
 #pragma unroll
-    for (int k = 0; k < kUnroll<VEC>; ++k) {
+    for (int k = 0; k < kUnroll; ++k) {
         const int c0 = w.col + k * kSeg;
         float g[8], u[8], d[8], o[8];
         dr[k].get(d);
@@ -176,9 +176,9 @@ __device__ __forceinline__ void unit_swiglu_backward(const SwigluArgs& a, const 
             g[j] = d[j] * u[j] * (s + silu * (1.f - s));   // dgate
             u[j] = d[j] * silu;                            // dup
         }
-        seg_store<BF16, VEC, FULL>(row_ptr(a.gate, w.row), c0, a.cols, lane, g);
-        seg_store<BF16, VEC, FULL>(row_ptr(a.up, w.row), c0, a.cols, lane, u);
-        if (a.a8.codes) seg_quant<VEC, FULL>(a.a8, w.row, c0, a.cols, lane, o);
+        seg_store<BF16, kMode<VEC>, FULL>(row_ptr(a.gate, w.row), c0, a.cols, lane, g);
+        seg_store<BF16, kMode<VEC>, FULL>(row_ptr(a.up, w.row), c0, a.cols, lane, u);
+        if (a.a8.codes) seg_quant<true, FULL>(a.a8, w.row, c0, a.cols, lane, o);
     }
 }
 template <bool BF16, bool VEC>
@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kThreads, BF16 && VEC ? kFitBackward : 4) k_sw
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    for (Walk<VEC> w(a.cols); w.row < a.rows; w.next()) {
-        if (VEC && w.col + Walk<VEC>::kWidth <= a.cols)
+    for (Walk w(a.cols); w.row < a.rows; w.next()) {
+        if (w.col + Walk::kWidth <= a.cols)
             unit_swiglu_backward<BF16, VEC, true>(a, w, lane);
         else
             unit_swiglu_backward<BF16, VEC, false>(a, w, lane);
@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(kThreads, BF16 && VEC ? kFitBackward : 4) k_sw
 }
 
 // Blocks for all units, at most four times what fits (the kernels stride over what is left).
-unsigned blocks_for(long long rows, int cols, int fit, bool vec) {
-    const int width = vec ? Walk<true>::kWidth : Walk<false>::kWidth;
+unsigned blocks_for(long long rows, int cols, int fit) {
+    constexpr int width = Walk::kWidth;
     const long long units = rows * ((cols + width - 1) / width);
     const long long b = (units + kThreads / 32 - 1) / (kThreads / 32);
     return (unsigned)(b < 4 * fit * kSms ? b : 4 * fit * kSms);
@@ -204,7 +204,7 @@ unsigned blocks_for(long long rows, int cols, int fit, bool vec) {
 
 template <typename Args>
 cudaError_t launch(void (*const (&k)[4])(Args), const Args& a, int fit, bool bf16, bool vec, cudaStream_t s) {
-    return launch_pdl(k[(bf16 ? 2 : 0) + (vec ? 1 : 0)], dim3(blocks_for(a.rows, a.cols, fit, vec)), dim3(kThreads), 0,
+    return launch_pdl(k[(bf16 ? 2 : 0) + (vec ? 1 : 0)], dim3(blocks_for(a.rows, a.cols, fit)), dim3(kThreads), 0,
                       s, a);
 }
 

@@ -313,11 +313,7 @@ __global__ void __launch_bounds__(kMaxThreads, S == 1 ? 2 : 1) k_rmsnorm_backwar
 #pragma unroll
     for (int k = 0; k < S; ++k) {
         const int c0 = (warp + k * warps) * kSeg;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = c0 + seg_col<VEC>(lane, j);
-            if (c < a.cols) out[c] = dw[k][j];
-        }
+        if (c0 < a.cols) seg_store<false, VEC ? kShifted : kByValue>(out, c0, a.cols, lane, dw[k]);
     }
 }
 
