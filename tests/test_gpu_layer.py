@@ -109,6 +109,32 @@ def test_pack_and_unpack_are_exact(mu, fmt, dtype, rows, cols, pad):
         assert np.array_equal(f64(y), L.unpack(q, s, fmt))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("offset", range(8))
+@pytest.mark.parametrize("pitch", [1, 4, 7, 8])
+def test_rows_at_every_offset(mu, dtype, offset, pitch):
+    """Rows that begin anywhere within 16 bytes: the same codes and values as aligned rows, nothing beside them touched."""
+    import torch
+    rows = 6
+    for cols in (1, 7, 8, 9, 31, 250, 255, 256, 257, 263, 505, 511, 512, 513, 1021):
+        ld = -(-cols // 8) * 8 + pitch
+        wide = rand((rows + 1, ld), dtype, 100 + cols)
+        flat = wide.flatten()
+        x = flat[offset:offset + rows * ld].view(rows, ld)[:, :cols]
+        whole = torch.zeros(rows, -(-cols // 8) * 8, dtype=dt(dtype), device="cuda")
+        whole[:, :cols] = x
+        got, want = mu.Act8.empty(rows, cols, "e4m3"), mu.Act8.empty(rows, cols, "e4m3")
+        mu.act_pack(x, got)
+        mu.act_pack(whole[:, :cols], want)
+        assert all(np.array_equal(g, w) for g, w in zip(held(got), held(want)))
+        expect = torch.full_like(flat, 77.0)
+        y = expect.clone()
+        mu.act_unpack(want, whole[:, :cols])
+        expect[offset:offset + rows * ld].view(rows, ld)[:, :cols] = whole[:, :cols]
+        mu.act_unpack(want, y[offset:offset + rows * ld].view(rows, ld)[:, :cols])
+        assert torch.equal(y, expect)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("aligned", [True, False])
 def test_pack_over_the_whole_range(mu, fmt, aligned):
