@@ -56,6 +56,7 @@ __device__ __forceinline__ void unit_act_pack(const PackArgs& a, const Walk& w, 
     for (int k = 0; k < kUnroll; ++k) raw[k].template load<FULL>(x, w.col + k * kSeg, a.cols, lane);
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
+        if (!FULL && w.col + k * kSeg >= a.cols) break;
         float v[8];
         raw[k].get(v);
         seg_quant<true, FULL>(a.q, w.row, w.col + k * kSeg, a.cols, lane, v);
@@ -82,6 +83,7 @@ __device__ __forceinline__ void unit_act_unpack(const PackArgs& a, const Walk& w
     for (int k = 0; k < kUnroll; ++k) raw[k].template load<FULL>(a.q, w.row, w.col + k * kSeg, a.cols, lane);
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
+        if (!FULL && w.col + k * kSeg >= a.cols) break;
         float v[8];
         raw[k].get(a.q.format, v);
         seg_store<BF16, kMode<VEC>, FULL>(y, w.col + k * kSeg, a.cols, lane, v);
@@ -126,6 +128,7 @@ __device__ __forceinline__ void unit_swiglu_forward(const SwigluArgs& a, const W
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
         const int c0 = w.col + k * kSeg;
+        if (!FULL && c0 >= a.cols) break;
         float g[8], u[8], o[8];
         gr[k].get(g);
         ur[k].get(u);
@@ -164,6 +167,7 @@ __device__ __forceinline__ void unit_swiglu_backward(const SwigluArgs& a, const 
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
         const int c0 = w.col + k * kSeg;
+        if (!FULL && c0 >= a.cols) break;
         float g[8], u[8], d[8], o[8];
         dr[k].get(d);
         gr[k].get(a.gate8.format, g);
