@@ -589,8 +589,9 @@ muon_status muon_rmsnorm_backward(muon_grad_plan p, const void* dy, int64_t lddy
  *              when x holds the unweighted norm).
  *   grad       dense row-major, grad_dtype (MUON_BF16 or MUON_F32, the plan's of
  *              muon_step), overwritten, or added to when accumulate is nonzero.
- * Operands are bf16 (exact for the 8-bit x), products and sums fp32.  The sums' order depends on
- * the sizes alone: the same inputs give the same bits.  1 <= m, n <= 2^20,
+ * Operands are bf16 (exact for the 8-bit x), products and sums fp32, those of at most 2048
+ * tokens in one accumulator of the tensor cores, whose additions truncate.  The sums' order
+ * depends on the sizes alone: the same inputs give the same bits.  1 <= m, n <= 2^20,
  * 0 <= tokens < 2^31.
  */
 muon_status muon_wgrad(muon_grad_plan p, const void* dy, int64_t lddy, const muon_act8* x, int64_t tokens, int64_t m,

@@ -77,10 +77,11 @@ struct WgradArgs {
     void* grad;
     int accumulate;
     int* status;
-    float* partial;      // kMaxParts tiles of 256 x 256 sums
+    float* partial;      // kMaxParts + kMaxPairs tiles of 256 x 256 sums
     int* counters;       // kMaxParts * 4 words, zero between calls
 };
-constexpr int kMaxParts = 240;
+constexpr int kMaxParts = 240;   // parts of split tiles
+constexpr int kMaxPairs = 76;    // CTA pairs, one tile of bf16 gradients' running sums each
 
 // bf16: the dtype of the Mat operands; vec: every one of them (and ld) 16-byte aligned.
 cudaError_t launch_act_pack(const PackArgs& a, bool bf16, bool vec, cudaStream_t s);
@@ -92,7 +93,7 @@ cudaError_t rmsnorm_prepare();   // once per device, before the first backward l
 // Blocks of the backward kernel for these sizes (its partial sums: blocks x cols floats).
 int rmsnorm_backward_blocks(long long rows, int cols, int sm_count);
 constexpr long long kNormPartialFloats = 8ll << 20;   // bound on blocks x cols
-constexpr long long kPartialFloats = kMaxParts * 65536ll;   // of a grad plan, for either reduction
+constexpr long long kPartialFloats = (kMaxParts + kMaxPairs) * 65536ll;   // of a grad plan, for either reduction
 static_assert(kPartialFloats >= kNormPartialFloats, "one region serves both");
 cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a, bool bf16, bool vec, int sm_count, cudaStream_t s);
 cudaError_t wgrad_prepare();   // once per device, before the first launch

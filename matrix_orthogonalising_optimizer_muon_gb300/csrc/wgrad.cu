@@ -57,6 +57,13 @@ struct Roles {
     static constexpr int kThreads = 32 * (kEpiFirst + kWgEpiWarps);
     static_assert(kRows % 8 == 0, "whole passes");
 };
+// Tokens that one accumulator takes.  The tensor cores' adds truncate, so its sum drifts in proportion to
+// them: by 1.1e-5 of itself over 16384 tokens of random data, by 1.3 % over 2^21 tokens of one sign.  The
+// epilogue adds up the chains' sums in fp32 instead: fp32 gradients in place, bf16 ones in the workspace.
+// That leaves 8.4e-7 (an fp32 product on the CUDA cores: 6.9e-7) and costs an fp32 gradient 7 % (16384 x
+// 18944 x 3584: 1437 -> 1541 us; chains of 4096 tokens: 2e-6, 1470 us), a bf16 one 5 to 8 % (there
+// 1258 -> 1312 us, 8192 x 3584 x 3584 144 -> 156).
+constexpr uint32_t kChain = 2048;
 constexpr int kBandM = 8;               // tiles along m whose columns of dy are in flight together
 constexpr int kSortGroups = 256;        // experts that are dealt out by their number of tokens
 constexpr int kTurnTable = 96;          // turns decoded at the start
@@ -105,7 +112,6 @@ struct WgradLaunch {
     Divisor tiles, band, wide_band, last_band, part;   // by tiles of a weight, of a band, bands' widths, parts
     int units;                     // whole tiles of all groups, then parts of split tiles
     int whole, parts;              // units below `whole` are tiles, the others one of `parts` of a tile
-    int chain_log;                 // log2 of the tokens one accumulator takes
     int wide;                      // rows of grad are aligned to four elements
     int sectors;                   // rows of a bf16 grad are aligned to 32 bytes
 };
@@ -254,6 +260,25 @@ __device__ __forceinline__ void part_load(const float* p, float (&f)[32]) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[4 * i + j] = __ldcg(p + (4 * i + j) * 256);
         }
+}
+// The same, added to f: 16 at a time, which the epilogue of copied dy has registers for.
+template <bool WIDE>
+__device__ __forceinline__ void part_add(const float* p, float (&f)[32]) {
+#pragma unroll
+    for (int h = 0; h < 8; h += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float* q = p + (h + i) * 1024;
+            x[i] = WIDE ? __ldcg(reinterpret_cast<const float4*>(q))
+                        : make_float4(__ldcg(q), __ldcg(q + 256), __ldcg(q + 512), __ldcg(q + 768));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float* v = f + 4 * (h + i);
+            v[0] += x[i].x, v[1] += x[i].y, v[2] += x[i].z, v[3] += x[i].w;
+        }
+    }
 }
 template <bool WIDE>
 __device__ __forceinline__ void part_store(float* p, const float (&f)[32], bool more) {
@@ -494,7 +519,7 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
     bool ok = true;
     for (int turn = 0; ok && turn < e.turns.count; ++turn) {
         const Unit w = e.turns.get(L, e.ex, e.table, turn);
-        const int chains = (int)(((uint32_t)(w.end - w.begin) + (1u << L.chain_log) - 1) >> L.chain_log);
+        const int chains = (int)(((uint32_t)(w.end - w.begin) + kChain - 1) / kChain);
         const int r0 = w.m0 + 128 * e.q + 32 * e.wq;
         if (chains == 0) {   // an expert without tokens
             const OutTile<BF16, WIDE> out(L, w, r0, e.lane);
@@ -504,11 +529,14 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
             }
             continue;
         }
-        // a part's sums go to the workspace, this warp's 32 x 256 of them as row-major rows
+        // a part's sums go to the workspace, this warp's 32 x 256 of them as row-major rows; so do those of
+        // a bf16 tile until its last chain, to the pair's own tile there, which each warp uses again
+        const long long mine = 4 * e.q + e.wq, at = WIDE ? rl * 256 + cl : e.lane;
         float* part = nullptr;
-        if (w.part >= 0)
-            part = L.a.partial + (((w.tile - L.whole) * 8ll + 4 * e.q + e.wq) * L.parts) * 8192 +
-                   (WIDE ? rl * 256 + cl : e.lane);
+        if (w.part >= 0) part = L.a.partial + ((w.tile - L.whole) * 8ll + mine) * L.parts * 8192 + at;
+        float* run = nullptr;
+        if (BF16 && part == nullptr && chains > 1)
+            run = L.a.partial + ((kMaxParts + e.turns.pair) * 8ll + mine) * 8192 + at;
         for (int ch = 0; ch < chains; ++ch) {
             const uint32_t acc = local & 1;
             if (!mbar_wait_idle(e.tfull + acc, local >> 1 & 1u, e.abort_flag, L.a.status, kStatusTimeoutEpilogue,
@@ -518,7 +546,7 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
             }
             tc_fence_after();
             const uint32_t tbase = e.tmem_base + acc * 256 + (static_cast<uint32_t>(e.wq * 32) << 16);
-            if (BF16 && WIDE && DIRECT && L.sectors && part == nullptr && !L.a.accumulate && ch == 0 && w.n0 + 256 <= L.a.n &&
+            if (BF16 && WIDE && DIRECT && L.sectors && part == nullptr && run == nullptr && !L.a.accumulate && w.n0 + 256 <= L.a.n &&
                 r0 + 32 <= L.a.m) {
                 store_rows(L, w, e, tbase, acc);
                 ++local;
@@ -547,11 +575,12 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
                     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(lds32(e.blk + i * WgCfg::OUT_LD + e.lane * 4));
                 }
                 __syncwarp();
-                if (part == nullptr) {
-                    out.put(f, c0, ch > 0);   // a later chain of tokens adds to what this warp wrote
-                } else {
-                    part_store<WIDE>(part + w.part * 8192 + c0, f, ch > 0);
-                }
+                if (run != nullptr && ch == chains - 1) part_add<WIDE>(run + c0, f);   // this thread's own sums
+                float* to = part != nullptr ? part + w.part * 8192 : ch < chains - 1 ? run : nullptr;
+                if (to != nullptr)
+                    part_store<WIDE>(to + c0, f, ch > 0);
+                else
+                    out.put(f, c0, !BF16 && ch > 0);   // a later chain of tokens adds to what this warp wrote
             }
             ++local;
         }
@@ -746,7 +775,7 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
             const uint64_t bd0 = sdesc_sw128(smem_u32(smem) + Cfg::A_BYTES, Cfg::CHUNK_BYTES, 1024);
             for (int turn = 0; ok && turn < turns.count; ++turn) {
                 const Unit w = turns.get(L, ex, table, turn);
-                const int steps = unit_steps(w), chain = 1 << (L.chain_log - 6);
+                const int steps = unit_steps(w), chain = kChain / kWgStepT;
                 const int last = ((w.end - w.begin - 1) & (kWgStepT - 1)) / 16 + 1;   // MMAs of the last step
                 for (int k0 = 0; ok && k0 < steps; k0 += chain, ++local) {
                     const uint32_t acc = local & 1;
@@ -956,7 +985,7 @@ cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaS
     L.tiles_n = (a.n + 255) / 256;
     const long long units = (long long)a.groups * L.tiles_m * L.tiles_n;
     if (units >= (1ll << 31)) return cudaErrorInvalidValue;
-    const int pairs = sm_count / 2;
+    const int pairs = std::min(sm_count / 2, kMaxPairs);
     L.whole = (int)units;
     L.parts = 1;
     if (!a.offsets) {
@@ -978,12 +1007,6 @@ cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaS
     L.wide_band.set(kBandM);
     L.last_band.set(std::max(L.tiles_m % kBandM, 1));
     L.part.set(L.parts);
-    // The tensor cores' adds truncate: the sum in one accumulator drifts in proportion to the
-    // number of tokens, by 1.1e-5 of itself over 16384 tokens of random data.  An fp32 gradient
-    // adds up partial sums of 2048 tokens in the epilogue instead, which leaves 8.4e-7 (an fp32
-    // product on the CUDA cores: 6.9e-7) and costs 7 % (16384 x 18944 x 3584: 1437 -> 1541 us;
-    // 4096 tokens: 2e-6, 1470 us).  A bf16 gradient's own rounding, 1.7e-3, hides the drift.
-    L.chain_log = bf16_grad ? 30 : 11;
     L.wide = a.n % 4 == 0 && (reinterpret_cast<uintptr_t>(a.grad) & (bf16_grad ? 7 : 15)) == 0;
     L.sectors = bf16_grad && a.n % 16 == 0 && (reinterpret_cast<uintptr_t>(a.grad) & 31) == 0;
     // TMA needs 16-byte aligned rows; x has them by its format
