@@ -3,8 +3,8 @@
 // All four kernels read and write each value once (HBM-bound).  A warp takes units of kUnroll
 // neighbouring segments of 256 values of a row, all loads before the first store.  HBM bounds
 // them once units that lie inside the row skip the per-lane masks (with masks the loads wait on one
-// another's branches: forward 207 us, backward 278).  Measured at 8192 x 18944 bf16: forward 202 us
-// (6.2 TB/s, 93 % of the measured copy rate), backward 219 us (6.4 TB/s, 96 %), pack 69 us (102 %),
+// another's branches: forward 207 us, backward 278).  Measured at 8192 x 18944 bf16: forward 200 us
+// (6.25 TB/s, 94 % of the measured copy rate), backward 226 us (6.25 TB/s, 94 %), pack 69 us (102 %),
 // unpack 71 us (99 %).  Rows that are not aligned are loaded and stored in shifted
 // pieces, bound by instruction issue (18945 columns: 295, 337, 85 and 96 us).
 #include "act8.cuh"
@@ -102,18 +102,37 @@ __global__ void __launch_bounds__(kThreads, VEC ? kFit : 6) k_act_unpack(const P
     }
 }
 
-// 1 / (1 + e^-z).  e^-z = 2^t 2^d with t = -z log2 e rounded and d, what the rounding left, by the
-// first term of its series: a relative error of about 3 ulp in the exponential and 1 in the
-// reciprocal (expf and a division: 217 us forward, 304 backward).  Zero below -87.3, where it leaves
-// the normal range (so that -infinity times it is a NaN, as in z / (1 + e^-z)).
-__device__ __forceinline__ float sigmoid(float z) {
-    const float c = fminf(z, 80.f);
-    const float t = c * -1.44269504f, d = fmaf(c, -1.44269504f, -t);
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+// e^x for |x| <= 88; SCALED, for -110 <= x <= -80, as 2^64 e^x times 2^-64, so that a result below the normal
+// range is rounded once.  e^x = 2^t 2^d with t = x log2 e rounded and 2^d by the first two terms of its
+// series: d is what the product's rounding left (an fma gives it exactly, as in Dekker, "A floating-point
+// technique for extending the available precision") and x times the rest of log2 e beyond one float, which
+// alone is 11 ulp at 87.  Within 5 u, u = 2^-24, by the documented error of the base-2 exponential (expf
+// and a division: 217 us forward, 304 backward).
+template <bool SCALED>
+__device__ __forceinline__ float exponential(float x) {
+    constexpr double log2e = 1.4426950408889634;
+    constexpr float hi = (float)log2e, lo = (float)(log2e - hi);
+    const float t = x * hi, d = fmaf(x, lo, fmaf(x, hi, -t));
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(SCALED ? t + 64.f : t));   // t + 64: exact
     e = fmaf(e, d * 0.693147181f, e);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return z < -87.3f ? 0.f : r;
+    return SCALED ? e * 5.42101086e-20f : e;
+}
+// 1 / (1 + e^-z), within 10 u for z >= -80.  Below, where the reciprocal would leave the normal range,
+// e^z itself, for which the eight values of a lane are looked over once (a choice for each of them: forward
+// 209 us, backward 231, against 200 and 226).
+__device__ __forceinline__ void sigmoid(const float (&z)[8], float (&s)[8]) {
+    const float least = fminf(fminf(fminf(z[0], z[1]), fminf(z[2], z[3])), fminf(fminf(z[4], z[5]), fminf(z[6], z[7])));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float e = exponential<false>(-fminf(z[j], 80.f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[j]) : "f"(1.f + e));
+    }
+    if (least < -80.f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (z[j] < -80.f) s[j] = exponential<true>(fmaxf(z[j], -110.f));
+    }
 }
 
 template <bool BF16, bool VEC, bool FULL>
@@ -132,8 +151,9 @@ __device__ __forceinline__ void unit_swiglu_forward(const SwigluArgs& a, const W
         float g[8], u[8], o[8];
         gr[k].get(g);
         ur[k].get(u);
+        sigmoid(g, o);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid(g[j]) * u[j];
+        for (int j = 0; j < 8; ++j) o[j] = g[j] * o[j] * u[j];
         if (a.a.p) seg_store<BF16, kMode<VEC>, FULL>(row_ptr(a.a, w.row), c0, a.cols, lane, o);
         if (a.gate8.codes) seg_quant<true, FULL>(a.gate8, w.row, c0, a.cols, lane, g);
         if (a.up8.codes) seg_quant<true, FULL>(a.up8, w.row, c0, a.cols, lane, u);
@@ -172,9 +192,10 @@ __device__ __forceinline__ void unit_swiglu_backward(const SwigluArgs& a, const 
         dr[k].get(d);
         gr[k].get(a.gate8.format, g);
         ur[k].get(a.up8.format, u);
+        sigmoid(g, o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float s = sigmoid(g[j]);
+            const float s = o[j];
             const float silu = g[j] * s;
             o[j] = silu * u[j];
             g[j] = d[j] * u[j] * (s + silu * (1.f - s));   // dgate

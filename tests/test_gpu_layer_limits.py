@@ -37,3 +37,51 @@ def test_wgrad_of_many_tokens_does_not_drift(mu, plan, dtype, expert, n):
     plan.sync()
     want = want.cpu().numpy()
     close(g, want + g0, (2 * (2048 + 8) + t // 2048 + 4) * U * want)
+
+
+# ------------------------------------------------------------------ SwiGLU
+def silu_bound(g, u):
+    """|error| of silu(g) u: the exponential 2 ulp and its correction's rounding (5 u), 1 + e (u), the reciprocal
+    2^-23 on [1, 2) (4 u), two products (2 u)."""
+    return 12 * U * (g * L.sigmoid(g) * u).__abs__()
+
+
+def test_silu_over_all_gates(mu):
+    """Gates evenly over [-87, 87], so the sigmoid from 1.6e-38 to 1."""
+    import torch
+    g = torch.linspace(-87, 87, 64 * 1024, device="cuda").view(64, 1024)
+    u = torch.ones_like(g)
+    a = torch.empty_like(g)
+    mu.swiglu_forward(g, u, a)
+    close(a, L.swiglu(f64(g), f64(u)), silu_bound(f64(g), f64(u)))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_silu_gradient_over_all_gates(mu, fmt):
+    import torch
+    g = torch.linspace(-87, 87, 64 * 1024, device="cuda").view(64, 1024)
+    u, d = rand((64, 1024), "f32", 1), rand((64, 1024), "f32", 2)
+    g8, u8, dg, du = filled(mu, g, fmt), filled(mu, u, fmt), torch.empty_like(d), torch.empty_like(d)
+    mu.swiglu_backward(d, g8, u8, dg, du)
+    g, u, d = values(g8), values(u8), f64(d)
+    s = L.sigmoid(g)
+    wg, wu = L.swiglu_grad(d, g, u)
+    # s (10 u), silu (11 u), 1 - s (10 u of s), their product, sum and the two products with da and up
+    close(dg, wg, 16 * U * np.abs(d * u) * s * np.where(g < 0, 1 - g * (1 - s), 1 + g) + 1e-44)
+    close(du, wu, 12 * U * np.abs(wu) + 1e-44)
+
+
+def test_silu_of_gates_that_are_not_finite(mu):
+    import torch
+    inf, nan = float("inf"), float("nan")
+    g = torch.tensor([[inf, -inf, nan, 0.0, 1.0, 2.0, -200.0, 200.0]], device="cuda")
+    u = torch.tensor([[2.0, 2.0, 2.0, inf, inf, nan, 2.0, 2.0]], device="cuda")
+    with np.errstate(all="ignore"):
+        want = f64(g) / (1 + np.exp(-f64(g))) * f64(u)
+    for dtype in ("f32", "bf16"):
+        a, g8 = torch.empty_like(g, dtype=dt(dtype)), mu.Act8.empty(1, 8)
+        mu.swiglu_forward(g.to(dt(dtype)), u.to(dt(dtype)), a, saved_gate=g8)
+        close(a.float(), want, np.full(8, 1e-30))
+        d, dg, du = torch.ones_like(a), torch.empty_like(a), torch.empty_like(a)
+        mu.swiglu_backward(d, g8, filled(mu, torch.ones_like(u), "e4m3"), dg, du)
+        assert dg.isnan().all() and du.isnan().all()     # the group of eight reads back as NaN
