@@ -478,13 +478,15 @@ typedef enum { MUON_ACT_E4M3 = 0, MUON_ACT_INT8 = 1 } muon_act_format;
  *           32 g .. 32 g + 31 and stands for 2^(byte - 127); 255 marks a group that
  *           held an infinity or a NaN: its codes are 0 and it reads back as NaN.
  * value = code * 2^(byte - 127).  Both pointers and both pitches are multiples of 16,
- * ldq >= cols, lds >= ceil(cols / 32); bytes that pad a row may be overwritten and are
- * never used.  The e4m3 codes 0x7f and 0xff (NaN), the whole number -128 and scale bytes outside 17 .. 248
- * and 255 are never written; what a reader makes of them is unspecified.  Every writer picks the smallest 2^e that brings the group's largest
- * magnitude within the codes' range (448 or 127), with -110 <= e <= 119 (e4m3) or
- * 121 (int8), and rounds value / 2^e to the nearest code, ties to even, saturating at
- * the largest.  Within that range of e every value is exact in bf16 (at most 8
- * significant bits, a normal number): readers lose nothing to bf16 operands.
+ * ldq >= cols, lds >= ceil(cols / 32); bytes that pad a row are not written, and readers
+ * fetch but never use them: the last row may end with its values in a longer buffer.  The
+ * e4m3 codes 0x7f and 0xff (NaN), the whole number -128 and scale bytes outside 17 .. 248
+ * and 255 are never written; what a reader makes of them is unspecified.  Every writer
+ * picks the smallest 2^e that brings the group's largest magnitude within the codes' range
+ * (448 or 127), with -110 <= e <= 119 (e4m3) or 121 (int8), and rounds value / 2^e to the
+ * nearest code, ties to even, saturating at the largest.  Within that range of e every
+ * value is exact in bf16 (at most 8 significant bits, a normal number): readers lose
+ * nothing to bf16 operands.
  */
 typedef struct {
     void* codes;

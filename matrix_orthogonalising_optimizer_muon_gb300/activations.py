@@ -49,7 +49,7 @@ class Act8:
                             _FORMATS[fmt], 0)
 
     @staticmethod
-    def _pitch(t):
+    def _pitch(t):   # of a single row: one that the library accepts, nothing goes by it
         return t.stride(0) if t.shape[0] > 1 else _pad16(t.shape[1])
 
     @classmethod

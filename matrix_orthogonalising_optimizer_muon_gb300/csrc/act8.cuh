@@ -278,11 +278,15 @@ __device__ __forceinline__ void seg_quant(const Act8& q, uint32_t row, int c0, i
         uint32_t lo = act_code2<FMT>(v[0] * inv, v[1] * inv) | act_code2<FMT>(v[2] * inv, v[3] * inv) << 16;
         uint32_t hi = act_code2<FMT>(v[4] * inv, v[5] * inv) | act_code2<FMT>(v[6] * inv, v[7] * inv) << 16;
         if (byte == 255u) lo = hi = 0;   // a group that is not finite
-        // row pitches are multiples of 16: the eight bytes lie within the row's padding
-        if (FULL || c0 + 8 * lane < cols) {
+        const int left = cols - c0 - 8 * lane;
+        if (FULL || left >= 8) {
             *reinterpret_cast<uint2*>(codes + 8 * lane) = make_uint2(lo, hi);
-            if ((lane & 3) == 0) scales[lane >> 2] = (uint8_t)byte;
+        } else {   // the row's end: what follows may be another's
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (j < left) codes[8 * lane + j] = (uint8_t)((j < 4 ? lo : hi) >> 8 * (j & 3));
         }
+        if ((FULL || left > 0) && (lane & 3) == 0) scales[lane >> 2] = (uint8_t)byte;
     } else {
         uint32_t mine = 0;
 #pragma unroll

@@ -4,7 +4,7 @@
 // neighbouring segments of 256 values of a row, all loads before the first store.  HBM bounds
 // them once units that lie inside the row skip the per-lane masks (with masks the loads wait on one
 // another's branches: forward 207 us, backward 278).  Measured at 8192 x 18944 bf16: forward 200 us
-// (6.25 TB/s, 94 % of the measured copy rate), backward 226 us (6.25 TB/s, 94 %), pack 69 us (102 %),
+// (6.25 TB/s, 94 % of the measured copy rate), backward 225 us (6.3 TB/s, 94 %), pack 69 us (102 %),
 // unpack 71 us (99 %).  Rows that are not aligned are loaded and stored in shifted
 // pieces, bound by instruction issue (18945 columns: 295, 337, 85 and 96 us).
 #include "act8.cuh"

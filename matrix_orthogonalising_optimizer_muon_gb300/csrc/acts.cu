@@ -107,7 +107,7 @@ struct Call {
         if (!ok) return;
         *q = Act8{static_cast<uint8_t*>(a->codes), static_cast<uint8_t*>(a->scales), (uint32_t)a->ldq, (uint32_t)a->lds,
                   a->format};
-        // the padding belongs to the tensor: writers may touch it
+        // whole 16-byte pieces, as readers fetch them
         ops.add(a->codes, rows, round_up(cols, 16), a->ldq, output);
         ops.add(a->scales, rows, round_up((cols + kActGroup - 1) / kActGroup, 16), a->lds, output);
     }

@@ -85,3 +85,39 @@ def test_silu_of_gates_that_are_not_finite(mu):
         d, dg, du = torch.ones_like(a), torch.empty_like(a), torch.empty_like(a)
         mu.swiglu_backward(d, g8, filled(mu, torch.ones_like(u), "e4m3"), dg, du)
         assert dg.isnan().all() and du.isnan().all()     # the group of eight reads back as NaN
+
+
+# ------------------------------------------------------------------ rows of an Act8 inside a longer buffer
+@pytest.mark.parametrize("cols", [1001, 1007, 9, 33])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_writers_keep_to_the_row(mu, cols, dtype):
+    """Codes and scales that are views into a longer buffer: what lies beside them stays as it was."""
+    import torch
+    x = rand((1, cols), dtype, 1, 2.0)
+    groups = (cols + 31) // 32
+
+    def view():
+        buf = torch.full((2, 4096), 0xA5, dtype=torch.uint8, device="cuda")
+        return buf, mu.Act8(buf[:1, :cols], buf[1:, :groups], cols, "int8")
+
+    def check(buf, want):
+        assert torch.equal(buf[0, :cols], want.codes[0, :cols]) and torch.equal(buf[1, :groups], want.scales[0, :groups])
+        assert bool((buf[0, cols:] == 0xA5).all()) and bool((buf[1, groups:] == 0xA5).all())
+
+    want = filled(mu, x, "int8")
+    buf, a = view()
+    mu.act_pack(x, a)
+    check(buf, want)
+    buf, a = view()
+    mu.swiglu_forward(x, x, saved_gate=a)
+    check(buf, want)
+    buf, a = view()
+    w, y = torch.ones(cols, device="cuda"), mu.Act8.empty(1, cols, "int8")
+    mu.rmsnorm_forward(x, w, 1e-6, saved=y)
+    mu.rmsnorm_forward(x, w, 1e-6, saved=a)
+    check(buf, y)
+    buf, a = view()
+    d, dg, du = torch.ones_like(x), torch.empty_like(x), torch.empty_like(x)
+    mu.swiglu_backward(d, want, want, dg, du, saved_out=y)
+    mu.swiglu_backward(d, want, want, dg, du, saved_out=a)
+    check(buf, y)
