@@ -43,6 +43,8 @@ class Act8:
                                  % (name, need, t.dtype, tuple(t.shape)))
         if codes.shape[0] != scales.shape[0]:
             raise ValueError("codes and scales differ in rows: %d and %d" % (codes.shape[0], scales.shape[0]))
+        if codes.get_device() != scales.get_device():
+            raise ValueError("codes and scales differ in device: %s and %s" % (codes.device, scales.device))
         self.codes, self.scales, self.rows, self.cols, self.fmt = codes, scales, codes.shape[0], cols, fmt
         self.device = codes.get_device()
         self.ref = MuonAct8(codes.data_ptr(), scales.data_ptr(), self._pitch(codes), self._pitch(scales),
