@@ -69,19 +69,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// One test of the phase, without suspending the thread.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Waits for the phase of parity `parity` of `bar` to complete.  Gives up when
 // `*abort` becomes nonzero or after kWaitTimeoutNs; on a timeout it raises
 // `*abort` and records `code` in the global status word.  Returns true on
@@ -279,15 +266,33 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_saddr) {
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_saddr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr) : "memory");
 }
-// The same with release at CTA scope.
-__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_saddr) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_saddr) : "memory");
+// Copies 16 bytes of this CTA's shared memory to another CTA's (both 16-byte aligned; shared::cluster
+// addresses of destination and barrier), counted on its barrier.  As an arrival: writes of this CTA that
+// are in the async proxy (fence.proxy.async) before the copy is issued precede it, and its completion is a
+// release at cluster scope, which no thread has to wait for.
+__device__ __forceinline__ void bulk_signal(uint32_t dst_cluster_saddr, const void* src, uint32_t bar_cluster_saddr) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(
+                     dst_cluster_saddr),
+                 "r"(smem_u32(src)), "r"(bar_cluster_saddr)
+                 : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// One test of the phase with cluster-scope acquire, without suspending the thread.
+__device__ __forceinline__ bool mbar_test_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}\n"
         : "=r"(ok)
         : "r"(smem_u32(bar)), "r"(parity)

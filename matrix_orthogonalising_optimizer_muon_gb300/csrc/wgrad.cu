@@ -15,8 +15,8 @@
 //   3-10   conversion of x into a 16 KB bf16 operand per step, four steps at a time
 //   11-14  epilogue: column scale, addition to grad, stores
 // Two rings: x as it arrives (full_r by TMA, empty_r by the conversion), and the operands (dy
-// and converted x; ready, on the even CTA, by both CTAs' conversion warps and dy's TMA bytes,
-// empty, on both, by the MMAs), so the MMA warp has one wait and one commit per step.
+// and converted x; ready, on the even CTA, by both CTAs' conversion warps, the odd one's through copies
+// of 16 bytes, and dy's TMA bytes, empty, on both, by the MMAs), so the MMA warp has one wait and one commit per step.
 //
 // What bounds it: shared memory.  A step moves 82 KB through each SM's 128 bytes a cycle (MMA
 // operands 32 KB, dy in 16 KB, codes in and out 18 KB, converted x 16 KB), 640 cycles where its
@@ -82,7 +82,8 @@ struct WgCfg {
     static constexpr int OUT_LD = 144;                      // row of a 32 x 32 block of floats, padded by 16 bytes
     static constexpr int OUT_WARP = 32 * OUT_LD;
     static constexpr int BAR_OFFSET = OUT_OFFSET + kWgEpiWarps * OUT_WARP;
-    static constexpr int EXPERTS_OFFSET = BAR_OFFSET + 512;
+    static constexpr int SIGNAL_OFFSET = BAR_OFFSET + 512;   // 16 bytes per conversion warp
+    static constexpr int EXPERTS_OFFSET = SIGNAL_OFFSET + 256;
     static constexpr int TABLE_OFFSET = EXPERTS_OFFSET + kSortGroups * 10;
     static constexpr int SMEM_BYTES = TABLE_OFFSET + kTurnTable * 32 + 1024;
 };
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
             mbar_init(empty_r + s, kGroupWarps);
         }
         for (int s = 0; s < kRingM; ++s) {
-            mbar_init(ready + s, 1 + 2 * kGroupWarps);
+            mbar_init(ready + s, 1 + kGroupWarps);
             mbar_init(empty + s, 1);
             mbar_init(tail + s, 1);
         }
@@ -743,19 +744,14 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
                             tma_load_2d(sa, &L.map_y, tail + slot, ym, t0);
                             tma_load_2d(sa + Cfg::CHUNK_BYTES, &L.map_y, tail + slot, ym + 64, t0);
                         }
-                        if (leader) mbar_arrive(ready + slot);
+                        if (leader) mbar_arrive_expect_tx(ready + slot, 16 * kGroupWarps);
                     } else {
                         const uint32_t fb = mapa_shared(smem_u32(ready + slot), 0);
-                        if (leader) mbar_arrive_expect_tx(ready + slot, 2 * Cfg::A_BYTES);
+                        if (leader) mbar_arrive_expect_tx(ready + slot, 2 * Cfg::A_BYTES + 16 * kGroupWarps);
                         tma_load_2d_pair(sa, &L.map_y, fb, ym, t0);
                         tma_load_2d_pair(sa + Cfg::CHUNK_BYTES, &L.map_y, fb, ym + 64, t0);
                     }
                     if (++slot == kRingM) slot = 0, ph ^= 1u;
-                }
-            }
-            if (!ok) {   // copies already issued signal the even CTA; give them time to land
-                const unsigned long long t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 2000000ull) {
                 }
             }
         }
@@ -789,7 +785,8 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
                     const int k1 = min(steps, k0 + chain);
                     const int whole = k1 == steps && last < 4 ? k1 - 1 : k1;
                     for (int k = k0; k < k1; ++k) {
-                        if (!next && !mbar_wait(ready + slot, ph, abort_flag, L.a.status, kStatusTimeoutMma)) {
+                        if (!next && !mbar_wait_cluster(ready + slot, ph, abort_flag, L.a.status,
+                                                        kStatusTimeoutMma)) {
                             ok = false;
                             break;
                         }
@@ -803,7 +800,7 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
                                 mma_f16kind_pair(d, ad + kStep, bd + kStep, idesc, 1);
                                 mma_f16kind_pair(d, ad + 2 * kStep, bd + 2 * kStep, idesc, 1);
                             }
-                            next = mbar_test_wait(ready + slot, ph);
+                            next = mbar_test_wait_cluster(ready + slot, ph);
                             if (one) {
                                 mma_f16kind_pair(d, ad + 3 * kStep, bd + 3 * kStep, idesc, 1);
                                 mma_commit_pair(done, 0x3);
@@ -906,14 +903,15 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(empty_r + r);
-                    // Release at CTA scope on either barrier: the MMAs read this warp's writes in its own
-                    // CTA's shared memory, where the fence above has put them.  A release at cluster scope
-                    // waits about 1000 cycles for the warp's other traffic (370 against 260 us at
-                    // 8192 tokens, 3584 x 3584).
+                    // The even CTA's MMAs read the odd CTA's operand too, so its arrival is a copy of 16
+                    // bytes whose completion releases at cluster scope.  A thread that releases at that
+                    // scope waits about 1800 cycles (238 against 156 us at 8192 tokens, 3584 x 3584; 369
+                    // with one warp that passes the odd CTA's steps on).
                     if (leader)
                         mbar_arrive(ready + b);
-                    else
-                        mbar_arrive_remote_cta(ready_lead + b * 8);
+                    else   // from and to this warp's 16 bytes, which mean nothing
+                        bulk_signal(ready_lead + Cfg::SIGNAL_OFFSET - Cfg::BAR_OFFSET - 16 * kRingR + 16 * (warp - kConvFirst),
+                                    smem + Cfg::SIGNAL_OFFSET + 16 * (warp - kConvFirst), ready_lead + b * 8);
                 }
             }
         }
@@ -932,6 +930,11 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
             epilogue<BF16, false, TMA_Y>(L, e);
     }
 
+    if (*abort_flag) {   // copies already issued signal the even CTA; give them time to land
+        const unsigned long long t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+    }
     tc_fence_before();
     cluster_sync();   // every MMA of the pair done, both TMEMs drained
     if (warp == 1) {

@@ -31,3 +31,18 @@ def test_codes_and_scales_lie_on_one_device():
     mu.Act8(OnDevice(0, (4, 64)), OnDevice(0, (4, 16)), 50, "int8")
     with pytest.raises(ValueError, match="device"):
         mu.Act8(OnDevice(0, (4, 64)), OnDevice(1, (4, 16)), 50, "int8")
+
+
+def test_arrivals_on_another_cta_order_memory_beyond_their_own():
+    """A release at CTA scope orders nothing for the CTA that waits: an arrival on a peer's barrier releases at
+    cluster scope, or is relaxed where there is no memory to hand over."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.abspath(mu.__file__)), "csrc")
+    seen = []
+    for path in glob.glob(os.path.join(csrc, "*.cu*")):
+        for instr in re.findall(r"mbarrier\.arrive[.\w:]*", open(path).read()):
+            if "shared::cluster" in instr:
+                seen.append(instr)
+    assert seen and all(".release.cluster." in i or ".relaxed.cluster." in i for i in seen), seen
