@@ -17,8 +17,7 @@ the library's ``muon_partition``) and broadcasts the updated parameters.
 
 The layer side (``activations``: ``Act8``, ``act_pack``, ``act_unpack``,
 ``rmsnorm_forward``, ``swiglu_forward``, ``swiglu_backward``, ``GradPlan``) makes the
-gradients the step reads from activations held in 8 bits; its names are resolved on
-first use, as that module imports torch.
+gradients the step reads from activations held in 8 bits.
 """
 from __future__ import annotations
 
@@ -38,19 +37,6 @@ __all__ = [
     "Act8", "act_pack", "act_unpack", "rmsnorm_forward", "swiglu_forward", "swiglu_backward", "GradPlan",
     "grad_plan_workspace_size",
 ]
-
-# names of the layer side, resolved from .activations on first use
-_LAYER = ("Act8", "act_pack", "act_unpack", "rmsnorm_forward", "swiglu_forward", "swiglu_backward", "GradPlan",
-          "grad_plan_workspace_size")
-
-
-def __getattr__(name):
-    if name in _LAYER:
-        from . import activations
-        globals().update({n: getattr(activations, n) for n in _LAYER})
-        return globals()[name]
-    raise AttributeError("module %r has no attribute %r" % (__name__, name))
-
 
 MUON_OK, MUON_ERR_INVALID_ARG, MUON_ERR_UNSUPPORTED, MUON_ERR_OOM = 0, 1, 2, 3
 MUON_ERR_CUDA, MUON_ERR_TIMEOUT, MUON_ERR_NONFINITE = 4, 5, 6
@@ -778,3 +764,7 @@ def measure_costs(shapes, grad_dtype: str = "bf16", sample: int = 4, reps: int =
             plan.close()
         del W, G, M
     return [per_shape[(min(m, n), max(m, n))] for m, n in shapes]
+
+
+from .activations import (Act8, GradPlan, act_pack, act_unpack, grad_plan_workspace_size,  # noqa: E402
+                          rmsnorm_forward, swiglu_backward, swiglu_forward)

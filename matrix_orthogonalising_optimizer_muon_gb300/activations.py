@@ -11,16 +11,23 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
-
 from . import (MUON_ACT_E4M3, MUON_ACT_INT8, MUON_BF16, MUON_F32, MuonAct8, _check, load)
 
 __all__ = ["Act8", "act_pack", "act_unpack", "rmsnorm_forward", "swiglu_forward", "swiglu_backward", "GradPlan",
            "grad_plan_workspace_size"]
 
 _FORMATS = {"e4m3": MUON_ACT_E4M3, "int8": MUON_ACT_INT8}
-_DTYPES = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
 ACT_GROUP = 32
+torch = None   # the module and its element types, from the first call on (_torch)
+_DTYPES = {}
+
+
+def _torch():
+    """Torch is imported by the first call that takes tensors, as in the rest of the binding."""
+    global torch
+    import torch as module
+    _DTYPES.update({module.float32: MUON_F32, module.bfloat16: MUON_BF16})
+    torch = module
 
 
 def _pad16(n: int) -> int:
@@ -35,6 +42,8 @@ class Act8:
     __slots__ = ("codes", "scales", "rows", "cols", "fmt", "device", "ref")
 
     def __init__(self, codes, scales, cols: int, fmt: str):
+        if torch is None:
+            _torch()
         if fmt not in _FORMATS:
             raise ValueError("fmt must be 'e4m3' or 'int8', got %r" % (fmt,))
         for t, need, name in ((codes, cols, "codes"), (scales, (cols + ACT_GROUP - 1) // ACT_GROUP, "scales")):
@@ -56,6 +65,8 @@ class Act8:
 
     @classmethod
     def empty(cls, rows: int, cols: int, fmt: str = "e4m3", device="cuda") -> "Act8":
+        if torch is None:
+            _torch()
         groups = (cols + ACT_GROUP - 1) // ACT_GROUP
         return cls(torch.empty((rows, _pad16(cols)), dtype=torch.uint8, device=device),
                    torch.empty((rows, _pad16(groups)), dtype=torch.uint8, device=device), cols, fmt)
@@ -81,9 +92,11 @@ def _mat(t, rows, cols, dtype, dev, name):
     return t.data_ptr(), t.stride(0) if rows > 1 else cols
 
 
-def _vec(t, n, dev, name, dtype=torch.float32):
+def _vec(t, n, dev, name, dtype=None):
     if t is None:
         return None
+    if dtype is None:
+        dtype = torch.float32
     if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s: need a contiguous %s tensor of %d elements on the current CUDA device, got %s %s on %s"
                          % (name, dtype, n, t.dtype, tuple(t.shape), t.device))
@@ -101,6 +114,8 @@ def _act(a, rows, cols, dev, name):
 
 def _shape(t, name):
     """(rows, cols, dtype, dtype code, current device) for the operand that sets a call's shape."""
+    if torch is None:
+        _torch()
     if t.dim() != 2 or t.dtype not in _DTYPES or not t.is_cuda:
         raise ValueError("%s: need a two-dimensional float32 or bfloat16 CUDA tensor, got %s %s on %s"
                          % (name, t.dtype, tuple(t.shape), t.device))
@@ -177,6 +192,8 @@ class GradPlan:
     (``muon_grad_plan_create``); one serves calls of any shapes, one after another."""
 
     def __init__(self):
+        if torch is None:
+            _torch()
         self.lib = load()
         h = ctypes.c_void_p()
         _check(self.lib.muon_grad_plan_create(ctypes.byref(h)), "muon_grad_plan_create")

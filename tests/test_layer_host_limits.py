@@ -46,3 +46,15 @@ def test_arrivals_on_another_cta_order_memory_beyond_their_own():
             if "shared::cluster" in instr:
                 seen.append(instr)
     assert seen and all(".release.cluster." in i or ".relaxed.cluster." in i for i in seen), seen
+
+
+def test_star_import_needs_no_torch():
+    """The package's names, the layer side's among them, on a machine without torch, as before there was a layer side."""
+    import os
+    import subprocess
+    import sys
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from matrix_orthogonalising_optimizer_muon_gb300 import *\n"
+            "assert grad_plan_workspace_size() > 0 and callable(rmsnorm_forward) and Act8.__slots__")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(mu.__file__)))
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
