@@ -460,8 +460,8 @@ muon_status muon_stage_times(muon_plan p, float* ms, double* flops, int32_t n_st
  * the step reads, from activations held in 8 bits between the forward and the
  * backward pass.  The conventions above hold, except that each call takes its
  * tensors themselves (one matrix per argument, a pointer and a row pitch `ld`
- * in elements, ld >= cols, below 2^32 bytes; rows need no alignment, 16-byte aligned rows are faster)
- * and that nothing but muon_wgrad and muon_rmsnorm_backward needs a plan.
+ * in elements, ld >= cols, below 2^32 bytes; rows need no alignment, 16-byte
+ * aligned rows are faster) and that nothing but muon_wgrad and muon_rmsnorm_backward needs a plan.
  * Values of a NULL optional argument are not computed.  Outputs must not
  * overlap inputs or one another unless a call says so; tensors that interleave
  * row by row with the same pitch (the two halves of one wide tensor) do not
@@ -593,7 +593,8 @@ muon_status muon_rmsnorm_backward(muon_grad_plan p, const void* dy, int64_t lddy
  *              muon_step), overwritten, or added to when accumulate is nonzero.
  * Operands are bf16 (exact for the 8-bit x), products and sums fp32, those of at most 2048
  * tokens in one accumulator of the tensor cores, whose additions truncate.  The sums' order
- * depends on the sizes alone: the same inputs give the same bits.  1 <= m, n <= 2^20,
+ * depends on the sizes alone: the same inputs give the same bits.  An fp32 grad is added to
+ * by reductions in L2, which flush subnormal numbers (below 2^-126 in magnitude) to zero.  1 <= m, n <= 2^20,
  * 0 <= tokens < 2^31.
  */
 muon_status muon_wgrad(muon_grad_plan p, const void* dy, int64_t lddy, const muon_act8* x, int64_t tokens, int64_t m,

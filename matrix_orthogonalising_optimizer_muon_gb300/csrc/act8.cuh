@@ -135,8 +135,9 @@ __device__ __forceinline__ void seg_load(const void* p, int c0, int cols, int la
     raw.get(v);
 }
 
-// Stores the segment's values below `cols`.  Every lane of the warp takes part.  Shifted: a lane stores the aligned piece (fp32: two) that begins in the lane below it, with the
-// values that reach into it from there; the segment's ragged ends go value by value.
+// Stores the segment's values below `cols`.  Every lane of the warp takes part.  Shifted: a lane stores
+// the aligned piece (fp32: two) that begins in the lane below it, with the values that reach into it
+// from there; the segment's ragged ends go value by value.
 template <bool BF16, int MODE, bool FULL = false>
 __device__ __forceinline__ void seg_store(void* p, int c0, int cols, int lane, const float (&v)[8]) {
     if constexpr (MODE == kByValue) {

@@ -183,7 +183,8 @@ constexpr int kRingMost = 4;
 // bulk copies while one is reduced, so that HBM stays busy across the reduction's barrier
 // with registers for one row only.
 template <bool BF16, bool VEC, int S, bool RING>
-__global__ void __launch_bounds__(kMaxThreads, S == 1 ? 2 : 1) k_rmsnorm_backward(const NormBwdArgs a, const RingShape ring) {
+__global__ void __launch_bounds__(kMaxThreads, S == 1 ? 2 : 1)
+    k_rmsnorm_backward(const NormBwdArgs a, const RingShape ring) {
     extern __shared__ __align__(128) uint8_t slots[];
     __shared__ __align__(16) float red[2][16];
     __shared__ uint64_t full[kRingMost];
@@ -389,7 +390,8 @@ cudaError_t launch_rmsnorm_forward(const NormArgs& a, bool bf16, bool vec, cudaS
                                k_rmsnorm_forward<true, false, 8>, k_rmsnorm_forward<true, true, 8>}};
     int warps, segs;
     norm_shape(a.cols, kFwdSegs, &warps, &segs);
-    return launch_pdl(k[segs == 8 ? 3 : segs >> 1][(bf16 ? 2 : 0) + (vec ? 1 : 0)], dim3((unsigned)a.rows), dim3(32 * warps), 0, s, a);
+    return launch_pdl(k[segs == 8 ? 3 : segs >> 1][(bf16 ? 2 : 0) + (vec ? 1 : 0)], dim3((unsigned)a.rows),
+                      dim3(32 * warps), 0, s, a);
 }
 
 int rmsnorm_backward_blocks(long long rows, int cols, int sm_count) {
@@ -416,7 +418,7 @@ cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a, bool bf16, bool vec, i
         r.scales = a.saved.codes ? up16((a.cols + kActGroup - 1) / kActGroup) : 0;
         r.dres = a.dres.p ? r.dy : 0;
         r.slot = r.dy + r.x + r.scales + r.dres;
-        // the blocks of an SM share its shared memory; a block that gets two rows or more uses the ring
+        // the blocks of an SM share its shared memory; rows of which two fit a block's share use the ring
         const int room = kRingRoom / std::max(kBwdWarps / warps, 1) - 1024;
         r.depth = std::min(room / r.slot, kRingMost);
         if (r.depth < 2) r.depth = 0;

@@ -15,18 +15,19 @@
 //   3-10   conversion of x into a 16 KB bf16 operand per step, four steps at a time
 //   11-14  epilogue: column scale, addition to grad, stores
 // Two rings: x as it arrives (full_r by TMA, empty_r by the conversion), and the operands (dy
-// and converted x; ready, on the even CTA, by both CTAs' conversion warps, the odd one's through copies
-// of 16 bytes, and dy's TMA bytes, empty, on both, by the MMAs), so the MMA warp has one wait and one commit per step.
+// and converted x; ready, on the even CTA, by both CTAs' conversion warps, the odd one's through
+// copies of 16 bytes, and dy's TMA bytes, empty, on both, by the MMAs), so the MMA warp has one
+// wait and one commit per step.
 //
 // What bounds it: shared memory.  A step moves 82 KB through each SM's 128 bytes a cycle (MMA
 // operands 32 KB, dy in 16 KB, codes in and out 18 KB, converted x 16 KB), 640 cycles where its
-// MMAs take 512.  Under the profiler at 8192 tokens x 3584 x 3584 the tensor pipe is busy 77 % of
-// the cycles with work and the shared-memory pipe 87 %.  Measured: 144 us there (1460 TFLOP/s; 196
-// tiles are 2.6 turns of the 76 pairs), 1465 us at 16384 x 18944 x 3584 with fp32 gradients (1520
-// TFLOP/s, 80 % of the measured burst rate of a library product, under the power cap), 1362 us
-// with bf16 ones.  256 x 256 is the largest tile whose accumulators fit TMEM twice, so that an
-// epilogue overlaps the next tile.  Weights of few tokens are bound by the epilogue: 32 experts of
-// 1024 x 2048 with 64 tokens each take 51 us, 21 of them HBM's for the gradients.
+// MMAs take 512.  Under the profiler at 8192 tokens x 3584 x 3584 the tensor pipe is busy 70 % of
+// the cycles with work and the shared-memory pipe 95 %, a part of it for the chains' sums (kChain).
+// Measured: 159 us there (1320 TFLOP/s; 196 tiles are 2.6 turns of the 76 pairs), 1500 us at 16384 x
+// 18944 x 3584 with fp32 or bf16 gradients (1480 TFLOP/s, 78 % of the measured burst rate of a library
+// product, under the power cap).  256 x 256 is the largest tile whose accumulators fit TMEM twice, so
+// that an epilogue overlaps the next tile.  Weights of few tokens are bound by the epilogue: 32 experts
+// of 1024 x 2048 with 64 tokens each take 42 us, 21 of them HBM's for the gradients.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -47,7 +48,8 @@ constexpr int kConvGroups = 4;
 constexpr int kConvFirst = 3;           // first conversion warp
 constexpr int kWgEpiWarps = 4;
 // Warps by whether dy comes by TMA or is copied by the conversion warps, which are then twice as many
-// (8192 x 3585 x 3584: 298 us; 434 with eight).
+// (8192 x 3585 x 3584: 298 us; 434 with eight; 335-365 since bf16 gradients add up chains: with 80
+// registers a thread their epilogue spills).
 template <bool TMA_Y>
 struct Roles {
     static constexpr int kConvWarps = TMA_Y ? 8 : 16;
@@ -61,8 +63,8 @@ struct Roles {
 // them: by 1.1e-5 of itself over 16384 tokens of random data, by 1.3 % over 2^21 tokens of one sign.  The
 // epilogue adds up the chains' sums in fp32 instead: fp32 gradients in place, bf16 ones in the workspace.
 // That leaves 8.4e-7 (an fp32 product on the CUDA cores: 6.9e-7) and costs an fp32 gradient 7 % (16384 x
-// 18944 x 3584: 1437 -> 1541 us; chains of 4096 tokens: 2e-6, 1470 us), a bf16 one 5 to 8 % (there
-// 1258 -> 1312 us, 8192 x 3584 x 3584 144 -> 156).
+// 18944 x 3584: 1437 -> 1541 us; chains of 4096 tokens: 2e-6, 1470 us), a bf16 one 10 % (there 1348 ->
+// 1513 us, 8192 x 3584 x 3584 134 -> 147, back to back).
 constexpr uint32_t kChain = 2048;
 constexpr int kBandM = 8;               // tiles along m whose columns of dy are in flight together
 constexpr int kSortGroups = 256;        // experts that are dealt out by their number of tokens
@@ -182,17 +184,25 @@ struct Turns {
         count = L.units / pairs;
         count += unit(count) < L.units;
     }
-    __device__ __forceinline__ int unit(int turn) const { return turn * pairs + (snake && (turn & 1) ? pairs - 1 - pair : pair); }
+    __device__ __forceinline__ int unit(int turn) const {
+        return turn * pairs + (snake && (turn & 1) ? pairs - 1 - pair : pair);
+    }
     __device__ __forceinline__ Unit get(const WgradLaunch& L, const Experts* ex, uint32_t table, int turn) const {
         if (turn >= kTurnTable) return decode_unit(L, ex, unit(turn));
         Unit u;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.m0), "=r"(u.n0), "=r"(u.begin), "=r"(u.end) : "r"(table + turn * 32));
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.group), "=r"(u.tile), "=r"(u.part), "=r"(u.pad) : "r"(table + turn * 32 + 16));
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.m0), "=r"(u.n0), "=r"(u.begin), "=r"(u.end)
+                     : "r"(table + turn * 32));
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.group), "=r"(u.tile), "=r"(u.part), "=r"(u.pad)
+                     : "r"(table + turn * 32 + 16));
         return u;
     }
 };
 
-__device__ __forceinline__ int unit_steps(const Unit& u) { return (int)((uint32_t)(u.end - u.begin + kWgStepT - 1) / kWgStepT); }
+__device__ __forceinline__ int unit_steps(const Unit& u) {
+    return (int)((uint32_t)(u.end - u.begin + kWgStepT - 1) / kWgStepT);
+}
 
 __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -547,8 +557,8 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
             }
             tc_fence_after();
             const uint32_t tbase = e.tmem_base + acc * 256 + (static_cast<uint32_t>(e.wq * 32) << 16);
-            if (BF16 && WIDE && DIRECT && L.sectors && part == nullptr && run == nullptr && !L.a.accumulate && w.n0 + 256 <= L.a.n &&
-                r0 + 32 <= L.a.m) {
+            if (BF16 && WIDE && DIRECT && L.sectors && part == nullptr && run == nullptr && !L.a.accumulate &&
+                w.n0 + 256 <= L.a.n && r0 + 32 <= L.a.m) {
                 store_rows(L, w, e, tbase, acc);
                 ++local;
                 continue;
@@ -910,7 +920,8 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
                     if (leader)
                         mbar_arrive(ready + b);
                     else   // from and to this warp's 16 bytes, which mean nothing
-                        bulk_signal(ready_lead + Cfg::SIGNAL_OFFSET - Cfg::BAR_OFFSET - 16 * kRingR + 16 * (warp - kConvFirst),
+                        bulk_signal(ready_lead + (Cfg::SIGNAL_OFFSET - Cfg::BAR_OFFSET - 16 * kRingR) +
+                                        16 * (warp - kConvFirst),
                                     smem + Cfg::SIGNAL_OFFSET + 16 * (warp - kConvFirst), ready_lead + b * 8);
                 }
             }
@@ -961,8 +972,10 @@ bool map_2d(CUtensorMap* map, const void* base, bool bytes, uint64_t cols, uint6
 typedef void (*WgradKernel)(WgradLaunch);
 WgradKernel pick(int fmt, bool tma_y, bool bf16) {
     static const WgradKernel k[2][2][2] = {
-        {{k_wgrad<kE4M3, false, false>, k_wgrad<kE4M3, false, true>}, {k_wgrad<kE4M3, true, false>, k_wgrad<kE4M3, true, true>}},
-        {{k_wgrad<kInt8, false, false>, k_wgrad<kInt8, false, true>}, {k_wgrad<kInt8, true, false>, k_wgrad<kInt8, true, true>}}};
+        {{k_wgrad<kE4M3, false, false>, k_wgrad<kE4M3, false, true>},
+         {k_wgrad<kE4M3, true, false>, k_wgrad<kE4M3, true, true>}},
+        {{k_wgrad<kInt8, false, false>, k_wgrad<kInt8, false, true>},
+         {k_wgrad<kInt8, true, false>, k_wgrad<kInt8, true, true>}}};
     return k[fmt][tma_y][bf16];
 }
 
@@ -1018,7 +1031,7 @@ cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaS
         !map_2d(&L.map_x, a.x.codes, true, a.n, a.tokens, a.x.ldq, 128, true) ||
         !map_2d(&L.map_s, a.x.scales, true, (a.n + kActGroup - 1) / kActGroup, a.tokens, a.x.lds, 16, false))
         return cudaErrorInvalidValue;
-        return launch_pdl_cluster(pick(a.x.format, tma_y, bf16_grad), dim3(2 * std::min(L.units, pairs)),
+    return launch_pdl_cluster(pick(a.x.format, tma_y, bf16_grad), dim3(2 * std::min(L.units, pairs)),
                               dim3(tma_y ? Roles<true>::kThreads : Roles<false>::kThreads), WgCfg::SMEM_BYTES,
                               s, 2u, L);
 }

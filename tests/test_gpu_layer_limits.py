@@ -186,7 +186,8 @@ def test_swiglu_in_many_turns(mu, rows, cols, pad):
     close_gpu(dgu[:, cols:], D * G * s, 16 * U * (D * G).abs() * s + 1e-30)
     v = G * s * V
     step = torch.exp2(a8.scales[:, :(cols + 31) // 32].double() - 127).repeat_interleave(32, 1)[:, :cols]
-    assert bool(((unpacked(mu, a8) - v).abs() <= 1.001 * torch.maximum(v.abs() / 16, 2.0 ** -10 * step) + 32 * U * v.abs()).all())
+    half = torch.maximum(v.abs() / 16, 2.0 ** -10 * step)
+    assert bool(((unpacked(mu, a8) - v).abs() <= 1.001 * half + 32 * U * v.abs()).all())
 
 
 @pytest.mark.parametrize("rows,cols,dtype,pad,source", [
