@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
                 const int steps = unit_steps(w);
                 const int ym = w.m0 + 128 * (int)q;
                 for (int k = 0; k < steps; ++k) {
-                    if (!mbar_wait_idle(empty + slot, ph, abort_flag, L.a.status, kStatusTimeoutProducer, false)) {
+                    if (!mbar_wait_idle(empty + slot, ph, abort_flag, L.a.status, kStatusTimeoutProducer, true)) {
                         ok = false;
                         break;
                     }
@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
                         if (row0 + 8 * i >= left) raw[2 * i] = raw[2 * i + 1] = make_uint4(0, 0, 0, 0), sc[i] = 0;
                 }
                 if (!mbar_wait_idle(empty + b, (it / kRingM & 1u) ^ 1u, abort_flag, L.a.status,
-                                    kStatusTimeoutProducer, false)) {
+                                    kStatusTimeoutProducer, true)) {
                     ok = false;
                     break;
                 }

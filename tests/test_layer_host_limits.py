@@ -58,3 +58,17 @@ def test_star_import_needs_no_torch():
             "assert grad_plan_workspace_size() > 0 and callable(rmsnorm_forward) and Act8.__slots__")
     root = os.path.dirname(os.path.dirname(os.path.abspath(mu.__file__)))
     subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
+
+
+def test_waits_for_another_cta_acquire_beyond_their_own():
+    """The weight gradient's barriers that the pair's other CTA completes (operands, freed slots, accumulators):
+    every wait on them acquires at cluster scope, as the pair GEMM's do."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(os.path.abspath(mu.__file__)), "csrc", "wgrad.cu")).read()
+    waits = re.findall(r"mbar_((?:test_|try_)?wait\w*)\(\s*(?:e\.)?(\w+) \+ ([^;{]*?)\)\)", src)
+    crossing = [(kind, bar, args) for kind, bar, args in waits if bar in ("ready", "empty", "tfull", "tempty")]
+    assert {bar for _, bar, _ in crossing} == {"ready", "empty", "tfull", "tempty"}
+    for kind, bar, args in crossing:
+        assert kind.endswith("_cluster") or args.rstrip(" )").endswith("true"), (kind, bar, args)
+    assert "mbar_test_wait(" not in src
