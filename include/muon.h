@@ -461,7 +461,8 @@ muon_status muon_stage_times(muon_plan p, float* ms, double* flops, int32_t n_st
  * backward pass.  The conventions above hold, except that each call takes its
  * tensors themselves (one matrix per argument, a pointer and a row pitch `ld`
  * in elements, ld >= cols, below 2^32 bytes; rows need no alignment, 16-byte
- * aligned rows are faster) and that nothing but muon_wgrad and muon_rmsnorm_backward needs a plan.
+ * aligned rows are faster) and that only muon_wgrad, muon_rmsnorm_backward, muon_product, muon_dgrad,
+ * muon_grad_norm and muon_grad_clip need a plan.
  * Values of a NULL optional argument are not computed.  Outputs must not
  * overlap inputs or one another unless a call says so; tensors that interleave
  * row by row with the same pitch (the two halves of one wide tensor) do not
@@ -546,7 +547,7 @@ muon_status muon_swiglu_backward(const void* da, int64_t ldda, const muon_act8* 
                                  int64_t lddu, const muon_act8* saved_out, void* stream);
 
 /*
- * A grad plan owns what the two gradient reductions need on the current device: one
+ * A grad plan owns what the reductions and the products need on the current device: one
  * workspace allocation of muon_grad_plan_workspace_size bytes, whatever shapes its
  * calls have, and a status word.  Calls on one plan share the workspace: they are
  * ordered by the caller, as those of a muon_plan.  muon_grad_plan_create
@@ -600,6 +601,91 @@ muon_status muon_rmsnorm_backward(muon_grad_plan p, const void* dy, int64_t lddy
 muon_status muon_wgrad(muon_grad_plan p, const void* dy, int64_t lddy, const muon_act8* x, int64_t tokens, int64_t m,
                        int64_t n, const int32_t* offsets, int32_t groups, const float* col_scale, void* grad,
                        muon_dtype grad_dtype, int32_t accumulate, void* stream);
+
+/*
+ * muon_product / muon_dgrad - the other two products of a weight (m x n, as muon_step takes
+ * it) beside muon_wgrad: y = x W^T, and the gradient of its input, dx = dy W.
+ *   x, dx      tokens x n, bf16.
+ *   y, dy      tokens x m, bf16.
+ *   weight     dense row-major bf16, m x n, or groups x m x n.
+ *   groups     as in muon_wgrad: 0 for one weight, else experts whose tokens offsets delimits
+ *              (device, groups + 1 int32, non-decreasing, clamped to [0, tokens]); each token is
+ *              multiplied with its expert's weight.  Rows of the output outside every expert are
+ *              left as they were, whatever the input holds there.
+ * Products and sums are fp32 and rounded to bf16 once.  The sums' order depends on the sizes and
+ * the offsets alone: the same inputs give the same bits.  1 <= m, n <= 2^20, 0 <= tokens < 2^31,
+ * groups <= 4096.
+ */
+muon_status muon_product(muon_grad_plan p, const void* x, int64_t ldx, const void* weight, int64_t tokens, int64_t m,
+                         int64_t n, const int32_t* offsets, int32_t groups, void* y, int64_t ldy, void* stream);
+muon_status muon_dgrad(muon_grad_plan p, const void* dy, int64_t lddy, const void* weight, int64_t tokens, int64_t m,
+                       int64_t n, const int32_t* offsets, int32_t groups, void* dx, int64_t lddx, void* stream);
+
+/*
+ * muon_expert_order - the order of tokens by expert that the calls with offsets take.
+ *   ids      device, tokens x choices int32, dense: the experts of each token.  A value outside
+ *            [0, experts) is no choice (a token that pads the batch).
+ *   offsets  device, experts + 1 int32: expert e has rows offsets[e] .. offsets[e + 1] - 1.
+ *   slots    device, tokens x choices int32: the row of each choice, -1 where there is none.
+ * Within an expert rows are in ascending order of token, then choice.  1 <= choices <= 64,
+ * 1 <= experts <= 4096, tokens * choices < 2^31.
+ */
+muon_status muon_expert_order(const int32_t* ids, int64_t tokens, int32_t choices, int32_t experts, int32_t* offsets,
+                              int32_t* slots, void* stream);
+
+/*
+ * Rows between the tokens' order (tokens x cols) and the experts' (rows x cols, of the same
+ * dtype), by the slots of muon_expert_order.  A slot outside [0, rows) is no choice.
+ *   muon_expert_dispatch          out[slots[t, j], :] = x[t, :].  Other rows of out are left as they were.
+ *                                 slots must not repeat a row.
+ *   muon_expert_combine           out[t, :] = sum over j of weights[t, j] expert_rows[slots[t, j], :], summed
+ *                                 in fp32 with j ascending; zero for a token without choices.  weights:
+ *                                 tokens x choices fp32, dense, or NULL for ones, which gives the gradient of
+ *                                 muon_expert_dispatch.
+ *   muon_expert_combine_backward  drows[slots[t, j], :] = weights[t, j] dout[t, :] (other rows are left as
+ *                                 they were; slots must not repeat a row) and dweights[t, j] = dout[t, :] .
+ *                                 expert_rows[slots[t, j], :], 0 where there is no choice.  Either output may be
+ *                                 NULL, and expert_rows without dweights.
+ * 1 <= choices <= 64, tokens * choices < 2^31, 0 <= rows < 2^31, 1 <= cols <= 2^20.
+ */
+muon_status muon_expert_dispatch(const void* x, int64_t ldx, const int32_t* slots, int64_t tokens, int32_t choices,
+                                 int64_t rows, int64_t cols, muon_dtype dtype, void* out, int64_t ldo, void* stream);
+muon_status muon_expert_combine(const void* expert_rows, int64_t ldr, const int32_t* slots, const float* weights,
+                                int64_t tokens, int32_t choices, int64_t rows, int64_t cols, muon_dtype dtype, void* out,
+                                int64_t ldo, void* stream);
+muon_status muon_expert_combine_backward(const void* dout, int64_t ldd, const int32_t* slots, const float* weights,
+                                         const void* expert_rows, int64_t ldr, int64_t tokens, int32_t choices,
+                                         int64_t rows, int64_t cols, muon_dtype dtype, void* drows, int64_t lddr,
+                                         float* dweights, void* stream);
+
+/*
+ * muon_grad_norm - the Euclidean norm of n gradients together, norm = sqrt(sum of all squares).
+ *   grads, counts, dtypes  HOST arrays of n device pointers, element counts (0: skipped) and
+ *                          muon_dtype codes, read before the call returns.  Each gradient is dense and
+ *                          aligned to its elements; the counts sum to at most 2^43.
+ *   norm                   device, one fp32.
+ * Squares are summed in fp32 over at most 32 values, then in fp64, in a fixed order; they neither overflow
+ * nor vanish, whatever the gradients' scale.  A NaN gives NaN, an infinity or a norm beyond fp32's range
+ * infinity; no gradients give 0.
+ */
+muon_status muon_grad_norm(muon_grad_plan p, const void* const* grads, const int64_t* counts, const int32_t* dtypes,
+                           int32_t n, float* norm, void* stream);
+
+/*
+ * muon_grad_clip - the gradients scaled to a norm of at most max_norm: g * (max_norm / norm) where
+ * norm > max_norm, in fp32, rounded once.  Where it is not, or is not finite, they are left as they are.
+ *   grads, counts, dtypes, n  as muon_grad_norm.
+ *   norm          device, one fp32, as muon_grad_norm left it (or of all ranks together).
+ *   max_norm      > 0, finite.
+ *   out           NULL: in place (nothing is written where nothing is scaled).  Else a HOST array of n device
+ *                 pointers that receive the result, of out_dtypes: fp32 sums, say, into the bf16 gradients
+ *                 that a step reads.  out[i] may be grads[i] itself if their types agree.
+ *   out_dtypes    HOST array of n muon_dtype codes, with out.
+ * No tensor that is written may overlap another one.
+ */
+muon_status muon_grad_clip(muon_grad_plan p, const void* const* grads, const int64_t* counts, const int32_t* dtypes,
+                           int32_t n, const float* norm, float max_norm, void* const* out, const int32_t* out_dtypes,
+                           void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,7 +17,9 @@ the library's ``muon_partition``) and broadcasts the updated parameters.
 
 The layer side (``activations``: ``Act8``, ``act_pack``, ``act_unpack``,
 ``rmsnorm_forward``, ``swiglu_forward``, ``swiglu_backward``, ``GradPlan``) makes the
-gradients the step reads from activations held in 8 bits.
+gradients the step reads from activations held in 8 bits.  ``experts`` (``expert_order``,
+``expert_dispatch``, ``expert_combine``, ``expert_combine_backward``) puts tokens in the order of
+their experts and back, for the grad plan's products by expert.
 """
 from __future__ import annotations
 
@@ -34,7 +36,8 @@ __all__ = [
     "MUON_ERR_CUDA", "MUON_ERR_TIMEOUT", "MUON_ERR_NONFINITE", "MUON_F32", "MUON_BF16",
     "MUON_MODE_NS", "MUON_MODE_ROWNORM", "EXPORTED",
     "MuonAct8", "MUON_ACT_E4M3", "MUON_ACT_INT8",
-    "Act8", "act_pack", "act_unpack", "rmsnorm_forward", "swiglu_forward", "swiglu_backward", "GradPlan",
+    "Act8", "act_pack", "act_unpack", "rmsnorm_forward", "swiglu_forward", "swiglu_backward", "GradPlan", "GradList",
+    "expert_order", "expert_dispatch", "expert_combine", "expert_combine_backward",
     "grad_plan_workspace_size",
 ]
 
@@ -132,6 +135,14 @@ EXPORTED = {
     "muon_rmsnorm_backward": (_I, [_P, _P, _L, _A, _P, _L, _P, _P, _P, _L, _L, _L, _I, _P, _L, _P,
                                    ctypes.c_int32, _P]),
     "muon_wgrad": (_I, [_P, _P, _L, _A, _L, _L, _L, _P, ctypes.c_int32, _P, _P, _I, ctypes.c_int32, _P]),
+    "muon_product": (_I, [_P, _P, _L, _P, _L, _L, _L, _P, ctypes.c_int32, _P, _L, _P]),
+    "muon_dgrad": (_I, [_P, _P, _L, _P, _L, _L, _L, _P, ctypes.c_int32, _P, _L, _P]),
+    "muon_expert_order": (_I, [_P, _L, ctypes.c_int32, ctypes.c_int32, _P, _P, _P]),
+    "muon_expert_dispatch": (_I, [_P, _L, _P, _L, ctypes.c_int32, _L, _L, _I, _P, _L, _P]),
+    "muon_expert_combine": (_I, [_P, _L, _P, _P, _L, ctypes.c_int32, _L, _L, _I, _P, _L, _P]),
+    "muon_expert_combine_backward": (_I, [_P, _L, _P, _P, _P, _L, _L, ctypes.c_int32, _L, _L, _I, _P, _L, _P, _P]),
+    "muon_grad_norm": (_I, [_P, _P, _P, _P, ctypes.c_int32, _P, _P]),
+    "muon_grad_clip": (_I, [_P, _P, _P, _P, ctypes.c_int32, _P, ctypes.c_float, _P, _P, _P]),
 }
 
 _lib = None
@@ -766,5 +777,6 @@ def measure_costs(shapes, grad_dtype: str = "bf16", sample: int = 4, reps: int =
     return [per_shape[(min(m, n), max(m, n))] for m, n in shapes]
 
 
-from .activations import (Act8, GradPlan, act_pack, act_unpack, grad_plan_workspace_size,  # noqa: E402
+from .activations import (Act8, GradList, GradPlan, act_pack, act_unpack, grad_plan_workspace_size,  # noqa: E402
                           rmsnorm_forward, swiglu_backward, swiglu_forward)
+from .experts import expert_combine, expert_combine_backward, expert_dispatch, expert_order  # noqa: E402

@@ -1,6 +1,7 @@
 """Layer-side operators of the library for torch tensors: activations held in 8 bits
-(``Act8``), the RMS norm with the residual's addition, SwiGLU, and the weight gradient
-that ``MuonPlan.step`` reads, formed from 8-bit activations (``GradPlan``).
+(``Act8``), the RMS norm with the residual's addition, SwiGLU, and, with a ``GradPlan``, the
+products of a weight or of experts' weights, the weight gradient that ``MuonPlan.step`` reads,
+formed from 8-bit activations, and the norm and clipping of all gradients (``GradList``).
 
 Argument marshalling only, as in the rest of the binding: outputs are the caller's
 tensors, work is enqueued on the current stream (or ``stream``), and a call that cannot
@@ -14,7 +15,7 @@ import ctypes
 from . import (MUON_ACT_E4M3, MUON_ACT_INT8, MUON_BF16, MUON_F32, MuonAct8, _check, load)
 
 __all__ = ["Act8", "act_pack", "act_unpack", "rmsnorm_forward", "swiglu_forward", "swiglu_backward", "GradPlan",
-           "grad_plan_workspace_size"]
+           "GradList", "grad_plan_workspace_size"]
 
 _FORMATS = {"e4m3": MUON_ACT_E4M3, "int8": MUON_ACT_INT8}
 ACT_GROUP = 32
@@ -187,8 +188,37 @@ def grad_plan_workspace_size() -> int:
     return n.value
 
 
+class GradList:
+    """Gradients of any shapes, fp32 or bf16, dense, as ``GradPlan.grad_norm`` and ``GradPlan.grad_clip`` take them:
+    their pointers, counts and types, gathered once (a list that is built anew for every call costs the host about
+    a microsecond per tensor).  It keeps the tensors alive."""
+
+    __slots__ = ("tensors", "device", "n", "pointers", "counts", "dtypes")
+
+    def __init__(self, tensors):
+        if torch is None:
+            _torch()
+        self.tensors = list(tensors)
+        self.device = self.tensors[0].get_device() if self.tensors else torch.cuda.current_device()
+        for i, t in enumerate(self.tensors):
+            if t.dtype not in _DTYPES or not t.is_cuda or not t.is_contiguous() or t.get_device() != self.device:
+                raise ValueError("gradient %d: need a contiguous float32 or bfloat16 CUDA tensor on %s, got %s %s on %s"
+                                 % (i, self.device, t.dtype, tuple(t.shape), t.device))
+        self.n = len(self.tensors)
+        self.pointers = (ctypes.c_void_p * self.n)(*[t.data_ptr() for t in self.tensors])
+        self.counts = (ctypes.c_int64 * self.n)(*[t.numel() for t in self.tensors])
+        self.dtypes = (ctypes.c_int32 * self.n)(*[_DTYPES[t.dtype] for t in self.tensors])
+
+
+def _grads(grads, dev, name):
+    grads = grads if isinstance(grads, GradList) else GradList(grads)
+    if grads.device != dev:
+        raise ValueError("%s: need gradients on the current CUDA device, got them on %s" % (name, grads.device))
+    return grads
+
+
 class GradPlan:
-    """Workspace and status word of the gradient reductions on the current device
+    """Workspace and status word of the reductions and products on the current device
     (``muon_grad_plan_create``); one serves calls of any shapes, one after another."""
 
     def __init__(self):
@@ -255,3 +285,49 @@ class GradPlan:
                                    _vec(offsets, groups + 1, dev, "offsets", torch.int32), groups,
                                    _vec(col_scale, n, dev, "col_scale"), grad.data_ptr(), _DTYPES[grad.dtype],
                                    1 if accumulate else 0, _stream(stream, dev)), "muon_wgrad")
+
+    def _product(self, name, x, weight, out, offsets, dgrad, stream):
+        dev = torch.cuda.current_device()
+        groups = 0 if offsets is None else offsets.numel() - 1
+        if x.dim() != 2 or weight.dim() != (2 if offsets is None else 3) or weight.dtype is not torch.bfloat16 \
+                or not weight.is_contiguous() or weight.get_device() != dev or groups < (offsets is not None) \
+                or (groups and weight.shape[0] != groups):
+            raise ValueError("%s: need a two-dimensional input and a contiguous bfloat16 weight %s on the current CUDA "
+                             "device, got %s and %s %s on %s" % (name, "(m, n)" if offsets is None else
+                                                                 "(%d, m, n)" % groups, tuple(x.shape), weight.dtype,
+                                                                 tuple(weight.shape), weight.device))
+        tokens, (m, n) = x.shape[0], weight.shape[-2:]
+        px, lx = _mat(x, tokens, m if dgrad else n, torch.bfloat16, dev, "dy" if dgrad else "x")
+        po, lo = _mat(out, tokens, n if dgrad else m, torch.bfloat16, dev, "dx" if dgrad else "out")
+        _check(getattr(self.lib, name)(self.handle, px, lx, weight.data_ptr(), tokens, m, n,
+                                       _vec(offsets, groups + 1, dev, "offsets", torch.int32), groups, po, lo,
+                                       _stream(stream, dev)), name)
+
+    def product(self, x, weight, out, offsets=None, stream=None):
+        """``muon_product``: out (tokens, m) = x (tokens, n) W^T, bfloat16, weight (m, n); with ``offsets`` (groups + 1
+        int32, on the device) weight is (groups, m, n), one per range of tokens, and rows outside them are left."""
+        self._product("muon_product", x, weight, out, offsets, False, stream)
+
+    def dgrad(self, dy, weight, dx, offsets=None, stream=None):
+        """``muon_dgrad``: dx (tokens, n) = dy (tokens, m) W, the gradient of ``product``'s input."""
+        self._product("muon_dgrad", dy, weight, dx, offsets, True, stream)
+
+    def grad_norm(self, grads, norm, stream=None):
+        """``muon_grad_norm``: norm (one float32, on the device) of all gradients of ``grads`` (a ``GradList`` or
+        tensors) together."""
+        dev = torch.cuda.current_device()
+        g = _grads(grads, dev, "grad_norm")
+        _check(self.lib.muon_grad_norm(self.handle, g.pointers, g.counts, g.dtypes, g.n, _vec(norm, 1, dev, "norm"),
+                                       _stream(stream, dev)), "muon_grad_norm")
+
+    def grad_clip(self, grads, norm, max_norm: float, out=None, stream=None):
+        """``muon_grad_clip``: the gradients times max_norm / norm where norm > max_norm, in place or into the
+        tensors of ``out``, which may be of the other type."""
+        dev = torch.cuda.current_device()
+        g = _grads(grads, dev, "grad_clip")
+        o = None if out is None else _grads(out, dev, "grad_clip")
+        if o is not None and bytes(o.counts) != bytes(g.counts):
+            raise ValueError("out: need tensors of the gradients' sizes")
+        _check(self.lib.muon_grad_clip(self.handle, g.pointers, g.counts, g.dtypes, g.n, _vec(norm, 1, dev, "norm"),
+                                       max_norm, None if o is None else o.pointers, None if o is None else o.dtypes,
+                                       _stream(stream, dev)), "muon_grad_clip")

@@ -19,8 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmuon_gb300.so")
 SOURCES = ["plan.cu", "step.cu", "capi.cu", "gemm.cu", "ns_small.cu", "ns_f32.cu", "elementwise.cu", "noalloc.cu",
-           "acts.cu", "act_elementwise.cu", "rmsnorm.cu", "wgrad.cu"]
-HEADERS = ["kernels.h", "plan.h", "ptx.cuh", "gemm_common.cuh", "acts.h", "act8.cuh"]
+           "acts.cu", "act_elementwise.cu", "rmsnorm.cu", "wgrad.cu", "product.cu", "experts.cu", "gradnorm.cu"]
+HEADERS = ["kernels.h", "plan.h", "ptx.cuh", "gemm_common.cuh", "acts.h", "act8.cuh", "grads.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE] + ARCH
 

@@ -22,6 +22,31 @@ namespace muon {
 constexpr int kSeg = 256;
 enum { kByValue = 0, kAligned = 1, kShifted = 2 };   // the first two convert from `rows are aligned`
 
+// Segments in flight per warp of the elementwise kernels: with one the loads do not cover HBM's latency (an
+// earlier SwiGLU forward kernel took 250 us, 222 with two), with four the registers leave too few warps (277).
+constexpr int kUnroll = 2;
+
+// Units of this warp: row and first column of each, in steps of the launch's warps without a
+// division per step.  Most lie inside the row and need no masks: they run as FULL.
+template <int THREADS>
+struct RowWalk {
+    static constexpr int kWidth = kUnroll * kSeg;
+    uint32_t row, drow;   // below 2^31 each
+    int col, dcol, width;
+    __device__ __forceinline__ RowWalk(int cols) {
+        const int units = (cols + kWidth - 1) / kWidth;
+        const uint32_t w = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
+        const uint32_t n = gridDim.x * (THREADS / 32);
+        row = w / units, col = (int)(w - row * units) * kWidth;
+        drow = n / units, dcol = (int)(n - drow * units) * kWidth;
+        width = units * kWidth;
+    }
+    __device__ __forceinline__ void next() {
+        row += drow, col += dcol;
+        if (col >= width) col -= width, ++row;
+    }
+};
+
 template <bool VEC>
 __device__ __forceinline__ int seg_col(int lane, int j) {
     return VEC ? 8 * lane + j : 32 * j + lane;
@@ -135,24 +160,16 @@ __device__ __forceinline__ void seg_load(const void* p, int c0, int cols, int la
     raw.get(v);
 }
 
-// Stores the segment's values below `cols`.  Every lane of the warp takes part.  Shifted: a lane stores
-// the aligned piece (fp32: two) that begins in the lane below it, with the values that reach into it
-// from there; the segment's ragged ends go value by value.
+// Stores the segment's values below `cols` as their words (bf16 in pairs, or fp32; not by value).  Every lane
+// of the warp takes part.  Shifted: a lane stores the aligned piece (fp32: two) that begins in the lane below
+// it, with the values that reach into it from there; the segment's ragged ends go value by value.
 template <bool BF16, int MODE, bool FULL = false>
-__device__ __forceinline__ void seg_store(void* p, int c0, int cols, int lane, const float (&v)[8]) {
-    if constexpr (MODE == kByValue) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = c0 + seg_col<false>(lane, j);
-            if (c < cols) store_one<BF16>(p, c, v[j]);
-        }
-        return;
-    }
-    if (MODE == kShifted && !FULL && c0 + kSeg <= cols) return seg_store<BF16, MODE, true>(p, c0, cols, lane, v);
+__device__ __forceinline__ void seg_store_words(void* p, int c0, int cols, int lane,
+                                                const uint32_t (&own)[BF16 ? 4 : 8]) {
+    static_assert(MODE != kByValue, "values in pairs");
+    if (MODE == kShifted && !FULL && c0 + kSeg <= cols)
+        return seg_store_words<BF16, MODE, true>(p, c0, cols, lane, own);
     constexpr int kWords = BF16 ? 4 : 8, kSize = BF16 ? 2 : 4;
-    uint32_t own[kWords];
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) own[i] = BF16 ? bf16_pair(v[2 * i], v[2 * i + 1]) : __float_as_uint(v[i]);
     const int c = c0 + 8 * lane;
     char* at = static_cast<char*>(p) + (long long)c * kSize;
     auto one = [&](char* to, uint32_t word, int j) {
@@ -207,6 +224,23 @@ __device__ __forceinline__ void seg_store(void* p, int c0, int cols, int lane, c
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (c - back + j < cols) one(at - shift, w[BF16 ? j >> 1 : j], j);
+    }
+}
+// The same for values in fp32.
+template <bool BF16, int MODE, bool FULL = false>
+__device__ __forceinline__ void seg_store(void* p, int c0, int cols, int lane, const float (&v)[8]) {
+    if constexpr (MODE == kByValue) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = c0 + seg_col<false>(lane, j);
+            if (c < cols) store_one<BF16>(p, c, v[j]);
+        }
+    } else {
+        constexpr int kWords = BF16 ? 4 : 8;
+        uint32_t own[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) own[i] = BF16 ? bf16_pair(v[2 * i], v[2 * i + 1]) : __float_as_uint(v[i]);
+        seg_store_words<BF16, MODE, FULL>(p, c0, cols, lane, own);
     }
 }
 

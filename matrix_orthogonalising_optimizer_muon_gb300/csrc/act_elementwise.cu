@@ -22,31 +22,9 @@ constexpr int kThreads = 256;
 // eight), SwiGLU backward 337 us with four (376 with five).
 constexpr int kFit = 8, kFitForward = 4, kFitBackward = 5;
 constexpr int kSms = 152;
-// Segments in flight per warp: with one the loads do not cover HBM's latency (an earlier forward kernel
-// took 250 us, 222 with two), with four the registers leave too few warps (277).
-constexpr int kUnroll = 2;
+using Walk = RowWalk<kThreads>;
 template <bool VEC>
 constexpr int kMode = VEC ? kAligned : kShifted;
-
-// Units of this warp: row and first column of each, in steps of the launch's warps without a
-// division per step.  Most lie inside the row and need no masks: they run as FULL.
-struct Walk {
-    static constexpr int kWidth = kUnroll * kSeg;
-    uint32_t row, drow;   // below 2^31 each
-    int col, dcol, width;
-    __device__ __forceinline__ Walk(int cols) {
-        const int units = (cols + kWidth - 1) / kWidth;
-        const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-        const uint32_t n = gridDim.x * (kThreads / 32);
-        row = w / units, col = (int)(w - row * units) * kWidth;
-        drow = n / units, dcol = (int)(n - drow * units) * kWidth;
-        width = units * kWidth;
-    }
-    __device__ __forceinline__ void next() {
-        row += drow, col += dcol;
-        if (col >= width) col -= width, ++row;
-    }
-};
 
 template <bool BF16, bool VEC, bool FULL>
 __device__ __forceinline__ void unit_act_pack(const PackArgs& a, const Walk& w, int lane) {

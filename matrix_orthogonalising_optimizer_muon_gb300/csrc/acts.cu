@@ -1,6 +1,7 @@
 // C entry points of the layer-side operators (include/muon.h): argument checks, the grad
 // plan, launches.  Host code only.
 #include "acts.h"
+#include "grads.h"
 #include "plan.h"
 
 struct muon_grad_plan_s {
@@ -8,6 +9,8 @@ struct muon_grad_plan_s {
     int sm_count = 0;
     void* ws = nullptr;       // status word, counters, partial sums
     int* status = nullptr;
+    int* arrived = nullptr;     // blocks of the norm in progress
+    double* running = nullptr;  // squares of the norm's launches so far
     int* counters = nullptr;
     float* partial = nullptr;
 };
@@ -20,6 +23,7 @@ constexpr int64_t kGradWorkspace = (int64_t)kWsHeader + kPartialFloats * 4;
 static_assert(kWsHeader % 256 == 0, "the partial sums are aligned");
 
 constexpr int64_t kMostPitch = 1ll << 32;   // bytes from row to row
+constexpr int64_t kMostValues = 1ll << 43;  // of a list of gradients
 
 // A strided range of device memory: `rows` rows of `width` bytes, `pitch` bytes apart.
 struct Range {
@@ -136,6 +140,89 @@ muon_status check_grad_plan(const muon_grad_plan_s* p) {
         const muon_status st__ = (expr);      \
         if (st__ != MUON_OK) return st__;     \
     } while (0)
+
+constexpr int kMostExperts = 4096;
+constexpr int kMostChoices = 64;
+
+// The moves between the tokens' order and the experts': c's rows are the tokens'.
+muon_status begin_move(Call* c, int64_t tokens, int32_t choices, int64_t rows, int64_t cols, muon_dtype dtype) {
+    MUON_CALL(begin(c, tokens, cols, dtype, kMaxDim));
+    if (choices < 1 || choices > kMostChoices || rows < 0) return MUON_ERR_INVALID_ARG;
+    if (tokens * choices >= (1ll << 31) || rows >= (1ll << 31)) return MUON_ERR_UNSUPPORTED;
+    return MUON_OK;
+}
+void set_move(MoveArgs* a, const int32_t* slots, const float* weights, int64_t tokens, int32_t choices, int64_t rows,
+              int64_t cols) {
+    a->slots = slots, a->weights = weights, a->tokens = (uint32_t)tokens, a->rows = (uint32_t)rows;
+    a->choices = choices, a->cols = (int)cols;
+}
+
+muon_status product(muon_grad_plan_s* p, const void* x, int64_t ldx, const void* weight, int64_t tokens, int64_t m,
+                    int64_t n, const int32_t* offsets, int32_t groups, void* y, int64_t ldy, bool transposed,
+                    void* stream) {
+    Call cx, cy;
+    ProductArgs a{};
+    Mat mat{};
+    MUON_CALL(begin(&cx, tokens, transposed ? m : n, MUON_BF16, kMaxDim));
+    MUON_CALL(begin(&cy, tokens, transposed ? n : m, MUON_BF16, kMaxDim));
+    if (!p || groups < 0 || groups > kMostExperts || (groups > 0) != (offsets != nullptr)) return MUON_ERR_INVALID_ARG;
+    cx.mat(&mat, x, ldx, false, tokens == 0);
+    if (!cx.ok) return MUON_ERR_INVALID_ARG;
+    cy.ops.add(x, tokens, cx.cols * 2, ldx * 2, false);
+    cy.mat(&mat, y, ldy, true, tokens == 0);
+    cy.vector(offsets, groups ? groups + 1 : 0, false, true);
+    cy.ok = cy.ok && weight && (reinterpret_cast<uintptr_t>(weight) & 1) == 0;
+    cy.ops.add(weight, (long long)std::max(groups, 1) * m, n * 2, n * 2, false);
+    MUON_CALL(cy.status());
+    MUON_CALL(check_grad_plan(p));
+    if (tokens == 0) return MUON_OK;
+    a.x = x, a.ldx = ldx, a.weight = weight, a.y = y, a.ldy = ldy, a.tokens = tokens, a.m = (int)m, a.n = (int)n;
+    a.transposed = transposed, a.offsets = offsets, a.groups = std::max(groups, 1);
+    a.status = p->status, a.partial = p->partial, a.counters = p->counters;
+    return cuda_status(launch_product(a, p->sm_count, static_cast<cudaStream_t>(stream)));
+}
+
+muon_status check_list(const void* const* p, const int64_t* counts, const int32_t* dtypes, int32_t n) {
+    if (n < 0 || (n > 0 && (!p || !counts || !dtypes))) return MUON_ERR_INVALID_ARG;
+    int64_t left = kMostValues;
+    for (int i = 0; i < n; ++i) {
+        if (dtypes[i] != MUON_F32 && dtypes[i] != MUON_BF16) return MUON_ERR_UNSUPPORTED;
+        if (counts[i] < 0) return MUON_ERR_INVALID_ARG;
+        if (counts[i] > left) return MUON_ERR_UNSUPPORTED;
+        left -= counts[i];
+        if (counts[i] > 0 && (!p[i] || (reinterpret_cast<uintptr_t>(p[i]) & (dtypes[i] == MUON_BF16 ? 1 : 3))))
+            return MUON_ERR_INVALID_ARG;
+    }
+    return MUON_OK;
+}
+
+// Whether a tensor that is written overlaps another one or the norm; out null: the gradients are written.
+bool lists_overlap(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int32_t n, void* const* out,
+                   const int32_t* out_dtypes, const float* norm) {
+    struct Span {
+        uintptr_t from, to;
+        int index;      // a tensor that is its own output counts once
+        bool written;
+    };
+    std::vector<Span> spans;
+    spans.reserve(2 * (size_t)n + 1);
+    spans.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, -1, false});
+    for (int i = 0; i < n; ++i) {
+        if (counts[i] == 0) continue;
+        const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
+        const uintptr_t o = out ? reinterpret_cast<uintptr_t>(out[i]) : g;
+        const int32_t od = out ? out_dtypes[i] : dtypes[i];
+        spans.push_back({o, o + (uintptr_t)counts[i] * (od == MUON_BF16 ? 2 : 4), i, true});
+        if (o != g || od != dtypes[i]) spans.push_back({g, g + (uintptr_t)counts[i] * (dtypes[i] == MUON_BF16 ? 2 : 4), i, false});
+    }
+    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.from < b.from; });
+    uintptr_t read_to = 0, written_to = 0;   // ends of what came before
+    for (const Span& s : spans) {
+        if (s.from < written_to || (s.written && s.from < read_to)) return true;
+        (s.written ? written_to : read_to) = std::max(s.written ? written_to : read_to, s.to);
+    }
+    return false;
+}
 
 }  // namespace
 
@@ -257,6 +344,8 @@ muon_status muon_grad_plan_create(muon_grad_plan* out) {
         return st;
     }
     p->status = static_cast<int*>(p->ws);
+    p->arrived = p->status + 1;
+    p->running = reinterpret_cast<double*>(p->status + 2);
     p->counters = reinterpret_cast<int*>(static_cast<char*>(p->ws) + 256);
     p->partial = reinterpret_cast<float*>(static_cast<char*>(p->ws) + kWsHeader);
     *out = p;
@@ -332,6 +421,113 @@ muon_status muon_wgrad(muon_grad_plan p, const void* dy, int64_t lddy, const muo
     a.grad = grad, a.accumulate = accumulate != 0, a.status = p->status;
     a.partial = p->partial, a.counters = p->counters;
     return cuda_status(launch_wgrad(a, grad_dtype == MUON_BF16, p->sm_count, static_cast<cudaStream_t>(stream)));
+}
+
+muon_status muon_product(muon_grad_plan p, const void* x, int64_t ldx, const void* weight, int64_t tokens, int64_t m,
+                         int64_t n, const int32_t* offsets, int32_t groups, void* y, int64_t ldy, void* stream) {
+    return product(p, x, ldx, weight, tokens, m, n, offsets, groups, y, ldy, false, stream);
+}
+
+muon_status muon_dgrad(muon_grad_plan p, const void* dy, int64_t lddy, const void* weight, int64_t tokens, int64_t m,
+                       int64_t n, const int32_t* offsets, int32_t groups, void* dx, int64_t lddx, void* stream) {
+    return product(p, dy, lddy, weight, tokens, m, n, offsets, groups, dx, lddx, true, stream);
+}
+
+muon_status muon_expert_order(const int32_t* ids, int64_t tokens, int32_t choices, int32_t experts, int32_t* offsets,
+                              int32_t* slots, void* stream) {
+    Call c;
+    MUON_CALL(begin_move(&c, tokens, choices, 0, 1, MUON_F32));
+    if (experts < 1 || experts > kMostExperts) return MUON_ERR_INVALID_ARG;
+    const long long n = (long long)tokens * choices;
+    c.vector(ids, n, false, n == 0);
+    c.vector(offsets, experts + 1, true, false);
+    c.vector(slots, n, true, n == 0);
+    MUON_CALL(c.status());
+    OrderArgs a{ids, n, experts, offsets, slots};
+    return cuda_status(launch_expert_order(a, static_cast<cudaStream_t>(stream)));
+}
+
+muon_status muon_expert_dispatch(const void* x, int64_t ldx, const int32_t* slots, int64_t tokens, int32_t choices,
+                                 int64_t rows, int64_t cols, muon_dtype dtype, void* out, int64_t ldo, void* stream) {
+    Call c;
+    MoveArgs a{};
+    MUON_CALL(begin_move(&c, tokens, choices, rows, cols, dtype));
+    c.mat(&a.x, x, ldx, false, tokens == 0);
+    c.rows = rows;
+    c.mat(&a.y, out, ldo, true, rows == 0);
+    c.vector(slots, (long long)tokens * choices, false, tokens == 0);
+    MUON_CALL(c.status());
+    if (tokens == 0 || rows == 0) return MUON_OK;
+    set_move(&a, slots, nullptr, tokens, choices, rows, cols);
+    return cuda_status(launch_expert_dispatch(a, dtype == MUON_BF16, c.vec, static_cast<cudaStream_t>(stream)));
+}
+
+muon_status muon_expert_combine(const void* expert_rows, int64_t ldr, const int32_t* slots, const float* weights,
+                                int64_t tokens, int32_t choices, int64_t rows, int64_t cols, muon_dtype dtype, void* out,
+                                int64_t ldo, void* stream) {
+    Call c;
+    MoveArgs a{};
+    MUON_CALL(begin_move(&c, tokens, choices, rows, cols, dtype));
+    c.mat(&a.x, out, ldo, true, tokens == 0);
+    c.rows = rows;
+    c.mat(&a.y, expert_rows, ldr, false, rows == 0);
+    c.vector(slots, (long long)tokens * choices, false, tokens == 0);
+    c.vector(weights, (long long)tokens * choices, false, true);
+    MUON_CALL(c.status());
+    if (tokens == 0) return MUON_OK;
+    set_move(&a, slots, weights, tokens, choices, rows, cols);
+    return cuda_status(launch_expert_combine(a, dtype == MUON_BF16, c.vec, static_cast<cudaStream_t>(stream)));
+}
+
+muon_status muon_expert_combine_backward(const void* dout, int64_t ldd, const int32_t* slots, const float* weights,
+                                         const void* expert_rows, int64_t ldr, int64_t tokens, int32_t choices,
+                                         int64_t rows, int64_t cols, muon_dtype dtype, void* drows, int64_t lddr,
+                                         float* dweights, void* stream) {
+    Call c;
+    MoveArgs a{};
+    MUON_CALL(begin_move(&c, tokens, choices, rows, cols, dtype));
+    if (tokens > 0 && ((!drows && !dweights) || (dweights && !expert_rows && rows > 0))) return MUON_ERR_INVALID_ARG;
+    c.mat(&a.x, dout, ldd, false, tokens == 0);
+    c.rows = rows;
+    c.mat(&a.y, expert_rows, ldr, false, true);
+    c.mat(&a.dy, drows, lddr, true, true);
+    c.vector(slots, (long long)tokens * choices, false, tokens == 0);
+    c.vector(weights, (long long)tokens * choices, false, tokens == 0);
+    c.vector(dweights, (long long)tokens * choices, true, true);
+    MUON_CALL(c.status());
+    if (tokens == 0) return MUON_OK;
+    set_move(&a, slots, weights, tokens, choices, rows, cols);
+    a.dweights = dweights;
+    return cuda_status(launch_expert_combine_backward(a, dtype == MUON_BF16, c.vec, static_cast<cudaStream_t>(stream)));
+}
+
+muon_status muon_grad_norm(muon_grad_plan p, const void* const* grads, const int64_t* counts, const int32_t* dtypes,
+                           int32_t n, float* norm, void* stream) {
+    if (!p || !norm || (reinterpret_cast<uintptr_t>(norm) & 3)) return MUON_ERR_INVALID_ARG;
+    MUON_CALL(check_list(grads, counts, dtypes, n));
+    MUON_CALL(check_grad_plan(p));
+    const GradList l{grads, counts, dtypes, nullptr, nullptr, n, false};
+    const GradNormArgs a{reinterpret_cast<double*>(p->partial), p->running, p->arrived, norm, p->sm_count};
+    return cuda_status(launch_grad_norm(l, a, static_cast<cudaStream_t>(stream)));
+}
+
+muon_status muon_grad_clip(muon_grad_plan p, const void* const* grads, const int64_t* counts, const int32_t* dtypes,
+                           int32_t n, const float* norm, float max_norm, void* const* out, const int32_t* out_dtypes,
+                           void* stream) {
+    if (!p || !norm || (reinterpret_cast<uintptr_t>(norm) & 3) || !std::isfinite(max_norm) || max_norm <= 0.f ||
+        (out == nullptr) != (out_dtypes == nullptr))
+        return MUON_ERR_INVALID_ARG;
+    MUON_CALL(check_list(grads, counts, dtypes, n));
+    if (out) MUON_CALL(check_list(const_cast<const void* const*>(out), counts, out_dtypes, n));
+    try {
+        if (lists_overlap(grads, counts, dtypes, n, out, out_dtypes, norm)) return MUON_ERR_INVALID_ARG;
+    } catch (const std::bad_alloc&) {
+        return MUON_ERR_OOM;
+    }
+    MUON_CALL(check_grad_plan(p));
+    const GradList l{grads, counts, dtypes, out ? out : const_cast<void* const*>(grads), out ? out_dtypes : dtypes, n,
+                     out == nullptr};
+    return cuda_status(launch_grad_clip(l, norm, max_norm, p->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -83,6 +83,43 @@ struct WgradArgs {
 constexpr int kMaxParts = 240;   // parts of split tiles
 constexpr int kMaxPairs = 76;    // CTA pairs, one tile of bf16 gradients' running sums each
 
+// The experts' order of tokens.
+struct OrderArgs {
+    const int* ids;      // n of them, tokens x choices
+    long long n;
+    int experts;
+    int* offsets;        // experts + 1
+    int* slots;          // n
+};
+
+// Rows moved between the tokens' order and the experts'.
+struct MoveArgs {
+    Mat x;               // the tokens' side
+    Mat y;               // the experts' side
+    Mat dy;              // combine backward: its gradient, or null
+    const int* slots;    // tokens x choices
+    const float* weights;   // tokens x choices, or null: ones
+    float* dweights;     // combine backward, or null
+    uint32_t tokens, rows;  // rows of y
+    int choices, cols;
+};
+
+struct ProductArgs {
+    const void* x;       // tokens x k bf16, row pitch ldx elements
+    long long ldx;
+    const void* weight;  // groups x m x n bf16, dense
+    void* y;             // tokens x out bf16, row pitch ldy
+    long long ldy;
+    long long tokens;
+    int m, n;
+    bool transposed;     // y = x W (k = m, out = n), else y = x W^T (k = n, out = m)
+    const int* offsets;  // groups + 1, or null
+    int groups;          // >= 1
+    int* status;
+    float* partial;
+    int* counters;
+};
+
 // bf16: the dtype of the Mat operands; vec: every one of them (and ld) 16-byte aligned.
 cudaError_t launch_act_pack(const PackArgs& a, bool bf16, bool vec, cudaStream_t s);
 cudaError_t launch_act_unpack(const PackArgs& a, bool bf16, bool vec, cudaStream_t s);
@@ -97,6 +134,11 @@ constexpr long long kPartialFloats = (kMaxParts + kMaxPairs) * 65536ll;   // of 
 static_assert(kPartialFloats >= kNormPartialFloats, "one region serves both");
 cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a, bool bf16, bool vec, int sm_count, cudaStream_t s);
 cudaError_t wgrad_prepare();   // once per device, before the first launch
+cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s);
+cudaError_t launch_expert_dispatch(const MoveArgs& a, bool bf16, bool vec, cudaStream_t s);
+cudaError_t launch_expert_combine(const MoveArgs& a, bool bf16, bool vec, cudaStream_t s);
+cudaError_t launch_expert_combine_backward(const MoveArgs& a, bool bf16, bool vec, cudaStream_t s);
+cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaStream_t s);
 
 }  // namespace muon

@@ -1,0 +1,70 @@
+// Lists of gradients as the norm and the clipping take them.  Host entry points in acts.cu,
+// kernels in gradnorm.cu.
+#pragma once
+#include <algorithm>
+
+#include "acts.h"
+
+namespace muon {
+
+// A gradient is walked in groups of eight values, the first of which may begin before it so that every
+// whole group is aligned to 16 bytes on the side that is written (the norm: read), in chunks of
+// kChunkGroups groups, one per block and turn.
+constexpr int kChunkGroups = 1024;
+
+struct GradEntry {
+    const void* p;
+    void* out;               // clip
+    long long count;
+    uint32_t first;          // first chunk
+    uint8_t bf16, out_bf16;
+    uint16_t pad;            // values by which the first group begins before the gradient
+};
+
+// Parameters of one launch: at most 32764 bytes, the few for short lists.
+constexpr int kTableFew = 30, kTableMost = 1000;
+template <int N>
+struct GradTable {
+    GradEntry e[N];
+    int n;
+    uint32_t chunks;
+};
+
+struct GradList {
+    const void* const* p;
+    const int64_t* counts;
+    const int32_t* dtypes;       // 0 fp32, 1 bf16
+    void* const* out;            // null: the norm alone
+    const int32_t* out_dtypes;
+    int n;
+    bool in_place;
+
+    template <int N>
+    void table(int from, int to, GradTable<N>* t) const {
+        t->n = to - from;
+        long long chunks = 0;
+        for (int i = from; i < to; ++i) {
+            GradEntry& e = t->e[i - from];
+            e.p = p[i], e.out = out ? out[i] : nullptr, e.count = counts[i];
+            e.bf16 = dtypes[i] == 1, e.out_bf16 = out ? out_dtypes[i] == 1 : 0;
+            const uintptr_t at = reinterpret_cast<uintptr_t>(out ? e.out : e.p);
+            const int esz = (out ? e.out_bf16 : e.bf16) ? 2 : 4;
+            e.pad = (uint16_t)((at & 15) / esz);
+            e.first = (uint32_t)chunks;
+            if (counts[i] > 0) chunks += ((counts[i] + e.pad + 7) / 8 + kChunkGroups - 1) / kChunkGroups;
+        }
+        t->chunks = (uint32_t)chunks;
+    }
+};
+
+struct GradNormArgs {
+    double* partial;   // a sum per block
+    double* running;   // the sum of the launches so far
+    int* arrived;      // zero between calls
+    float* norm;
+    int sm_count;
+};
+cudaError_t launch_grad_norm(const GradList& l, const GradNormArgs& a, cudaStream_t s);
+cudaError_t launch_grad_clip(const GradList& l, const float* norm, float max_norm, int sm_count, cudaStream_t s);
+
+}  // namespace muon
