@@ -336,6 +336,7 @@ muon_status muon_grad_plan_create(muon_grad_plan* out) {
     }
     if (st == MUON_OK) st = cuda_status(wgrad_prepare());
     if (st == MUON_OK) st = cuda_status(rmsnorm_prepare());
+    if (st == MUON_OK) st = cuda_status(product_prepare());
     if (st == MUON_OK) st = cuda_status(cudaMemset(p->ws, 0, kWsHeader));
     if (st == MUON_OK) st = cuda_status(cudaDeviceSynchronize());
     if (st != MUON_OK) {

@@ -138,6 +138,7 @@ cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s);
 cudaError_t launch_expert_dispatch(const MoveArgs& a, bool bf16, bool vec, cudaStream_t s);
 cudaError_t launch_expert_combine(const MoveArgs& a, bool bf16, bool vec, cudaStream_t s);
 cudaError_t launch_expert_combine_backward(const MoveArgs& a, bool bf16, bool vec, cudaStream_t s);
+cudaError_t product_prepare();   // once per device, before the first launch
 cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaStream_t s);
 
