@@ -18,7 +18,7 @@ struct muon_grad_plan_s {
 namespace {
 using namespace muon_impl;
 
-constexpr size_t kWsHeader = 256 + kMaxParts * 4 * sizeof(int);   // status word, counters
+constexpr size_t kWsHeader = 256 + kCounters * sizeof(int);   // status word, counters
 constexpr int64_t kGradWorkspace = (int64_t)kWsHeader + kPartialFloats * 4;
 static_assert(kWsHeader % 256 == 0, "the partial sums are aligned");
 

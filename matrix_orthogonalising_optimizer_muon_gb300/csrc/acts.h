@@ -78,9 +78,10 @@ struct WgradArgs {
     int accumulate;
     int* status;
     float* partial;      // kMaxParts + kMaxPairs tiles of 256 x 256 sums
-    int* counters;       // kMaxParts * 4 words, zero between calls
+    int* counters;       // kCounters words, zero between calls
 };
 constexpr int kMaxParts = 240;   // parts of split tiles
+constexpr int kCounters = 1280;  // of parts that have arrived: 4 per part of a split tile, or 16 per CTA pair
 constexpr int kMaxPairs = 76;    // CTA pairs, one tile of bf16 gradients' running sums each
 
 // The experts' order of tokens.

@@ -9,15 +9,16 @@
 //
 // A cluster of two CTAs computes tiles of 256 outputs x up to 256 tokens (tcgen05.mma.cta_group::2, fp32
 // accumulators in TMEM, double-buffered).  Per CTA: warp 0 issues the TMA loads, warp 1 the MMAs (the
-// even CTA's), warps 2-5 are the epilogue; where rows are not 16-byte aligned, 16 more warps copy them into
+// even CTA's), warps 2-9 are the epilogue; where rows are not 16-byte aligned, 16 more warps copy them into
 // shared memory instead of TMA.  A step is 64 values of the contraction: 16 KB of the weight and up to
 // 16 KB of tokens per CTA, in a ring of six.
 //
 // How the work is dealt out (every CTA derives the same plan from the offsets): tiles in the order experts,
-// bands of kBand token tiles, outputs, token tiles, so that the tiles in flight share operands in L2.  All but
-// the last turns of long launches go round the CTA pairs; what is left is cut into stretches of equal
-// cost, one per pair, that may begin and end inside a tile's sum.  Such tiles' partial sums meet in the
-// workspace, and the part that comes last adds them up in their order.
+// bands of kBand token tiles, outputs, token tiles, one per CTA pair and turn, so that the tiles in flight share
+// operands in L2.  (A contiguous run of tiles per pair balances ragged experts better, but each operand is then
+// read again a whole tile later, when L2 has lost it: 102 us against 64 for the 32 experts below.)  The last,
+// incomplete turn may be cut along the contraction; its partial sums meet in the workspace, and the part that
+// comes last adds them up in their order.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -33,30 +34,49 @@ namespace {
 
 constexpr int kStepK = 64;
 constexpr int kRing = 6;
-constexpr int kEpiFirst = 2, kEpi = 4;             // epilogue warps
-constexpr int kCopyFirst = kEpiFirst + kEpi;
+constexpr int kEpiFirst = 2;
 constexpr int kCopyGroups = 4, kGroupWarps = 4;    // copying warps: groups that take steps in turn
+// Epilogue warps: two for each quarter of the TMEM lanes, on alternate blocks of 32 tokens; one where the copying
+// warps leave no registers for more.
 template <bool COPY>
-constexpr int kThreadsOf = 32 * (kCopyFirst + (COPY ? kCopyGroups * kGroupWarps : 0));
+struct Roles {
+    static constexpr int kEpi = COPY ? 4 : 8;
+    static constexpr int kCopyFirst = kEpiFirst + kEpi;
+    static constexpr int kThreads = 32 * (kCopyFirst + (COPY ? kCopyGroups * kGroupWarps : 0));
+};
 constexpr int kBand = 8;
 constexpr int kBins = 512;                         // experts are searched in at most this many bins
 constexpr int kItems = 96;                         // items decoded at the start
-constexpr int kMostPairs = 76;
 
 struct Cfg {
     static constexpr int A_BYTES = 128 * kStepK * 2;
     static constexpr int CHUNK_BYTES = 64 * kStepK * 2;   // 64 outputs of an MN-major weight
     static constexpr int SLOT_BYTES = 2 * A_BYTES;
     static constexpr int OUT_OFFSET = kRing * SLOT_BYTES;
-    static constexpr int OUT_WARP = 2 * 2048;             // two blocks of 32 outputs x 32 tokens in bf16
-    static constexpr int BAR_OFFSET = OUT_OFFSET + kEpi * OUT_WARP;
+    static constexpr int OUT_WARP = 2048;                 // 32 outputs x 32 tokens in bf16
+    static constexpr int BAR_OFFSET = OUT_OFFSET + 8 * OUT_WARP;
     static constexpr int SIGNAL_OFFSET = BAR_OFFSET + 256;   // 16 bytes per copying warp
     static constexpr int PLAN_OFFSET = SIGNAL_OFFSET + 256;
-    static constexpr int ITEM_OFFSET = PLAN_OFFSET + 2 * (kBins + 4) * 4 + 2 * (kMostPairs + 4) * 4 + 64;
+    static constexpr int ITEM_OFFSET = PLAN_OFFSET + 4 * kBins * 4 + 2 * kBins * 2 + 416;
     static constexpr int SMEM_BYTES = ITEM_OFFSET + kItems * 32 + 1024;
 };
 static_assert(Cfg::SMEM_BYTES <= 232448, "product kernel exceeds the shared memory of one CTA");
 static_assert(Cfg::ITEM_OFFSET % 16 == 0, "items are loaded 16 bytes at a time");
+
+// Division of whole numbers below 2^31 by a divisor known at launch, as in wgrad.cu.
+struct Divisor {
+    uint32_t d, m;
+    int s;
+    __host__ void set(uint32_t divisor) {
+        d = divisor;
+        s = 0;
+        while ((1ull << s) < d) ++s;
+        m = (uint32_t)(((((1ull << s) - d) << 32) / d) + 1);
+    }
+    __device__ __forceinline__ int div(int n) const {
+        return (int)(((unsigned long long)(uint32_t)n + __umulhi((uint32_t)n, m)) >> s);
+    }
+};
 
 struct ProductLaunch {
     CUtensorMap map_w, map_x[4];   // map_x: boxes of 128, 64, 32 and 16 tokens
@@ -64,20 +84,28 @@ struct ProductLaunch {
     int out, k, steps, tiles_m;    // outputs, contraction, its steps, tiles along the outputs
     int tma_w, tma_x;              // rows are aligned to 16 bytes
     int wide;                      // rows of y are aligned to four elements
+    Divisor by_tiles;              // by tiles_m
+    int tiles[3];                  // one weight: token tiles when they are at most 256, 128, 64 tokens high
 };
 
-// The launch's plan in shared memory.
+// The launch's plan in shared memory.  Where there is more than one turn, experts are placed by decreasing height
+// of their tiles (when they are at most kBins): the turns' tiles are then alike, and the last turn's are the lowest.
 struct Plan {
-    int tiles[kBins + 4];      // token tiles before each bin of experts
-    int cost[kBins + 4];       // their cost
-    int unit[kMostPairs + 4];  // begins of the pairs' stretches: tile and step
-    int step[kMostPairs + 4];
-    int count[4];              // token tiles when they are 256, 128, 64 tokens high
-    int cap, stride, turns, pairs;   // tile height, experts per bin, whole turns, stretches
-    int units;
-    int pad[7];
+    int tiles[kBins + 4];                     // token tiles before the expert, or the bin of experts, at each place
+    int begin[kBins], end[kBins], count[kBins];   // of each expert (at most kBins): tokens and tiles
+    uint16_t height[kBins], order[kBins];     // of each expert; the expert at each place
+    int start[kMaxPairs + 4];   // begins of the pairs' stretches, in steps from the first tile of the last turn
+    int next[12];                // places of the heights while they are dealt out
+    int sums[4];                 // token tiles when they are at most 256, 128, 64 tokens high
+    int pairs, pad[3];           // stretches
 };
 static_assert(sizeof(Plan) == Cfg::ITEM_OFFSET - Cfg::PLAN_OFFSET, "plan's place");
+
+// What every thread knows of the plan.
+struct Outline {
+    int cap, units, turns, stretches;   // greatest height of a tile, tiles, whole turns, stretches
+    int stride, bins;                   // experts per bin of Plan::tiles
+};
 
 struct __align__(16) Item {
     int m0, t0, end, group;    // first output, first token, end of the expert's tokens
@@ -85,223 +113,231 @@ struct __align__(16) Item {
     int part;                  // parts << 16 | part << 8 | first pair; 0: the whole sum
 };
 
-// Cost of a tile's step, in 32 cycles: the weight's 16 KB take as long as 256 tokens' MMAs do.
-__device__ __forceinline__ int tile_cost(int n) { return 8 + (n >> 5); }
-
 __device__ __forceinline__ void expert_range(const ProductArgs& a, int g, int* begin, int* end) {   // tokens < 2^31
     *begin = a.offsets ? min(max(a.offsets[g], 0), (int)a.tokens) : 0;
     *end = a.offsets ? min(max(a.offsets[g + 1], *begin), (int)a.tokens) : (int)a.tokens;
 }
 
-// An expert's token tiles: all `cap` high but the last.
-struct Tiles {
-    int begin, end, count, tail;   // tail: the last one's height in steps of 32
-    __device__ __forceinline__ Tiles(const ProductArgs& a, int g, int cap) {
-        expert_range(a, g, &begin, &end);
-        count = (int)((uint32_t)(end - begin + cap - 1) / (uint32_t)cap);
-        const int left = end - begin - (count - 1) * cap;
-        tail = (left + 31) & ~31;
-    }
-    __device__ __forceinline__ int cost(int cap) const {
-        return count ? (count - 1) * tile_cost(cap) + tile_cost(tail) : 0;
-    }
-};
-
-// The expert that tile `v` of all experts' token tiles (or cost, by `key`) lies in.
-__device__ __forceinline__ int find_bin(const int* key, int bins, int v) {
-    int lo = 0, hi = bins - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (key[mid] <= v)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return lo;
+// An expert's token tiles: as few as the greatest height allows, of equal height in steps of 32 (the last
+// may be lower).
+__device__ __forceinline__ void cut_range(int tokens, int cap, int* count, int* height) {
+    const int n = (int)((uint32_t)(tokens + cap - 1) >> (cap == 256 ? 8 : cap == 128 ? 7 : 6));
+    // 32 times the quotient rounded down, then up to what holds all tokens: at most twice, for the division's error
+    int h = (int)((float)tokens / (float)max(n, 1) * 0.03125f) << 5;
+    if ((long long)h * n < tokens) h += 32;
+    if ((long long)h * n < tokens) h += 32;
+    *count = n, *height = h;
 }
 
-struct Where {
-    int group, m, t;   // expert, tile along the outputs, token tile
-};
-
-// Tile u of the launch.
-__device__ __forceinline__ Where decode_unit(const ProductLaunch& L, const Plan& p, int u) {
-    const int bins = (L.a.groups + p.stride - 1) / p.stride;
-    const int v = u / L.tiles_m;
-    Where w;
-    const int b = find_bin(p.tiles, bins, v);
-    int before = p.tiles[b];
-    w.group = b * p.stride;
-    Tiles e(L.a, w.group, p.cap);
-    while (before + e.count <= v && w.group + 1 < L.a.groups) {
-        before += e.count;
-        e = Tiles(L.a, ++w.group, p.cap);
+// Tile u of the launch, the whole of its sum.
+__device__ __forceinline__ Item decode_unit(const ProductLaunch& L, const Plan& p, const Outline& o, int u) {
+    Item it;
+    const int v = L.by_tiles.div(u);
+    int before = 0, count, height;
+    if (o.stride > 1) {
+        int lo = 0, hi = o.bins - 1;
+        while (lo < hi) {   // the last bin whose tiles begin at or before v
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.tiles[mid] <= v)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        before = p.tiles[lo];
+        it.group = lo * o.stride;
+        for (;; ++it.group, before += count) {
+            expert_range(L.a, it.group, &it.t0, &it.end);
+            cut_range(it.end - it.t0, o.cap, &count, &height);
+            if (before + count > v) break;
+        }
+    } else {
+        int lo = 0;
+        if (o.bins > 1) {
+            int hi = o.bins - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.tiles[mid] <= v)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            before = p.tiles[lo];
+            lo = p.order[lo];
+        }
+        it.group = lo, it.t0 = p.begin[lo], it.end = p.end[lo], count = p.count[lo], height = p.height[lo];
     }
-    int r = u - before * L.tiles_m;
-    const int band = r / (kBand * L.tiles_m);
-    r -= band * kBand * L.tiles_m;
-    const int wide = min(kBand, e.count - band * kBand);
-    w.m = r / wide;
-    w.t = band * kBand + r - w.m * wide;
-    return w;
+    uint32_t r = u - before * L.tiles_m;
+    int band = 0;
+    if (count > kBand) {
+        band = (int)(r / (uint32_t)(kBand * L.tiles_m));
+        r -= band * kBand * L.tiles_m;
+    }
+    const uint32_t wide = min(kBand, count - band * kBand), m = r / wide;
+    it.m0 = (int)m * 256, it.t0 += (band * kBand + (int)(r - m * wide)) * height;
+    it.k0 = 0, it.k1 = L.steps, it.part = 0;
+    it.n = min(height, (it.end - it.t0 + 31) & ~31);
+    return it;
 }
 
-// Cost of all tiles before tile u, in steps times tile_cost.
-__device__ __forceinline__ long long cost_before(const ProductLaunch& L, const Plan& p, int u) {
-    if (u == 0) return 0;
-    const Where w = decode_unit(L, p, u);
-    const int b = w.group / p.stride;
-    int before = p.cost[b];
-    for (int g = b * p.stride; g < w.group; ++g) before += Tiles(L.a, g, p.cap).cost(p.cap);
-    const Tiles e(L.a, w.group, p.cap);
-    const int full = tile_cost(p.cap), band = w.t / kBand;
-    const int wide = min(kBand, e.count - band * kBand);
-    long long c = (long long)before * L.tiles_m + (long long)band * kBand * L.tiles_m * full;
-    const int column = wide * full - (band * kBand + wide == e.count ? full - tile_cost(e.tail) : 0);
-    c += (long long)w.m * column + (long long)(w.t - band * kBand) * full;
-    return c * L.steps;
+// Places of the experts by decreasing height, those without tiles last: one warp.
+__device__ __forceinline__ void order_experts(Plan& p, int groups, int lane) {
+    if (lane < 12) p.next[lane] = 0;
+    __syncwarp();
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {   // count the heights, then deal out the places
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int g = g0 + lane, key = g < groups ? 8 - (p.height[g] >> 5) : 9;
+            const unsigned peers = __match_any_sync(0xffffffffu, key);
+            const int rank = __popc(peers & ((1u << lane) - 1)), at = p.next[key] + rank;
+            __syncwarp();
+            if (rank == 0) p.next[key] += __popc(peers);
+            __syncwarp();
+            if (pass == 1 && g < groups) p.order[at] = (uint16_t)g;
+        }
+        if (pass == 0) {
+            const int n = lane < 12 ? p.next[lane] : 0;
+            int sum = n;
+#pragma unroll
+            for (int d = 1; d < 16; d *= 2) {
+                const int x = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += x;
+            }
+            if (lane < 12) p.next[lane] = sum - n;
+            __syncwarp();
+        }
+    }
 }
 
-// The tile and step where the cost before is c: T is wide enough for the whole cost.
-template <typename T>
-__device__ __forceinline__ void locate(const ProductLaunch& L, const Plan& p, T c, int* unit, int* step) {
-    const int bins = (L.a.groups + p.stride - 1) / p.stride;
-    const T scale = (T)L.tiles_m * (T)L.steps;
-    const int b = find_bin(p.cost, bins, (int)(c / scale));
-    T left = c - (T)p.cost[b] * scale;
-    int g = b * p.stride, before = p.tiles[b];
-    Tiles e(L.a, g, p.cap);
-    while (left >= (T)e.cost(p.cap) * scale && g + 1 < L.a.groups) {
-        left -= (T)e.cost(p.cap) * scale;
-        before += e.count;
-        e = Tiles(L.a, ++g, p.cap);
+// Begins of the stretches of the last turn's `rest` tiles, one warp: parts of a tile have at least `edge` steps.
+__device__ __forceinline__ void cut_last_turn(const ProductLaunch& L, Plan& p, int stretches, int span, int least,
+                                              int lane) {
+    const int edge = max(min(least, L.steps / 2), 1);
+    for (int i = lane; i <= stretches; i += 32) {
+        int at = i == stretches ? span : (int)((long long)span * i / stretches);
+        const int k = at % L.steps;
+        if (k < edge)
+            at -= k;
+        else if (k > L.steps - edge)
+            at += L.steps - k;
+        p.start[i] = at;
     }
-    const int full = tile_cost(p.cap);
-    const int band = min((int)(left / ((T)(kBand * full) * scale)), (e.count - 1) / kBand);
-    left -= (T)band * (T)(kBand * full) * scale;
-    const int wide = min(kBand, e.count - band * kBand);
-    const bool ends = band * kBand + wide == e.count;
-    const T column = (T)(wide * full - (ends ? full - tile_cost(e.tail) : 0)) * (T)L.steps;
-    const int m = min((int)(left / column), L.tiles_m - 1);
-    left -= (T)m * column;
-    const int t = min((int)(left / (T)(full * L.steps)), wide - 1);
-    left -= (T)t * (T)(full * L.steps);
-    *unit = (before + band * kBand) * L.tiles_m + m * wide + t;
-    *step = min((int)(left / (T)(ends && t == wide - 1 ? tile_cost(e.tail) : full)), L.steps);
 }
 
 // Fills the plan: all threads of the CTA.
-__device__ void make_plan(const ProductLaunch& L, Plan& p, int threads) {
-    const int tid = threadIdx.x, lane = tid & 31, pairs = gridDim.x >> 1;
-    if (tid < 4) p.count[tid] = 0;
-    __syncthreads();
-    // heights of tiles: 256 tokens if those fill the GPU once, else 128 or 64
-    int c0 = 0, c1 = 0, c2 = 0;
-    for (int g = tid; g < L.a.groups; g += threads) {
-        int b, e;
-        expert_range(L.a, g, &b, &e);
-        c0 += (e - b + 255) >> 8, c1 += (e - b + 127) >> 7, c2 += (e - b + 63) >> 6;
-    }
-    c0 = __reduce_add_sync(0xffffffffu, c0), c1 = __reduce_add_sync(0xffffffffu, c1);
-    c2 = __reduce_add_sync(0xffffffffu, c2);
-    if (lane == 0 && c2 > 0) atomicAdd(p.count, c0), atomicAdd(p.count + 1, c1), atomicAdd(p.count + 2, c2);
-    __syncthreads();
-    const int need = (pairs + L.tiles_m - 1) / L.tiles_m;
-    const int most = p.count[0] == p.count[2] ? 64 : p.count[0] == p.count[1] ? 128 : 256;   // no expert has more
-    const int cap = min(p.count[0] >= need ? 256 : p.count[1] >= need ? 128 : 64, most);
-    const int stride = (L.a.groups + kBins - 1) / kBins, bins = (L.a.groups + stride - 1) / stride;
-    for (int b = tid; b < bins; b += threads) {
-        int tiles = 0, cost = 0;
-        for (int g = b * stride; g < min((b + 1) * stride, L.a.groups); ++g) {
-            const Tiles e(L.a, g, cap);
-            tiles += e.count, cost += e.cost(cap);
+__device__ __forceinline__ Outline make_plan(const ProductLaunch& L, Plan& p, int threads) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pairs = gridDim.x >> 1, groups = L.a.groups;
+    Outline o;
+    o.stride = (groups + kBins - 1) / kBins;
+    o.bins = (groups + o.stride - 1) / o.stride;
+    int n0 = L.tiles[0], n1 = L.tiles[1], n2 = L.tiles[2];
+    if (groups > 1 || L.a.offsets) {
+        if (tid < 4) p.sums[tid] = 0;
+        __syncthreads();
+        n0 = n1 = n2 = 0;
+        for (int g = tid; g < groups; g += threads) {
+            int b, e;
+            expert_range(L.a, g, &b, &e);
+            if (o.stride == 1) p.begin[g] = b, p.end[g] = e;
+            n0 += (e - b + 255) >> 8, n1 += (e - b + 127) >> 7, n2 += (e - b + 63) >> 6;
         }
-        p.tiles[b] = tiles, p.cost[b] = cost;
+        n0 = __reduce_add_sync(0xffffffffu, n0), n1 = __reduce_add_sync(0xffffffffu, n1);
+        n2 = __reduce_add_sync(0xffffffffu, n2);
+        if (lane == 0 && n2 > 0) atomicAdd(p.sums, n0), atomicAdd(p.sums + 1, n1), atomicAdd(p.sums + 2, n2);
+        __syncthreads();
+        n0 = p.sums[0], n1 = p.sums[1], n2 = p.sums[2];
+    } else if (tid == 0) {
+        p.begin[0] = 0, p.end[0] = (int)L.a.tokens;
     }
-    __syncthreads();
-    if (tid < 32) {   // sums of the bins before
-        int tiles = 0, cost = 0;
-        for (int b0 = 0; b0 < bins; b0 += 32) {
-            const int b = b0 + lane, t = b < bins ? p.tiles[b] : 0, c = b < bins ? p.cost[b] : 0;
-            int st = t, sc = c;
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int x = __shfl_up_sync(0xffffffffu, st, d), y = __shfl_up_sync(0xffffffffu, sc, d);
-                if (lane >= d) st += x, sc += y;
+    // the greatest height is 256 tokens if such tiles fill the GPU once, else 128 or 64
+    int n = n0;
+    o.cap = 256;
+    if (n0 == n2 || (n0 * L.tiles_m < pairs && n1 * L.tiles_m < pairs))
+        o.cap = 64, n = n2;
+    else if (n0 == n1 || n0 * L.tiles_m < pairs)
+        o.cap = 128, n = n1;
+    o.units = n * L.tiles_m;
+    // The tiles of the last, incomplete turn are cut along the contraction into stretches of equal length, one
+    // per pair, where that saves more than joining the parts takes: about 6 steps' time and, to write and read
+    // them, 34 more for 256 tokens.
+    const int whole = o.units / pairs, rest = o.units - whole * pairs, high = o.cap >> 5, least = 2 + high;
+    const bool cut = rest > 0 && L.steps * (pairs - rest) > (6 + 34 * high / 8) * pairs;   // steps <= 2^14
+    o.turns = whole + (rest > 0 && !cut);
+    o.stretches = cut ? max(min(pairs, rest * L.steps / least), 1) : 0;
+    if (o.stride == 1) {
+        for (int g = tid; g < groups; g += threads) {
+            int count, height;
+            cut_range(p.end[g] - p.begin[g], o.cap, &count, &height);
+            p.count[g] = count, p.height[g] = (uint16_t)height, p.order[g] = (uint16_t)g;
+        }
+    } else {
+        for (int b = tid; b < o.bins; b += threads) {
+            int tiles = 0;
+            for (int g = b * o.stride; g < min((b + 1) * o.stride, groups); ++g) {
+                int begin, end, count, height;
+                expert_range(L.a, g, &begin, &end);
+                cut_range(end - begin, o.cap, &count, &height);
+                tiles += count;
             }
-            if (b < bins) p.tiles[b] = tiles + st - t, p.cost[b] = cost + sc - c;
-            tiles += __shfl_sync(0xffffffffu, st, 31), cost += __shfl_sync(0xffffffffu, sc, 31);
-        }
-        if (lane == 0) {
-            p.tiles[bins] = tiles, p.cost[bins] = cost;
-            p.cap = cap, p.stride = stride;
-            p.units = tiles * L.tiles_m;
-            p.turns = p.units / pairs >= 8 ? p.units / pairs - 3 : 0;
+            p.tiles[b] = tiles;
         }
     }
+    if (cut && warp == 1) cut_last_turn(L, p, o.stretches, rest * L.steps, least, lane);
     __syncthreads();
-    // stretches of equal cost; parts of a tile have at least `least` steps, and tiles are cut only if that
-    // shortens the longest stretch by more than joining the parts takes
-    const int first = p.turns * pairs, rest = p.units - first, full = tile_cost(cap), least = 2 + cap / 32;
-    const long long from = cost_before(L, p, first);
-    const long long total = (long long)p.cost[bins] * L.tiles_m * L.steps, span = total - from;
-    const int whole = (rest + pairs - 1) / pairs;
-    const bool cut = span / pairs + (long long)least * full < (long long)whole * full * L.steps;
-    int stretches = pairs;
-    if (cut) stretches = (int)min((long long)pairs, max(span / (least * full), 1ll));
-    for (int i = tid; i <= stretches; i += threads) {
-        int u = i == 0 ? first : p.units, k = 0;
-        if (i > 0 && i < stretches && span > 0) {
-            const long long c = from + span * i / stretches;
-            if (total < (1ll << 27))   // 8 tiles' cost, at most 15 times a tile's least, is below 2^31
-                locate<uint32_t>(L, p, (uint32_t)c, &u, &k);
-            else
-                locate<unsigned long long>(L, p, (unsigned long long)c, &u, &k);
-            const int edge = max(min(least, L.steps / 2), 1);
-            if (cut ? k > L.steps - edge : 2 * k >= L.steps)
-                ++u, k = 0;
-            else if (!cut || k < edge)
-                k = 0;
+    if (o.bins > 1) {
+        if (warp == 0) {
+            if (o.stride == 1 && o.units > pairs) {
+                order_experts(p, groups, lane);
+                __syncwarp();
+            }
+            int tiles = 0;
+            for (int b0 = 0; b0 < o.bins; b0 += 32) {   // tiles of the places before
+                const int b = b0 + lane, t = b >= o.bins ? 0 : o.stride == 1 ? p.count[p.order[b]] : p.tiles[b];
+                int sum = t;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int x = __shfl_up_sync(0xffffffffu, sum, d);
+                    if (lane >= d) sum += x;
+                }
+                if (b < o.bins) p.tiles[b] = tiles + sum - t;
+                tiles += __shfl_sync(0xffffffffu, sum, 31);
+            }
         }
-        p.unit[i] = u, p.step[i] = k;
+        __syncthreads();
     }
-    if (tid == 0) p.pairs = stretches;
-    __syncthreads();
+    return o;
 }
 
-// What a CTA pair does, one item per turn.
+// What a CTA pair does, one item per turn: whole tiles, every other turn backwards (pairs get high and low
+// tiles alike), then its stretch of the last turn.
 struct Items {
     int pair, pairs, turns, count;
-    __device__ __forceinline__ Items(const Plan& p) : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), turns(p.turns) {
+    __device__ __forceinline__ Items(const ProductLaunch& L, const Plan& p, const Outline& o)
+        : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), turns(o.turns) {
+        if (turns > 0 && unit_of(turns - 1) >= o.units) --turns;
         count = turns;
-        if (pair < p.pairs) count += p.unit[pair + 1] - p.unit[pair] + (p.step[pair + 1] > 0);
+        if (pair < o.stretches && p.start[pair + 1] > p.start[pair])
+            count += (p.start[pair + 1] - 1) / L.steps - p.start[pair] / L.steps + 1;
     }
-    __device__ __forceinline__ Item decode(const ProductLaunch& L, const Plan& p, int turn) const {
-        Item it;
-        int u;
-        it.k0 = 0, it.k1 = L.steps, it.part = 0;
-        if (turn < turns) {   // every other turn backwards: a pair gets tiles of every height
-            u = turn * pairs + (turn & 1 ? pairs - 1 - pair : pair);
-        } else {
-            u = p.unit[pair] + turn - turns;
-            if (turn == turns) it.k0 = p.step[pair];
-            if (u == p.unit[pair + 1]) it.k1 = p.step[pair + 1];
-            if (it.k0 > 0 || it.k1 < L.steps) {
-                int a = it.k0 > 0 ? pair - 1 : pair;   // the pair that has the tile's first steps
-                while (p.unit[a] == u && p.step[a] > 0) --a;
-                int z = pair;                          // the one that has its last
-                while (z + 1 < p.pairs && p.unit[z + 1] == u) ++z;
-                it.part = (z - a + 1) << 16 | (pair - a) << 8 | a;
-            }
+    __device__ __forceinline__ int unit_of(int turn) const {
+        return turn * pairs + (turn & 1 ? pairs - 1 - pair : pair);
+    }
+    __device__ __forceinline__ Item decode(const ProductLaunch& L, const Plan& p, const Outline& o, int turn) const {
+        if (turn < turns) return decode_unit(L, p, o, unit_of(turn));
+        const int from = p.start[pair], to = p.start[pair + 1];
+        const int u = from / L.steps + turn - turns, begin = u * L.steps, end = begin + L.steps;
+        Item it = decode_unit(L, p, o, o.turns * pairs + u);
+        it.k0 = max(from - begin, 0), it.k1 = min(to - begin, L.steps);
+        if (it.k0 > 0 || it.k1 < L.steps) {
+            int a = pair, z = pair;   // the pairs that have the tile's first and last steps
+            while (p.start[a] > begin) --a;
+            while (p.start[z + 1] < end) ++z;
+            it.part = (z - a + 1) << 16 | (pair - a) << 8 | a;
         }
-        const Where w = decode_unit(L, p, u);
-        const Tiles e(L.a, w.group, p.cap);
-        it.group = w.group, it.m0 = w.m * 256, it.t0 = e.begin + w.t * p.cap, it.end = e.end;
-        it.n = w.t == e.count - 1 ? e.tail : p.cap;
         return it;
     }
-    __device__ __forceinline__ Item get(const ProductLaunch& L, const Plan& p, uint32_t table, int turn) const {
-        if (turn >= kItems) return decode(L, p, turn);
+    __device__ __forceinline__ Item get(const ProductLaunch& L, const Plan& p, const Outline& o, uint32_t table,
+                                        int turn) const {
+        if (turn >= kItems) return decode(L, p, o, turn);
         Item u;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(u.m0), "=r"(u.t0), "=r"(u.end), "=r"(u.group)
@@ -366,6 +402,7 @@ struct Epilogue {
     uint64_t* tfull;
     volatile int* abort_flag;
     int q, wq, lane;
+    int first, step;   // this warp's first block of tokens, and from one to its next
 };
 
 // Hands accumulator `acc` back to the MMA warp once this warp's last load from it is complete.
@@ -379,9 +416,11 @@ __device__ __forceinline__ void release_tmem(const Epilogue& e, uint32_t acc) {
 // Aligned rows: pairs of tokens in bf16 through shared memory, from which a lane takes four outputs of two
 // tokens; else a lane stores its output of each token, a warp 64 bytes of a row at a time.
 __device__ __forceinline__ void store_block(const ProductLaunch& L, const Epilogue& e, const float (&f)[32], int c0, int t,
-                                            int end, uint32_t blk) {
+                                            int end) {
     char* y = static_cast<char*>(L.a.y);
+    const uint32_t blk = e.blk;
     if (L.wide) {
+        __syncwarp();   // the block before has been read
 #pragma unroll
         for (int p = 0; p < 16; ++p) sts32(blk + p * 128 + e.lane * 4, bf16_pair(f[2 * p], f[2 * p + 1]));
         __syncwarp();
@@ -414,66 +453,80 @@ __device__ __forceinline__ void store_block(const ProductLaunch& L, const Epilog
 }
 
 // A lane's 32 sums of a block in the workspace: 16 bytes per lane and access, neighbours side by side.
+struct Block {
+    float4 x[8];
+    __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __ldcg(reinterpret_cast<const float4*>(p + i * 128));
+    }
+    __device__ __forceinline__ void add_to(float (&f)[32]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[4 * i] += x[i].x, f[4 * i + 1] += x[i].y, f[4 * i + 2] += x[i].z, f[4 * i + 3] += x[i].w;
+    }
+};
 __device__ __forceinline__ void part_store(float* p, const uint32_t (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         *reinterpret_cast<uint4*>(p + i * 128) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
-template <bool FIRST>
-__device__ __forceinline__ void part_add(const float* p, float (&f)[32]) {
-    float4 x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __ldcg(reinterpret_cast<const float4*>(p + i * 128));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        f[4 * i] = FIRST ? x[i].x : f[4 * i] + x[i].x, f[4 * i + 1] = FIRST ? x[i].y : f[4 * i + 1] + x[i].y;
-        f[4 * i + 2] = FIRST ? x[i].z : f[4 * i + 2] + x[i].z, f[4 * i + 3] = FIRST ? x[i].w : f[4 * i + 3] + x[i].w;
-    }
-}
 
-// One epilogue warp: TMEM lane quarter wq, that is 32 outputs of a tile.
-__device__ __forceinline__ void epilogue(const ProductLaunch& L, const Plan& plan, const Items& items, const Epilogue& e) {
+// One epilogue warp: TMEM lane quarter wq, that is 32 outputs of a tile, and every block of tokens or every other.
+template <bool COPY>
+__device__ __forceinline__ void epilogue(const ProductLaunch& L, const Plan& plan, const Outline& outline,
+                                         const Items& items, const Epilogue& e) {
     int local = 0;
     for (int turn = 0; turn < items.count; ++turn, ++local) {
-        const Item w = items.get(L, plan, e.table, turn);
+        const Item w = items.get(L, plan, outline, e.table, turn);
         const uint32_t acc = local & 1;
         if (!mbar_wait_idle(e.tfull + acc, local >> 1 & 1u, e.abort_flag, L.a.status, kStatusTimeoutEpilogue, true)) return;
         tc_fence_after();
         const uint32_t tbase = e.tmem_base + acc * 256 + (static_cast<uint32_t>(e.wq * 32) << 16);
-        const int c0 = w.m0 + 128 * e.q + 32 * e.wq, mine = 4 * e.q + e.wq;
+        const int c0 = w.m0 + 128 * e.q + 32 * e.wq;
         const int parts = w.part >> 16, part = w.part >> 8 & 255, first = w.part & 255;
         // a pair has at most two parts of tiles: one that begins inside its tile, one that begins with it
         auto slot = [&](int k) {
-            return L.a.partial + ((2 * (first + k) + (k == 0)) * 8ll + mine) * 8192 + e.lane * 4;
+            return L.a.partial + ((2 * (first + k) + (k == 0)) * 8ll + 4 * e.q + e.wq) * 8192 + e.lane * 4;
         };
-        for (int c = 0; c < w.n; c += 32) {
+        for (int c = e.first; c < w.n; c += e.step) {
             uint32_t v[32];
             tmem_ld32(tbase + c, v);
             tmem_ld_wait();
-            if (c + 32 >= w.n) release_tmem(e, acc);
+            if (c + e.step >= w.n) release_tmem(e, acc);
             if (parts) {
                 part_store(slot(part) + c * 32, v);
             } else {
                 float f[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-                store_block(L, e, f, c0, w.t0 + c, w.end, e.blk + (c & 32) * 64);
+                store_block(L, e, f, c0, w.t0 + c, w.end);
             }
         }
-        if (parts) {
-            __threadfence();
-            __syncwarp();
-            int* count = L.a.counters + first * 8 + mine;
+        if (e.first >= w.n) {   // no block of this tile
+            release_tmem(e, acc);
+        } else if (parts) {
+            int* count = L.a.counters + (first * 2 + e.q) * 8 + e.wq + (e.first >> 3);
             int seen = 0;
-            if (e.lane == 0) seen = atomicAdd(count, 1);
-            if (__shfl_sync(0xffffffffu, seen, 0) == parts - 1) {
+            __syncwarp();   // the warp's sums before lane 0's release, the others' after its acquire
+            if (e.lane == 0)
+                asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(seen) : "l"(count) : "memory");
+            if (__shfl_sync(0xffffffffu, seen, 0) == parts - 1) {   // the last part: all of them, in their order
                 if (e.lane == 0) *count = 0;   // for the next call
-                __threadfence();
-                for (int c = 0; c < w.n; c += 32) {
-                    float f[32];
-                    part_add<true>(slot(0) + c * 32, f);
-                    for (int k = 1; k < parts; ++k) part_add<false>(slot(k) + c * 32, f);
-                    store_block(L, e, f, c0, w.t0 + c, w.end, e.blk + (c & 32) * 64);
+                for (int c = e.first; c < w.n; c += e.step) {
+                    Block a;
+                    a.load(slot(0) + c * 32);
+                    float f[32] = {};
+                    for (int k = 0; k < parts; ++k) {
+                        if (COPY) {
+                            a.add_to(f);
+                            if (k + 1 < parts) a.load(slot(k + 1) + c * 32);
+                        } else {   // the next part is on its way while this one is added
+                            const Block b = a;
+                            if (k + 1 < parts) a.load(slot(k + 1) + c * 32);
+                            b.add_to(f);
+                        }
+                    }
+                    store_block(L, e, f, c0, w.t0 + c, w.end);
                 }
             }
         }
@@ -482,7 +535,8 @@ __device__ __forceinline__ void epilogue(const ProductLaunch& L, const Plan& pla
 
 // MN: the weight is MN-major (dx = dy W).  COPY: an operand's rows are not aligned.
 template <bool MN, bool COPY>
-__global__ void __launch_bounds__(kThreadsOf<COPY>) k_product(const __grid_constant__ ProductLaunch L) {
+__global__ void __launch_bounds__(Roles<COPY>::kThreads) k_product(const __grid_constant__ ProductLaunch L) {
+    using R = Roles<COPY>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFFSET);
@@ -505,7 +559,7 @@ __global__ void __launch_bounds__(kThreadsOf<COPY>) k_product(const __grid_const
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull + a, 1);
-            mbar_init(tempty + a, 2 * kEpi);
+            mbar_init(tempty + a, 2 * R::kEpi);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -522,19 +576,23 @@ __global__ void __launch_bounds__(kThreadsOf<COPY>) k_product(const __grid_const
     const uint32_t tmem_base = *tmem_slot;
     pdl_trigger();
     pdl_wait();
-    make_plan(L, plan, kThreadsOf<COPY>);
-    const Items items(plan);
-    for (int t = threadIdx.x; t < min(items.count, kItems); t += kThreadsOf<COPY>)
-        reinterpret_cast<Item*>(smem + Cfg::ITEM_OFFSET)[t] = items.decode(L, plan, t);
+    const Outline outline = make_plan(L, plan, R::kThreads);
+    const Items items(L, plan, outline);
+    for (int t = threadIdx.x; t < min(items.count, kItems); t += R::kThreads)
+        reinterpret_cast<Item*>(smem + Cfg::ITEM_OFFSET)[t] = items.decode(L, plan, outline, t);
     __syncthreads();
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- TMA, completion on the even CTA's barrier
+        // ---------------- TMA, completion on the even CTA's barrier.  The whole warp runs the loop and one elected
+        // lane issues (a loop of one lane alone: 64 us against 58 for the 32 experts' product; a second warp
+        // for the tokens gains nothing more).  Where all rows are copied, the odd CTA's warp must not even wait:
+        // nothing waits for it, so the ring could pass it by two rounds, whose parity it takes for none.
+        if (!COPY || leader || L.tma_w || L.tma_x) {
+            const bool one = elect_one();
             uint32_t slot = 0, ph = 1;
             bool ok = true;
             for (int turn = 0; ok && turn < items.count; ++turn) {
-                const Item w = items.get(L, plan, table, turn);
+                const Item w = items.get(L, plan, outline, table, turn);
                 const int rows = w.n >> 1, t0 = w.t0 + (int)q * rows, m0 = w.m0 + 128 * (int)q;
                 const uint32_t bytes = (!COPY || L.tma_w ? 2 * Cfg::A_BYTES : 0) + (!COPY || L.tma_x ? 2 * rows * 128 : 0) +
                                        (COPY ? 16 * kGroupWarps : 0);
@@ -543,25 +601,30 @@ __global__ void __launch_bounds__(kThreadsOf<COPY>) k_product(const __grid_const
                         ok = false;
                         break;
                     }
-                    uint8_t *sa = smem + slot * Cfg::SLOT_BYTES, *sb = sa + Cfg::A_BYTES;
-                    const uint32_t fb = mapa_shared(smem_u32(full + slot), 0);
-                    if (leader) mbar_arrive_expect_tx(full + slot, bytes);
-                    const int kk = k * kStepK;
-                    if (!COPY || L.tma_w) {
-                        if (MN) {
-                            tma_load_3d_pair(sa, &L.map_w, fb, m0, kk, w.group);
-                            tma_load_3d_pair(sa + Cfg::CHUNK_BYTES, &L.map_w, fb, m0 + 64, kk, w.group);
-                        } else {
-                            tma_load_3d_pair(sa, &L.map_w, fb, kk, m0, w.group);
+                    if (one) {
+                        uint8_t* to = smem + slot * Cfg::SLOT_BYTES;
+                        const uint32_t fb = mapa_shared(smem_u32(full + slot), 0);
+                        const int kk = k * kStepK;
+                        if (leader) mbar_arrive_expect_tx(full + slot, bytes);
+                        if (!COPY || L.tma_w) {
+                            if (MN) {
+                                tma_load_3d_pair(to, &L.map_w, fb, m0, kk, w.group);
+                                tma_load_3d_pair(to + Cfg::CHUNK_BYTES, &L.map_w, fb, m0 + 64, kk, w.group);
+                            } else {
+                                tma_load_3d_pair(to, &L.map_w, fb, kk, m0, w.group);
+                            }
                         }
-                    }
-                    if (!COPY || L.tma_x) {
-                        int at = 0;
+                        if (COPY && !L.tma_x) {
+                        } else if (rows == 128) {
+                            tma_load_2d_pair(to + Cfg::A_BYTES, &L.map_x[0], fb, kk, t0);
+                        } else {
+                            int at = 0;
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            if (rows & (128 >> b)) {
-                                tma_load_2d_pair(sb + at * 128, &L.map_x[b], fb, kk, t0 + at);
-                                at += 128 >> b;
+                            for (int b = 1; b < 4; ++b) {
+                                if (rows & (128 >> b)) {
+                                    tma_load_2d_pair(to + Cfg::A_BYTES + at * 128, &L.map_x[b], fb, kk, t0 + at);
+                                    at += 128 >> b;
+                                }
                             }
                         }
                     }
@@ -584,7 +647,7 @@ __global__ void __launch_bounds__(kThreadsOf<COPY>) k_product(const __grid_const
             const uint64_t bd0 = sdesc_sw128(smem_u32(smem) + Cfg::A_BYTES, 16, 1024);
             const int last = ((L.k - 1) & (kStepK - 1)) / 16 + 1;        // MMAs of the contraction's last step
             for (int turn = 0; ok && turn < items.count; ++turn, ++local) {
-                const Item w = items.get(L, plan, table, turn);
+                const Item w = items.get(L, plan, outline, table, turn);
                 const uint32_t idesc = idesc_make(true, 256, w.n, MN, false);
                 const uint32_t acc = local & 1;
                 if (!mbar_wait_idle(tempty + acc, (local >> 1 & 1u) ^ 1u, abort_flag, L.a.status, kStatusTimeoutMma,
@@ -632,7 +695,7 @@ __global__ void __launch_bounds__(kThreadsOf<COPY>) k_product(const __grid_const
             }
             __syncwarp();
         }
-    } else if (warp < kCopyFirst) {
+    } else if (warp < R::kCopyFirst) {
         // ---------------- epilogue
         Epilogue e;
         e.tmem_base = tmem_base;
@@ -642,17 +705,18 @@ __global__ void __launch_bounds__(kThreadsOf<COPY>) k_product(const __grid_const
         e.tfull = tfull;
         e.abort_flag = abort_flag;
         e.q = (int)q, e.wq = warp & 3, e.lane = lane;
-        epilogue(L, plan, items, e);
+        e.first = (warp - kEpiFirst) / 4 * 32, e.step = R::kEpi / 4 * 32;
+        epilogue<COPY>(L, plan, outline, items, e);
     } else if (COPY) {
         // ---------------- copies of rows that are not aligned: group g takes every kCopyGroups-th step
-        const int cw = (warp - kCopyFirst) % kGroupWarps;
-        const uint32_t g = (warp - kCopyFirst) / kGroupWarps;
+        const int cw = (warp - R::kCopyFirst) % kGroupWarps;
+        const uint32_t g = (warp - R::kCopyFirst) / kGroupWarps;
         const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
-        const uint32_t signal_lead = mapa_shared(smem_u32(smem + Cfg::SIGNAL_OFFSET), 0) + 16 * (warp - kCopyFirst);
+        const uint32_t signal_lead = mapa_shared(smem_u32(smem + Cfg::SIGNAL_OFFSET), 0) + 16 * (warp - R::kCopyFirst);
         uint32_t it = 0, slot = 0, ph = 1;
         bool ok = true;
         for (int turn = 0; ok && turn < items.count; ++turn) {
-            const Item w = items.get(L, plan, table, turn);
+            const Item w = items.get(L, plan, outline, table, turn);
             const int rows = w.n >> 1, t0 = w.t0 + (int)q * rows, m0 = w.m0 + 128 * (int)q;
             const char* wp = static_cast<const char*>(L.a.weight) + (long long)w.group * L.a.m * L.a.n * 2;
             const char* xp = static_cast<const char*>(L.a.x) + t0 * L.a.ldx * 2;
@@ -684,12 +748,13 @@ __global__ void __launch_bounds__(kThreadsOf<COPY>) k_product(const __grid_const
                     if (leader)
                         mbar_arrive(full + s);
                     else
-                        bulk_signal(signal_lead, smem + Cfg::SIGNAL_OFFSET + 16 * (warp - kCopyFirst), full_lead + s * 8);
+                        bulk_signal(signal_lead, smem + Cfg::SIGNAL_OFFSET + 16 * (warp - R::kCopyFirst), full_lead + s * 8);
                 }
             }
         }
     }
 
+    __syncwarp();
     if (*abort_flag) {   // copies already issued signal the even CTA; give them time to land
         const unsigned long long t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 2000000ull) {
@@ -740,6 +805,8 @@ cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s) {
     L.k = a.transposed ? a.m : a.n;
     L.steps = (L.k + kStepK - 1) / kStepK;
     L.tiles_m = (L.out + 255) / 256;
+    L.by_tiles.set(L.tiles_m);
+    for (int i = 0; i < 3; ++i) L.tiles[i] = (int)((a.tokens + (256 >> i) - 1) / (256 >> i));
     if ((a.tokens / 64 + a.groups) * L.tiles_m >= (1ll << 31)) return cudaErrorInvalidValue;
     L.tma_w = a.n % 8 == 0 && (reinterpret_cast<uintptr_t>(a.weight) & 15) == 0;
     L.tma_x = ((reinterpret_cast<uintptr_t>(a.x) | (uintptr_t)(a.ldx * 2)) & 15) == 0;
@@ -750,8 +817,8 @@ cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s) {
     for (int b = 0; L.tma_x && b < 4; ++b)
         if (!map_tokens(&L.map_x[b], a.x, L.k, a.tokens, a.ldx * 2, 128 >> b)) return cudaErrorInvalidValue;
     const bool copy = !L.tma_w || !L.tma_x;
-    return launch_pdl_cluster(pick(a.transposed, copy), dim3(2 * std::min(sm_count / 2, kMostPairs)),
-                              dim3(copy ? kThreadsOf<true> : kThreadsOf<false>), Cfg::SMEM_BYTES, s, 2u, L);
+    return launch_pdl_cluster(pick(a.transposed, copy), dim3(2 * std::min(sm_count / 2, kMaxPairs)),
+                              dim3(copy ? Roles<true>::kThreads : Roles<false>::kThreads), Cfg::SMEM_BYTES, s, 2u, L);
 }
 
 }  // namespace muon

@@ -731,7 +731,9 @@ __global__ void __launch_bounds__(Roles<TMA_Y>::kThreads) k_wgrad(const __grid_c
             }
         }
     } else if (warp == 2) {
-        if (lane == 0) {
+        // The odd CTA has nothing to do here where dy is copied.  It must not wait either: nothing waits for it,
+        // so the ring could pass it by two rounds, whose parity it takes for none.
+        if (lane == 0 && (TMA_Y || leader)) {
             // ---------------- TMA of dy, completion on the even CTA's barrier
             uint32_t slot = 0, ph = 1;
             bool ok = true;
