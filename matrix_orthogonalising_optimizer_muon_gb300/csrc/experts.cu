@@ -14,9 +14,12 @@ namespace {
 // contiguous share of the ids, its warps contiguous shares of that.  Pass 1 counts each warp's ids by
 // expert in shared memory; the counts of earlier warps, earlier CTAs (read from their shared memory)
 // and smaller experts give each warp its first slot per expert; pass 2 deals the slots out, 32 ids at
-// a time, neighbours with the same expert by their rank among the warp's lanes.
+// a time, neighbours with the same expert by their rank among the warp's lanes.  What bounds it is latency:
+// a warp's ids are loaded kBatch groups of 32 at a time (131072 ids: 8 us; 22 one group at a time) and, when
+// that is all it has, kept for pass 2.
 constexpr int kOrderThreads = 1024;
 constexpr int kOrderCounts = 32768;   // counts in shared memory: warps x experts
+constexpr int kBatch = 16;
 
 __device__ __forceinline__ int remote_int(uint32_t local_saddr, uint32_t rank) {
     int v;
@@ -24,60 +27,77 @@ __device__ __forceinline__ int remote_int(uint32_t local_saddr, uint32_t rank) {
     return v;
 }
 
+// Ids from .. of one batch, -1 for those that are no expert or at and beyond `to`.
+__device__ __forceinline__ void load_ids(const OrderArgs& a, long long from, long long to, int lane, int (&id)[kBatch]) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) id[j] = from + 32 * j + lane < to ? a.ids[from + 32 * j + lane] : -1;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) id[j] = (unsigned)id[j] < (unsigned)a.experts ? id[j] : -1;
+}
+
+// warps: that count and deal, a power of two; ctas: of the cluster, 1 or 8.
 __global__ void __launch_bounds__(kOrderThreads) k_expert_order(const OrderArgs a, int warps, int ctas) {
     extern __shared__ int smem[];
-    const int E = a.experts;
-    int* count = smem;                    // [warps][E]
-    int* total = smem + warps * E;        // [E]: this CTA's counts
+    const int E = a.experts, row = warps + 1;   // an expert's counts lie side by side, odd rows against bank conflicts
+    int* count = smem;                    // [E][row]
+    int* total = smem + E * row;          // [E]: this CTA's counts
     int* base = total + E;                // [E]: the CTA's first slot
     __shared__ int chunk[kOrderThreads / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = ctas > 1 ? (int)cluster_ctarank() : 0;
+    for (int i = threadIdx.x; i < E * row; i += kOrderThreads) count[i] = 0;
     pdl_trigger();
     pdl_wait();
 
-    for (int i = threadIdx.x; i < warps * E; i += kOrderThreads) count[i] = 0;
-    __syncthreads();
     // shares of 32 ids, as even as that allows
     const long long groups = (a.n + 31) / 32, parts = (long long)ctas * warps, w = (long long)rank * warps + warp;
-    const long long from = groups * w / parts * 32, to = min(groups * (w + 1) / parts * 32, a.n);
-    int* mine = count + warp * E;
-    if (warp < warps) {
-        for (long long i = from + lane; i < to; i += 32) {
-            const int id = a.ids[i];
-            if ((unsigned)id < (unsigned)E) atomicAdd(mine + id, 1);
-        }
+    const long long from = warp < warps ? groups * w / parts * 32 : 0;
+    const long long to = warp < warps ? min(groups * (w + 1) / parts * 32, a.n) : 0;
+    int id[kBatch];
+    if (from < to) load_ids(a, from, to, lane, id);
+    __syncthreads();
+    for (long long i = from; i < to; i += 32 * kBatch) {
+        if (i > from) load_ids(a, i, to, lane, id);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (id[j] >= 0) atomicAdd(count + id[j] * row + warp, 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kOrderThreads) {   // counts of earlier warps
-        int sum = 0;
-        for (int k = 0; k < warps; ++k) {
-            const int c = count[k * E + e];
-            count[k * E + e] = sum;
-            sum += c;
+    // counts of earlier warps: `warps` lanes per expert
+    const int sub = lane & (warps - 1);
+    for (int e0 = warp * (32 / warps); e0 < E; e0 += kOrderThreads / warps) {
+        const int e = e0 + lane / warps, c = e < E ? count[e * row + sub] : 0;
+        int sum = c;
+        for (int d = 1; d < warps; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d, warps);
+            if (sub >= d) sum += o;
         }
-        total[e] = sum;
+        if (e < E) {
+            count[e * row + sub] = sum - c;
+            if (sub == warps - 1) total[e] = sum;
+        }
     }
     if (ctas > 1)
         cluster_sync();
     else
         __syncthreads();
-    // counts of earlier CTAs and of smaller experts: a scan over the experts, kOrderThreads at a time
+    // counts of earlier CTAs, and of all: a lane per CTA, the sums to base and, for now, the first counts' row end
+    for (int i0 = 0; i0 < E * ctas; i0 += kOrderThreads) {
+        const int i = i0 + threadIdx.x, e = i / ctas, r = i - e * ctas;
+        int all = 0;
+        if (e < E) all = ctas > 1 ? remote_int(smem_u32(total + e), r) : total[e];
+        int before = r < rank ? all : 0;
+        for (int d = 1; d < ctas; d *= 2) {
+            all += __shfl_xor_sync(0xffffffffu, all, d);
+            before += __shfl_xor_sync(0xffffffffu, before, d);
+        }
+        if (e < E && r == 0) base[e] = before, count[e * row + warps] = all;
+    }
+    __syncthreads();
+    // smaller experts: a scan, kOrderThreads at a time
     int carry = 0;
     for (int e0 = 0; e0 < E; e0 += kOrderThreads) {
-        const int e = e0 + threadIdx.x;
-        int before = 0, all = 0;
-        if (e < E) {
-            if (ctas > 1) {
-                for (int r = 0; r < ctas; ++r) {
-                    const int c = remote_int(smem_u32(total + e), r);
-                    before += r < rank ? c : 0;
-                    all += c;
-                }
-            } else {
-                all = total[e];
-            }
-        }
+        const int e = e0 + threadIdx.x, all = e < E ? count[e * row + warps] : 0;
         int scan = all;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -86,35 +106,36 @@ __global__ void __launch_bounds__(kOrderThreads) k_expert_order(const OrderArgs 
         }
         if (lane == 31) chunk[warp] = scan;
         __syncthreads();
-        int lower = carry, whole = 0;
-        for (int k = 0; k < kOrderThreads / 32; ++k) {
-            lower += k < warp ? chunk[k] : 0;
-            whole += chunk[k];
+        int lower = chunk[lane];   // every warp scans the warps' sums
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, lower, d);
+            if (lane >= d) lower += o;
         }
-        carry += whole;
+        const int mine = warp ? __shfl_sync(0xffffffffu, lower, warp - 1) : 0;
         if (e < E) {
-            const int first = lower + scan - all;
-            base[e] = first + before;
+            const int first = carry + mine + scan - all;
+            base[e] += first;
             if (rank == 0) a.offsets[e] = first;
         }
+        carry += __shfl_sync(0xffffffffu, lower, 31);
         __syncthreads();
     }
     if (rank == 0 && threadIdx.x == 0) a.offsets[E] = carry;
-    if (warp < warps) {
-        for (int e = lane; e < E; e += 32) mine[e] += base[e];
-        __syncwarp();
-        for (long long i0 = from; i0 < to; i0 += 32) {
-            const long long i = i0 + lane;
-            int id = i < to ? a.ids[i] : -1;
-            if ((unsigned)id >= (unsigned)E) id = -1;
-            const unsigned peers = __match_any_sync(0xffffffffu, id);
+    for (long long i = from; i < to; i += 32 * kBatch) {
+        if (to - from > 32 * kBatch) load_ids(a, i, to, lane, id);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (i + 32 * j >= to) break;
+            const unsigned peers = __match_any_sync(0xffffffffu, id[j]);
             const int rk = __popc(peers & ((1u << lane) - 1));
             int slot = -1;
-            if (id >= 0) slot = mine[id] + rk;
+            int* mine = count + id[j] * row + warp;
+            if (id[j] >= 0) slot = base[id[j]] + *mine + rk;
             __syncwarp();
-            if (id >= 0 && rk == 0) mine[id] += __popc(peers);
+            if (id[j] >= 0 && rk == 0) *mine += __popc(peers);
             __syncwarp();
-            if (i < to) a.slots[i] = slot;
+            if (i + 32 * j + lane < to) a.slots[i + 32 * j + lane] = slot;
         }
     }
     if (ctas > 1) cluster_sync();   // no CTA leaves while another reads its counts
@@ -154,27 +175,41 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const MoveArgs a) {
     }
 }
 
+// Choices whose rows are on their way together: with one, the loads do not cover HBM's latency (backward, 8192 x 4
+// rows of 3584 in bf16: 98 us, 84 with four).
+template <bool BF16>
+constexpr int kTogether = BF16 ? 4 : 2;
+
 // x[t, :] = sum over j of weights[t, j] y[slots[t, j], :], in fp32, j ascending.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_combine(const MoveArgs a) {
+    constexpr int kJ = kTogether<BF16>;
     const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
     for (Walk w(a.cols); w.row < a.tokens; w.next()) {
         float acc[kUnroll][8] = {};
-        for (int j = 0; j < a.choices; ++j) {
-            const int s = slot_row(a, w.row, j);
-            if (s < 0) continue;
-            const float f = a.weights ? a.weights[(uint64_t)w.row * a.choices + j] : 1.f;
-            Raw<BF16, kMode<VEC>> raw[kUnroll];
+        for (int j0 = 0; j0 < a.choices; j0 += kJ) {
+            int s[kJ];
+            Raw<BF16, kMode<VEC>> raw[kJ][kUnroll];
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k) raw[k].load(row_ptr(a.y, s), w.col + k * kSeg, a.cols, lane);
+            for (int j = 0; j < kJ; ++j) s[j] = j0 + j < a.choices ? slot_row(a, w.row, j0 + j) : -1;
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                float v[8];
-                raw[k].get(v);
+            for (int j = 0; j < kJ; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[k][i] = fmaf(f, v[i], acc[k][i]);
+                for (int k = 0; k < kUnroll; ++k)
+                    if (s[j] >= 0) raw[j][k].load(row_ptr(a.y, s[j]), w.col + k * kSeg, a.cols, lane);
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                if (s[j] < 0) continue;
+                const float f = a.weights ? a.weights[(uint64_t)w.row * a.choices + j0 + j] : 1.f;
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k) {
+                    float v[8];
+                    raw[j][k].get(v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[k][i] = fmaf(f, v[i], acc[k][i]);
+                }
             }
         }
 #pragma unroll
@@ -187,47 +222,62 @@ __global__ void __launch_bounds__(kThreads) k_combine(const MoveArgs a) {
 // dy[slots[t, j], :] = weights[t, j] x[t, :] and dweights[t, j] = x[t, :] . y[slots[t, j], :]: `span` warps
 // share a token's columns, their sums meet in shared memory and are added in order.
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_combine_backward(const MoveArgs a, int span) {
-    __shared__ float part[kThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = kThreads / 32 / span, q = warp % span;
+__global__ void __launch_bounds__(kThreads, 4) k_combine_backward(const MoveArgs a, int span) {
+    constexpr int kJ = kTogether<BF16>, kWarps = kThreads / 32;
+    __shared__ float part[2][kWarps][kJ];   // in turn, so that one barrier a round is enough
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = kWarps / span, q = warp % span;
+    int round = 0;
     pdl_trigger();
     pdl_wait();
     for (uint32_t t0 = blockIdx.x * per; t0 < a.tokens; t0 += gridDim.x * per) {
         const uint32_t t = t0 + warp / span;
-        for (int j = 0; j < a.choices; ++j) {
-            const int s = t < a.tokens ? slot_row(a, t, j) : -1;
-            float sum = 0.f;
-            if (s >= 0) {
-                const float f = a.weights[(uint64_t)t * a.choices + j];
-                for (int c0 = q * kSeg; c0 < a.cols; c0 += span * kSeg) {
-                    Raw<BF16, kMode<VEC>> xr, yr;
-                    float x[8], y[8];
-                    xr.load(row_ptr(a.x, t), c0, a.cols, lane);
-                    if (a.dweights) yr.load(row_ptr(a.y, s), c0, a.cols, lane);
-                    xr.get(x);
-                    if (a.dweights) {
-                        yr.get(y);
+        for (int j0 = 0; j0 < a.choices; j0 += kJ, round ^= 1) {
+            int s[kJ];
+            float f[kJ], sum[kJ] = {};
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) sum = fmaf(x[i], y[i], sum);
+            for (int j = 0; j < kJ; ++j) {
+                s[j] = t < a.tokens && j0 + j < a.choices ? slot_row(a, t, j0 + j) : -1;
+                f[j] = s[j] >= 0 ? a.weights[(uint64_t)t * a.choices + j0 + j] : 0.f;
+            }
+            for (int c0 = q * kSeg; t < a.tokens && c0 < a.cols; c0 += span * kSeg) {
+                Raw<BF16, kMode<VEC>> xr, yr[kJ];
+                float x[8];
+                xr.load(row_ptr(a.x, t), c0, a.cols, lane);
+                if (a.dweights) {
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j)
+                        if (s[j] >= 0) yr[j].load(row_ptr(a.y, s[j]), c0, a.cols, lane);
+                }
+                xr.get(x);
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    if (s[j] < 0) continue;
+                    float v[8];
+                    if (a.dweights) {
+                        yr[j].get(v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sum[j] = fmaf(x[i], v[i], sum[j]);
                     }
                     if (a.dy.p) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] *= f;
-                        seg_store<BF16, kMode<VEC>>(row_ptr(a.dy, s), c0, a.cols, lane, x);
+                        for (int i = 0; i < 8; ++i) v[i] = x[i] * f[j];
+                        seg_store<BF16, kMode<VEC>>(row_ptr(a.dy, s[j]), c0, a.cols, lane, v);
                     }
                 }
             }
             if (a.dweights) {
 #pragma unroll
-                for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (lane == 0) part[warp] = sum;
-                __syncthreads();
-                if (q == 0 && lane == 0 && t < a.tokens) {
-                    float all = part[warp];
-                    for (int k = 1; k < span; ++k) all += part[warp + k];
-                    a.dweights[(uint64_t)t * a.choices + j] = all;
+                for (int j = 0; j < kJ; ++j) {
+#pragma unroll
+                    for (int d = 16; d > 0; d /= 2) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+                    if (lane == j) part[round][warp][j] = sum[j];
                 }
                 __syncthreads();
+                if (q == 0 && lane < kJ && t < a.tokens && j0 + lane < a.choices) {
+                    float all = part[round][warp][lane];
+                    for (int k = 1; k < span; ++k) all += part[round][warp + k][lane];
+                    a.dweights[(uint64_t)t * a.choices + j0 + lane] = all;
+                }
             }
         }
     }
@@ -247,7 +297,7 @@ cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s) {
     int warps = kOrderThreads / 32;
     while (warps * a.experts > kOrderCounts) warps /= 2;
     const int ctas = a.n <= 8192 ? 1 : 8;
-    const size_t bytes = (size_t)(warps + 2) * a.experts * sizeof(int);
+    const size_t bytes = (size_t)(warps + 3) * a.experts * sizeof(int);
     // per call: an attribute of the current device
     const cudaError_t set =
         cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);

@@ -10,33 +10,64 @@ namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnrollGroups = kChunkGroups / kThreads;   // of eight values per thread and chunk
+// Blocks per SM: 32 KB of loads in flight each (256 threads, 8 loads of 16 bytes) cover HBM's latency.
+constexpr int kFit = 4;
+constexpr int kWords = 32;   // of a chunk per thread
 
-// Eight values of a gradient from element `start` on, zero outside [0, count).
+// A thread's groups of a chunk as loaded: group i is its i-th of every kThreads-th.
 template <bool BF16>
-__device__ __forceinline__ void load_eight(const void* p, long long start, long long count, bool vec, float (&v)[8]) {
-    if (vec && start >= 0 && start + 8 <= count) {
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + start * (BF16 ? 2 : 4));
-        if (BF16) {
-            const uint4 a = q[0];
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Groups {
+    static constexpr int kPer = BF16 ? 4 : 8, kCount = kWords / kPer;
+    static_assert(kCount * kThreads == (BF16 ? kChunkGroups16 : kChunkGroups32), "the chunk's groups");
+    uint32_t r[kWords];
+    // Groups from g0 on of a gradient whose first group begins `pad` values before it; zero outside it.  vec: whole
+    // groups are aligned to 16 bytes.
+    __device__ __forceinline__ void load(const GradEntry& e, long long g0, bool vec) {
+        const long long first = (g0 + threadIdx.x) * 8 - e.pad;
+        if (vec && g0 * 8 >= e.pad && (g0 + kCount * kThreads) * 8 - e.pad <= e.count) {   // the whole chunk
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-        } else {
-            const uint4 a = q[0], b = q[1];
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+            for (int i = 0; i < kCount; ++i) whole(e.p, first + i * 8ll * kThreads, r + i * kPer);
+            return;
         }
-        return;
-    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = start + j >= 0 && start + j < count ? load_one<BF16>(p, start + j) : 0.f;
-}
+        for (int i = 0; i < kCount; ++i) {
+            const long long at = first + i * 8ll * kThreads;
+            if (vec && at >= 0 && at + 8 <= e.count) {
+                whole(e.p, at, r + i * kPer);
+            } else {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = at + j >= 0 && at + j < e.count ? load_one<BF16>(e.p, at + j) : 0.f;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    r[i * kPer + j] = BF16 ? bf16_bits(v[2 * j]) | bf16_bits(v[2 * j + 1]) << 16 : __float_as_uint(v[j]);
+            }
+        }
+    }
+    static __device__ __forceinline__ uint32_t bf16_bits(float v) { return __float_as_uint(v) >> 16; }
+    static __device__ __forceinline__ void whole(const void* p, long long at, uint32_t* w) {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int i = 0; i < kPer / 4; ++i) {
+            const uint4 a = __ldcs(q + i);
+            w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+        }
+    }
+    __device__ __forceinline__ void get(int i, float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (BF16)
+                v[j] = j & 1 ? bf16_hi(r[i * kPer + j / 2]) : bf16_lo(r[i * kPer + j / 2]);
+            else
+                v[j] = __uint_as_float(r[i * kPer + j % kPer]);
+        }
+    }
+};
 
 template <bool BF16>
 __device__ __forceinline__ void store_eight(void* p, long long start, long long count, const float (&v)[8]) {
-    if (start >= 0 && start + 8 <= count) {   // aligned by the chunks' layout
+    if (start >= 0 && start + 8 <= count) {   // aligned by the groups' layout
         uint4* q = reinterpret_cast<uint4*>(static_cast<char*>(p) + start * (BF16 ? 2 : 4));
         if (BF16) {
             q[0] = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
@@ -51,47 +82,55 @@ __device__ __forceinline__ void store_eight(void* p, long long start, long long 
         if (start + j >= 0 && start + j < count) store_one<BF16>(p, start + j, v[j]);
 }
 
-// Squares of a chunk's values.  fp32 sums of one thread's run; a run whose sum is beyond the range where every
-// square that counts is exact to 2^-24 (an overflow, or values below 2^-45) is summed again in 64 bits, so that
-// the norm is right for gradients of any scale.
+// Squares of a thread's values of a chunk in 64 bits, read again.
 template <bool BF16>
-__device__ __forceinline__ double chunk_squares(const GradEntry& e, long long g0) {
-    float v[kUnrollGroups][8];
-#pragma unroll
-    for (int k = 0; k < kUnrollGroups; ++k)
-        load_eight<BF16>(e.p, (g0 + k * kThreads + threadIdx.x) * 8 - e.pad, e.count, true, v[k]);
-    float s = 0.f;
-    uint32_t any = 0;
-#pragma unroll
-    for (int k = 0; k < kUnrollGroups; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            s = fmaf(v[k][j], v[k][j], s);
-            any |= __float_as_uint(v[k][j]) << 1;
-        }
-    if (any == 0) return 0.0;
-    if (s > 8.0e-28f && s <= 3.0e38f) return s;
+__device__ __noinline__ double chunk_squares_wide(const void* p, long long first, long long count) {
     double d = 0.0;
-#pragma unroll
-    for (int k = 0; k < kUnrollGroups; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d += (double)v[k][j] * (double)v[k][j];
+    for (int i = 0; i < Groups<BF16>::kCount; ++i)
+        for (int j = 0; j < 8; ++j) {
+            const long long at = first + i * 8ll * kThreads + j;
+            const double v = at >= 0 && at < count ? (double)load_one<BF16>(p, at) : 0.0;
+            d += v * v;
+        }
     return d;
 }
-
-// Index of the gradient that chunk c lies in.
-template <int N>
-__device__ __forceinline__ int find_entry(const GradTable<N>& t, uint32_t c) {
-    int lo = 0, hi = t.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (t.e[mid].first <= c)
-            lo = mid;
-        else
-            hi = mid - 1;
+// The same, in fp32 by four sums of at most 16 values; where one of them is beyond the range in which every square
+// that counts is exact to 2^-24 (an overflow, or values below 2^-45), in 64 bits, so that the norm is right for
+// gradients of any scale.  Sums of zeros that are exact are the common case among small ones.
+template <bool BF16>
+__device__ __forceinline__ double chunk_squares(const GradEntry& e, long long g0) {
+    Groups<BF16> g;
+    g.load(e, g0, true);
+    float s[4] = {};
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < g.kCount; ++i) {
+        float v[8];
+        g.get(i, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[(i * 8 + j) & 3] = fmaf(v[j], v[j], s[(i * 8 + j) & 3]);
+#pragma unroll
+        for (int j = 0; j < g.kPer; ++j) any |= BF16 ? g.r[i * g.kPer + j] & 0x7fff7fffu : g.r[i * g.kPer + j] << 1;
     }
-    return lo;
+    const float least = fminf(fminf(s[0], s[1]), fminf(s[2], s[3])), sum = (s[0] + s[1]) + (s[2] + s[3]);
+    if ((least > 8.0e-28f && sum <= 3.0e38f) || any == 0) return sum;
+    return chunk_squares_wide<BF16>(e.p, (g0 + threadIdx.x) * 8 - e.pad, e.count);
 }
+
+// The chunks of this block, one after another, and the gradient that each lies in.
+struct ChunkWalk {
+    uint32_t c, to;
+    int i;
+    template <int N>
+    __device__ __forceinline__ explicit ChunkWalk(const GradTable<N>& t)
+        : c((uint32_t)((uint64_t)t.chunks * blockIdx.x / gridDim.x)),
+          to((uint32_t)((uint64_t)t.chunks * (blockIdx.x + 1) / gridDim.x)), i(t.start[blockIdx.x]) {}
+    template <int N>
+    __device__ __forceinline__ const GradEntry& entry(const GradTable<N>& t) {
+        while (i + 1 < t.n && t.e[i + 1].first <= c) ++i;
+        return t.e[i];
+    }
+};
 
 __device__ __forceinline__ double block_sum(double d) {
     __shared__ double part[kThreads / 32];
@@ -108,19 +147,15 @@ __device__ __forceinline__ double block_sum(double d) {
 // Block b sums a contiguous share of the chunks; the block that comes last adds up all blocks' sums in
 // their order, so the same gradients give the same bits.
 template <int N>
-__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ GradTable<N> t, double* partial,
+__global__ void __launch_bounds__(kThreads, kFit) k_grad_norm(const __grid_constant__ GradTable<N> t, double* partial,
                                                         double* running, int* arrived, float* norm, int first, int last) {
     pdl_trigger();
     pdl_wait();
-    const uint32_t from = (uint32_t)((uint64_t)t.chunks * blockIdx.x / gridDim.x);
-    const uint32_t to = (uint32_t)((uint64_t)t.chunks * (blockIdx.x + 1) / gridDim.x);
     double sum = 0.0;
-    int i = from < to ? find_entry(t, from) : 0;
-    for (uint32_t c = from; c < to; ++c) {
-        while (i + 1 < t.n && t.e[i + 1].first <= c) ++i;
-        const GradEntry& e = t.e[i];
-        const long long g0 = (long long)(c - e.first) * kChunkGroups;
-        sum += e.bf16 ? chunk_squares<true>(e, g0) : chunk_squares<false>(e, g0);
+    for (ChunkWalk w(t); w.c < w.to; ++w.c) {
+        const GradEntry& e = w.entry(t);
+        const long long k = w.c - e.first;
+        sum += e.bf16 ? chunk_squares<true>(e, k * kChunkGroups16) : chunk_squares<false>(e, k * kChunkGroups32);
     }
     sum = block_sum(sum);
     __shared__ bool is_last;
@@ -146,58 +181,53 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
 
 template <bool IN16, bool OUT16>
 __device__ __forceinline__ void chunk_scale(const GradEntry& e, long long g0, float f) {
-    const bool vec = ((reinterpret_cast<uintptr_t>(e.p) - e.pad * (IN16 ? 2 : 4)) & 15) == 0;
-    float v[kUnrollGroups][8];
+    Groups<IN16> g;
+    g.load(e, g0, ((reinterpret_cast<uintptr_t>(e.p) - e.pad * (IN16 ? 2 : 4)) & 15) == 0);
 #pragma unroll
-    for (int k = 0; k < kUnrollGroups; ++k)
-        load_eight<IN16>(e.p, (g0 + k * kThreads + threadIdx.x) * 8 - e.pad, e.count, vec, v[k]);
+    for (int i = 0; i < g.kCount; ++i) {
+        float v[8];
+        g.get(i, v);
 #pragma unroll
-    for (int k = 0; k < kUnrollGroups; ++k) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] *= f;
-        store_eight<OUT16>(e.out, (g0 + k * kThreads + threadIdx.x) * 8 - e.pad, e.count, v[k]);
+        for (int j = 0; j < 8; ++j) v[j] *= f;
+        store_eight<OUT16>(e.out, (g0 + i * kThreads + threadIdx.x) * 8 - e.pad, e.count, v);
     }
 }
 
 // out = g times max_norm / norm where the norm is finite and beyond max_norm, else g itself; in place
 // nothing is read or written then.
 template <int N>
-__global__ void __launch_bounds__(kThreads) k_grad_clip(const __grid_constant__ GradTable<N> t, const float* norm,
+__global__ void __launch_bounds__(kThreads, kFit) k_grad_clip(const __grid_constant__ GradTable<N> t, const float* norm,
                                                         float max_norm, int in_place) {
     pdl_trigger();
     pdl_wait();
     const float x = *norm;
     const float f = x > max_norm && x <= 3.402823466e38f ? max_norm / x : 1.f;
     if (in_place && f == 1.f) return;
-    const uint32_t from = (uint32_t)((uint64_t)t.chunks * blockIdx.x / gridDim.x);
-    const uint32_t to = (uint32_t)((uint64_t)t.chunks * (blockIdx.x + 1) / gridDim.x);
-    int i = from < to ? find_entry(t, from) : 0;
-    for (uint32_t c = from; c < to; ++c) {
-        while (i + 1 < t.n && t.e[i + 1].first <= c) ++i;
-        const GradEntry& e = t.e[i];
-        const long long g0 = (long long)(c - e.first) * kChunkGroups;
+    for (ChunkWalk w(t); w.c < w.to; ++w.c) {
+        const GradEntry& e = w.entry(t);
+        const long long k = w.c - e.first;
         if (e.bf16)
-            e.out_bf16 ? chunk_scale<true, true>(e, g0, f) : chunk_scale<true, false>(e, g0, f);
+            e.out_bf16 ? chunk_scale<true, true>(e, k * kChunkGroups16, f)
+                       : chunk_scale<true, false>(e, k * kChunkGroups16, f);
         else
-            e.out_bf16 ? chunk_scale<false, true>(e, g0, f) : chunk_scale<false, false>(e, g0, f);
+            e.out_bf16 ? chunk_scale<false, true>(e, k * kChunkGroups32, f)
+                       : chunk_scale<false, false>(e, k * kChunkGroups32, f);
     }
 }
 
 template <int N>
 cudaError_t norm_of(const GradList& l, int from, int to, const GradNormArgs& a, bool last, cudaStream_t s) {
     GradTable<N> t;
-    l.table(from, to, &t);
-    const int blocks = (int)std::min<long long>(t.chunks, 4ll * a.sm_count);
-    return launch_pdl(k_grad_norm<N>, dim3(std::max(blocks, 1)), dim3(kThreads), 0, s, t, a.partial, a.running, a.arrived,
+    const int blocks = l.table(from, to, kFit * a.sm_count, &t);
+    return launch_pdl(k_grad_norm<N>, dim3(blocks), dim3(kThreads), 0, s, t, a.partial, a.running, a.arrived,
                       a.norm, from == 0, (int)last);
 }
 template <int N>
 cudaError_t clip_of(const GradList& l, int from, int to, const float* norm, float max_norm, int sm_count,
                     cudaStream_t s) {
     GradTable<N> t;
-    l.table(from, to, &t);
-    const int blocks = (int)std::min<long long>(t.chunks, 4ll * sm_count);
-    return launch_pdl(k_grad_clip<N>, dim3(std::max(blocks, 1)), dim3(kThreads), 0, s, t, norm, max_norm, (int)l.in_place);
+    const int blocks = l.table(from, to, kFit * sm_count, &t);
+    return launch_pdl(k_grad_clip<N>, dim3(blocks), dim3(kThreads), 0, s, t, norm, max_norm, (int)l.in_place);
 }
 
 }  // namespace

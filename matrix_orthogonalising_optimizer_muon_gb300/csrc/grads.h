@@ -8,9 +8,9 @@
 namespace muon {
 
 // A gradient is walked in groups of eight values, the first of which may begin before it so that every
-// whole group is aligned to 16 bytes on the side that is written (the norm: read), in chunks of
-// kChunkGroups groups, one per block and turn.
-constexpr int kChunkGroups = 1024;
+// whole group is aligned to 16 bytes on the side that is written (the norm: read), in chunks of 32 KB, one per
+// block and turn.
+constexpr int kChunkGroups16 = 2048, kChunkGroups32 = 1024;   // groups of a chunk, by the type that is read
 
 struct GradEntry {
     const void* p;
@@ -22,10 +22,12 @@ struct GradEntry {
 };
 
 // Parameters of one launch: at most 32764 bytes, the few for short lists.
-constexpr int kTableFew = 30, kTableMost = 1000;
+constexpr int kTableFew = 30, kTableMost = 960;
+constexpr int kMostBlocks = 640;
 template <int N>
 struct GradTable {
     GradEntry e[N];
+    uint16_t start[kMostBlocks];   // the gradient that each block's first chunk lies in
     int n;
     uint32_t chunks;
 };
@@ -39,8 +41,9 @@ struct GradList {
     int n;
     bool in_place;
 
+    // The table of gradients from .. to - 1 for at most `most` blocks, which share the chunks evenly; returns how many.
     template <int N>
-    void table(int from, int to, GradTable<N>* t) const {
+    int table(int from, int to, int most, GradTable<N>* t) const {
         t->n = to - from;
         long long chunks = 0;
         for (int i = from; i < to; ++i) {
@@ -48,12 +51,19 @@ struct GradList {
             e.p = p[i], e.out = out ? out[i] : nullptr, e.count = counts[i];
             e.bf16 = dtypes[i] == 1, e.out_bf16 = out ? out_dtypes[i] == 1 : 0;
             const uintptr_t at = reinterpret_cast<uintptr_t>(out ? e.out : e.p);
-            const int esz = (out ? e.out_bf16 : e.bf16) ? 2 : 4;
+            const int esz = (out ? e.out_bf16 : e.bf16) ? 2 : 4, groups = e.bf16 ? kChunkGroups16 : kChunkGroups32;
             e.pad = (uint16_t)((at & 15) / esz);
             e.first = (uint32_t)chunks;
-            if (counts[i] > 0) chunks += ((counts[i] + e.pad + 7) / 8 + kChunkGroups - 1) / kChunkGroups;
+            if (counts[i] > 0) chunks += ((counts[i] + e.pad + 7) / 8 + groups - 1) / groups;
         }
         t->chunks = (uint32_t)chunks;
+        const int blocks = (int)std::max<long long>(std::min<long long>(chunks, std::min(most, kMostBlocks)), 1);
+        for (int b = 0, i = 0; b < blocks; ++b) {
+            const uint32_t c = (uint32_t)(t->chunks * (uint64_t)b / blocks);
+            while (i + 1 < t->n && t->e[i + 1].first <= c) ++i;
+            t->start[b] = (uint16_t)i;
+        }
+        return blocks;
     }
 };
 

@@ -1,7 +1,7 @@
 """The norm of all gradients and their clipping on the GPU against fp64.
 
-The squares of up to 32 values are summed in fp32 (33 roundings of 2^-24 at most), the rest in fp64; the norm is the
-root, so half of that, and one rounding to fp32: 18 u.  Scaling: the factor is one fp32 division of the rounded norm,
+The squares of up to 64 values are summed in fp32 (19 roundings of 2^-24 on any way at most), the rest in fp64; the norm
+is the root, so half of that, and one rounding to fp32: below 18 u.  Scaling: the factor is one fp32 division of the rounded norm,
 the product one rounding, then the output type's own: within 2.5 u (fp32) of g max_norm / norm as the call read the norm."""
 import numpy as np
 import pytest
