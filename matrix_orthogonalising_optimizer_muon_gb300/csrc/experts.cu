@@ -15,8 +15,8 @@ namespace {
 // expert in shared memory; the counts of earlier warps, earlier CTAs (read from their shared memory)
 // and smaller experts give each warp its first slot per expert; pass 2 deals the slots out, 32 ids at
 // a time, neighbours with the same expert by their rank among the warp's lanes.  What bounds it is latency:
-// a warp's ids are loaded kBatch groups of 32 at a time (131072 ids: 8 us; 22 one group at a time) and, when
-// that is all it has, kept for pass 2.
+// a warp's ids are loaded kBatch groups of 32 at a time and, when that is all it has, kept for pass 2
+// (131072 ids of 128 experts: 13.3 us, 512 ids 6).
 constexpr int kOrderThreads = 1024;
 constexpr int kOrderCounts = 32768;   // counts in shared memory: warps x experts
 constexpr int kBatch = 16;
@@ -35,9 +35,22 @@ __device__ __forceinline__ void load_ids(const OrderArgs& a, long long from, lon
     for (int j = 0; j < kBatch; ++j) id[j] = (unsigned)id[j] < (unsigned)a.experts ? id[j] : -1;
 }
 
-// warps: that count and deal, a power of two; ctas: of the cluster, 1 or 8.
-__global__ void __launch_bounds__(kOrderThreads) k_expert_order(const OrderArgs a, int warps, int ctas) {
+// Lanes of the warp with the same id < 2^bits: as many votes as bits (the instruction that matches all lanes
+// takes a scheduler 200 cycles, 131072 ids 21 us).
+__device__ __forceinline__ unsigned same_id(int id, int bits) {
+    unsigned peers = 0xffffffffu;
+    for (int b = 0; b < bits; ++b) {
+        const bool one = id >> b & 1;
+        const unsigned with = __ballot_sync(0xffffffffu, one);
+        peers &= one ? with : ~with;
+    }
+    return peers;
+}
+
+// 2^lw warps count and deal; 2^lc CTAs in the cluster, at most 16.
+__global__ void __launch_bounds__(kOrderThreads) k_expert_order(const OrderArgs a, int lw, int lc) {
     extern __shared__ int smem[];
+    const int warps = 1 << lw, ctas = 1 << lc, bits = 32 - __clz(a.experts);   // ids 0 .. experts
     const int E = a.experts, row = warps + 1;   // an expert's counts lie side by side, odd rows against bank conflicts
     int* count = smem;                    // [E][row]
     int* total = smem + E * row;          // [E]: this CTA's counts
@@ -65,11 +78,12 @@ __global__ void __launch_bounds__(kOrderThreads) k_expert_order(const OrderArgs 
     __syncthreads();
     // counts of earlier warps: `warps` lanes per expert
     const int sub = lane & (warps - 1);
-    for (int e0 = warp * (32 / warps); e0 < E; e0 += kOrderThreads / warps) {
-        const int e = e0 + lane / warps, c = e < E ? count[e * row + sub] : 0;
+    for (int e0 = warp << (5 - lw); e0 < E; e0 += kOrderThreads >> lw) {
+        const int e = e0 + (lane >> lw), c = e < E ? count[e * row + sub] : 0;
         int sum = c;
-        for (int d = 1; d < warps; d *= 2) {
-            const int o = __shfl_up_sync(0xffffffffu, sum, d, warps);
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
             if (sub >= d) sum += o;
         }
         if (e < E) {
@@ -83,13 +97,14 @@ __global__ void __launch_bounds__(kOrderThreads) k_expert_order(const OrderArgs 
         __syncthreads();
     // counts of earlier CTAs, and of all: a lane per CTA, the sums to base and, for now, the first counts' row end
     for (int i0 = 0; i0 < E * ctas; i0 += kOrderThreads) {
-        const int i = i0 + threadIdx.x, e = i / ctas, r = i - e * ctas;
+        const int i = i0 + threadIdx.x, e = i >> lc, r = i & (ctas - 1);
         int all = 0;
         if (e < E) all = ctas > 1 ? remote_int(smem_u32(total + e), r) : total[e];
         int before = r < rank ? all : 0;
-        for (int d = 1; d < ctas; d *= 2) {
-            all += __shfl_xor_sync(0xffffffffu, all, d);
-            before += __shfl_xor_sync(0xffffffffu, before, d);
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) {
+            const int x = __shfl_xor_sync(0xffffffffu, all, d), y = __shfl_xor_sync(0xffffffffu, before, d);
+            if (d < ctas) all += x, before += y;
         }
         if (e < E && r == 0) base[e] = before, count[e * row + warps] = all;
     }
@@ -127,7 +142,7 @@ __global__ void __launch_bounds__(kOrderThreads) k_expert_order(const OrderArgs 
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (i + 32 * j >= to) break;
-            const unsigned peers = __match_any_sync(0xffffffffu, id[j]);
+            const unsigned peers = same_id(id[j] < 0 ? E : id[j], bits);
             const int rk = __popc(peers & ((1u << lane) - 1));
             int slot = -1;
             int* mine = count + id[j] * row + warp;
@@ -294,15 +309,22 @@ unsigned row_blocks(const MoveArgs& a, int fit) {
 }  // namespace
 
 cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s) {
-    int warps = kOrderThreads / 32;
-    while (warps * a.experts > kOrderCounts) warps /= 2;
-    const int ctas = a.n <= 8192 ? 1 : 8;
-    const size_t bytes = (size_t)(warps + 3) * a.experts * sizeof(int);
+    int lw = 5;
+    while ((a.experts << lw) > kOrderCounts) --lw;
+    // One CTA for the smallest (8192 ids of 256: 10.8 us, 8.1 with eight), the largest cluster there is for long ones,
+    // whose ranking is bound by instruction issue, unless reading all CTAs' counts takes longer: 65536 ids of 256
+    // 12.8 us with eight CTAs and 14.3 with sixteen, 131072 of 128 16.1 and 13.3, of 4096 51 and 84.
+    const int lc = a.n <= 2048 ? 0 : a.n >= 100000 && a.experts <= 1024 ? 4 : 3;
+    if (lc == 4) {
+        const cudaError_t e = cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    const size_t bytes = (size_t)((1 << lw) + 3) * a.experts * sizeof(int);
     // per call: an attribute of the current device
     const cudaError_t set =
         cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (set != cudaSuccess) return set;
-    return launch_pdl_cluster(k_expert_order, dim3(ctas), dim3(kOrderThreads), bytes, s, (unsigned)ctas, a, warps, ctas);
+    return launch_pdl_cluster(k_expert_order, dim3(1 << lc), dim3(kOrderThreads), bytes, s, 1u << lc, a, lw, lc);
 }
 
 cudaError_t launch_expert_dispatch(const MoveArgs& a, bool bf16, bool vec, cudaStream_t s) {
