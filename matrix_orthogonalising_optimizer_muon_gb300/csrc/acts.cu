@@ -19,7 +19,7 @@ namespace {
 using namespace muon_impl;
 
 constexpr size_t kWsHeader = 256 + kCounters * sizeof(int);   // status word, counters
-constexpr int64_t kGradWorkspace = (int64_t)kWsHeader + kPartialFloats * 4;
+constexpr int64_t kGradWorkspace = (int64_t)kWsHeader + kPartialFloats * 4 + kAlignedBytes;
 static_assert(kWsHeader % 256 == 0, "the partial sums are aligned");
 
 constexpr int64_t kMostPitch = 1ll << 32;   // bytes from row to row
@@ -179,6 +179,7 @@ muon_status product(muon_grad_plan_s* p, const void* x, int64_t ldx, const void*
     a.x = x, a.ldx = ldx, a.weight = weight, a.y = y, a.ldy = ldy, a.tokens = tokens, a.m = (int)m, a.n = (int)n;
     a.transposed = transposed, a.offsets = offsets, a.groups = std::max(groups, 1);
     a.status = p->status, a.partial = p->partial, a.counters = p->counters;
+    a.aligned = p->partial + kPartialFloats;
     return cuda_status(launch_product(a, p->sm_count, static_cast<cudaStream_t>(stream)));
 }
 

@@ -111,6 +111,7 @@ struct ProductArgs {
     const void* weight;  // groups x m x n bf16, dense
     void* y;             // tokens x out bf16, row pitch ldy
     long long ldy;
+    int first;           // of these tokens among those that offsets counts
     long long tokens;
     int m, n;
     bool transposed;     // y = x W (k = m, out = n), else y = x W^T (k = n, out = m)
@@ -119,7 +120,9 @@ struct ProductArgs {
     int* status;
     float* partial;
     int* counters;
+    void* aligned;       // kAlignedBytes for rows that are not
 };
+constexpr long long kAlignedBytes = 256ll << 20;
 
 // bf16: the dtype of the Mat operands; vec: every one of them (and ld) 16-byte aligned.
 cudaError_t launch_act_pack(const PackArgs& a, bool bf16, bool vec, cudaStream_t s);

@@ -9,8 +9,8 @@
 //
 // A cluster of two CTAs computes tiles of 256 outputs x up to 256 tokens (tcgen05.mma.cta_group::2, fp32
 // accumulators in TMEM, double-buffered).  Per CTA: warp 0 issues the TMA loads, warp 1 the MMAs (the
-// even CTA's), warps 2-9 are the epilogue; where rows are not 16-byte aligned, 16 more warps copy them into
-// shared memory instead of TMA.  A step is 64 values of the contraction: 16 KB of the weight and up to
+// even CTA's), warps 2-9 are the epilogue, two for each quarter of the TMEM lanes, on alternate blocks of 32
+// tokens.  A step is 64 values of the contraction: 16 KB of the weight and up to
 // 16 KB of tokens per CTA, in a ring of six.
 //
 // How the work is dealt out (every CTA derives the same plan from the offsets): tiles in the order experts,
@@ -34,16 +34,8 @@ namespace {
 
 constexpr int kStepK = 64;
 constexpr int kRing = 6;
-constexpr int kEpiFirst = 2;
-constexpr int kCopyGroups = 4, kGroupWarps = 4;    // copying warps: groups that take steps in turn
-// Epilogue warps: two for each quarter of the TMEM lanes, on alternate blocks of 32 tokens; one where the copying
-// warps leave no registers for more.
-template <bool COPY>
-struct Roles {
-    static constexpr int kEpi = COPY ? 4 : 8;
-    static constexpr int kCopyFirst = kEpiFirst + kEpi;
-    static constexpr int kThreads = 32 * (kCopyFirst + (COPY ? kCopyGroups * kGroupWarps : 0));
-};
+constexpr int kEpiFirst = 2, kEpi = 8;             // epilogue warps
+constexpr int kThreads = 32 * (kEpiFirst + kEpi);
 constexpr int kBand = 8;
 constexpr int kBins = 512;                         // experts are searched in at most this many bins
 constexpr int kItems = 96;                         // items decoded at the start
@@ -54,9 +46,8 @@ struct Cfg {
     static constexpr int SLOT_BYTES = 2 * A_BYTES;
     static constexpr int OUT_OFFSET = kRing * SLOT_BYTES;
     static constexpr int OUT_WARP = 2048;                 // 32 outputs x 32 tokens in bf16
-    static constexpr int BAR_OFFSET = OUT_OFFSET + 8 * OUT_WARP;
-    static constexpr int SIGNAL_OFFSET = BAR_OFFSET + 256;   // 16 bytes per copying warp
-    static constexpr int PLAN_OFFSET = SIGNAL_OFFSET + 256;
+    static constexpr int BAR_OFFSET = OUT_OFFSET + kEpi * OUT_WARP;
+    static constexpr int PLAN_OFFSET = BAR_OFFSET + 256;
     static constexpr int ITEM_OFFSET = PLAN_OFFSET + 4 * kBins * 4 + 2 * kBins * 2 + 416;
     static constexpr int SMEM_BYTES = ITEM_OFFSET + kItems * 32 + 1024;
 };
@@ -82,7 +73,6 @@ struct ProductLaunch {
     CUtensorMap map_w, map_x[4];   // map_x: boxes of 128, 64, 32 and 16 tokens
     ProductArgs a;
     int out, k, steps, tiles_m;    // outputs, contraction, its steps, tiles along the outputs
-    int tma_w, tma_x;              // rows are aligned to 16 bytes
     int wide;                      // rows of y are aligned to four elements
     Divisor by_tiles;              // by tiles_m
     int tiles[3];                  // one weight: token tiles when they are at most 256, 128, 64 tokens high
@@ -114,8 +104,9 @@ struct __align__(16) Item {
 };
 
 __device__ __forceinline__ void expert_range(const ProductArgs& a, int g, int* begin, int* end) {   // tokens < 2^31
-    *begin = a.offsets ? min(max(a.offsets[g], 0), (int)a.tokens) : 0;
-    *end = a.offsets ? min(max(a.offsets[g + 1], *begin), (int)a.tokens) : (int)a.tokens;
+    const int last = a.first + (int)a.tokens;
+    *begin = a.offsets ? min(max(a.offsets[g], a.first), last) - a.first : 0;
+    *end = a.offsets ? max(min(max(a.offsets[g + 1], a.first), last) - a.first, *begin) : (int)a.tokens;
 }
 
 // An expert's token tiles: as few as the greatest height allows, of equal height in steps of 32 (the last
@@ -349,9 +340,6 @@ struct Items {
     }
 };
 
-__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -361,48 +349,12 @@ __device__ __forceinline__ void sts32(uint32_t a, uint32_t x) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
 }
 
-// Rows first, first + step, ... of a swizzled operand box of 64 values a row (kBatch at a time), from rows
-// that are not 16-byte aligned: a lane makes 16 bytes from the two aligned pieces that hold them.  Every piece
-// loaded holds a value of its row.  Rows at and beyond `rows` and columns at and beyond `cols` become zero.
-constexpr int kBatch = 4;
-__device__ __forceinline__ void copy_rows(const char* base, long long pitch, int rows, int col, int cols, uint32_t dst,
-                                          int count, int lane, int warp) {
-    const int j = lane & 7, c = col + 8 * j;
-    for (int r0 = 4 * warp; r0 < count; r0 += 4 * kGroupWarps * kBatch) {
-        uint32_t v[kBatch][8];
-        int d[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * 4 * kGroupWarps + (lane >> 3);
-            const uintptr_t line = reinterpret_cast<uintptr_t>(base) + (uintptr_t)(r * pitch);
-            const uintptr_t at = line + (uintptr_t)(2ll * c);
-            d[i] = (int)(at & 15);
-            const uint4* q = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
-            const bool live = r < rows && r < count && c < cols;
-            uint4 x = make_uint4(0, 0, 0, 0), y = x;
-            if (live) x = *q;
-            if (live && d[i] && reinterpret_cast<uintptr_t>(q + 1) < line + 2ull * cols) y = q[1];
-            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-            v[i][4] = y.x, v[i][5] = y.y, v[i][6] = y.z, v[i][7] = y.w;
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * 4 * kGroupWarps + (lane >> 3);
-            words_down<true>(v[i], d[i]);
-            const int left = cols - c;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[i][k] &= left > 2 * k + 1 ? 0xffffffffu : left > 2 * k ? 0xffffu : 0u;
-            if (r < count) sts128(dst + r * 128 + ((j ^ (r & 7)) << 4), make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]));
-        }
-    }
-}
-
 struct Epilogue {
     uint32_t tmem_base, tempty_lead, blk, table;
     uint64_t* tfull;
     volatile int* abort_flag;
     int q, wq, lane;
-    int first, step;   // this warp's first block of tokens, and from one to its next
+    int first;   // this warp's first block of tokens, every other of which are its
 };
 
 // Hands accumulator `acc` back to the MMA warp once this warp's last load from it is complete.
@@ -472,7 +424,6 @@ __device__ __forceinline__ void part_store(float* p, const uint32_t (&v)[32]) {
 }
 
 // One epilogue warp: TMEM lane quarter wq, that is 32 outputs of a tile, and every block of tokens or every other.
-template <bool COPY>
 __device__ __forceinline__ void epilogue(const ProductLaunch& L, const Plan& plan, const Outline& outline,
                                          const Items& items, const Epilogue& e) {
     int local = 0;
@@ -488,11 +439,11 @@ __device__ __forceinline__ void epilogue(const ProductLaunch& L, const Plan& pla
         auto slot = [&](int k) {
             return L.a.partial + ((2 * (first + k) + (k == 0)) * 8ll + 4 * e.q + e.wq) * 8192 + e.lane * 4;
         };
-        for (int c = e.first; c < w.n; c += e.step) {
+        for (int c = e.first; c < w.n; c += 64) {
             uint32_t v[32];
             tmem_ld32(tbase + c, v);
             tmem_ld_wait();
-            if (c + e.step >= w.n) release_tmem(e, acc);
+            if (c + 64 >= w.n) release_tmem(e, acc);
             if (parts) {
                 part_store(slot(part) + c * 32, v);
             } else {
@@ -512,19 +463,14 @@ __device__ __forceinline__ void epilogue(const ProductLaunch& L, const Plan& pla
                 asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(seen) : "l"(count) : "memory");
             if (__shfl_sync(0xffffffffu, seen, 0) == parts - 1) {   // the last part: all of them, in their order
                 if (e.lane == 0) *count = 0;   // for the next call
-                for (int c = e.first; c < w.n; c += e.step) {
+                for (int c = e.first; c < w.n; c += 64) {
                     Block a;
                     a.load(slot(0) + c * 32);
                     float f[32] = {};
                     for (int k = 0; k < parts; ++k) {
-                        if (COPY) {
-                            a.add_to(f);
-                            if (k + 1 < parts) a.load(slot(k + 1) + c * 32);
-                        } else {   // the next part is on its way while this one is added
-                            const Block b = a;
-                            if (k + 1 < parts) a.load(slot(k + 1) + c * 32);
-                            b.add_to(f);
-                        }
+                        const Block b = a;   // the next part is on its way while this one is added
+                        if (k + 1 < parts) a.load(slot(k + 1) + c * 32);
+                        b.add_to(f);
                     }
                     store_block(L, e, f, c0, w.t0 + c, w.end);
                 }
@@ -533,10 +479,9 @@ __device__ __forceinline__ void epilogue(const ProductLaunch& L, const Plan& pla
     }
 }
 
-// MN: the weight is MN-major (dx = dy W).  COPY: an operand's rows are not aligned.
-template <bool MN, bool COPY>
-__global__ void __launch_bounds__(Roles<COPY>::kThreads) k_product(const __grid_constant__ ProductLaunch L) {
-    using R = Roles<COPY>;
+// MN: the weight is MN-major (dx = dy W).
+template <bool MN>
+__global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ ProductLaunch L) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::BAR_OFFSET);
@@ -554,17 +499,17 @@ __global__ void __launch_bounds__(Roles<COPY>::kThreads) k_product(const __grid_
     const bool leader = q == 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRing; ++s) {
-            mbar_init(full + s, 1 + (COPY ? kGroupWarps : 0));
+            mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull + a, 1);
-            mbar_init(tempty + a, 2 * R::kEpi);
+            mbar_init(tempty + a, 2 * kEpi);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        if (!COPY || L.tma_w) tma_prefetch_desc(&L.map_w);
+        tma_prefetch_desc(&L.map_w);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
@@ -576,60 +521,52 @@ __global__ void __launch_bounds__(Roles<COPY>::kThreads) k_product(const __grid_
     const uint32_t tmem_base = *tmem_slot;
     pdl_trigger();
     pdl_wait();
-    const Outline outline = make_plan(L, plan, R::kThreads);
+    const Outline outline = make_plan(L, plan, kThreads);
     const Items items(L, plan, outline);
-    for (int t = threadIdx.x; t < min(items.count, kItems); t += R::kThreads)
+    for (int t = threadIdx.x; t < min(items.count, kItems); t += kThreads)
         reinterpret_cast<Item*>(smem + Cfg::ITEM_OFFSET)[t] = items.decode(L, plan, outline, t);
     __syncthreads();
 
     if (warp == 0) {
         // ---------------- TMA, completion on the even CTA's barrier.  The whole warp runs the loop and one elected
         // lane issues (a loop of one lane alone: 64 us against 58 for the 32 experts' product; a second warp
-        // for the tokens gains nothing more).  Where all rows are copied, the odd CTA's warp must not even wait:
-        // nothing waits for it, so the ring could pass it by two rounds, whose parity it takes for none.
-        if (!COPY || leader || L.tma_w || L.tma_x) {
-            const bool one = elect_one();
-            uint32_t slot = 0, ph = 1;
-            bool ok = true;
-            for (int turn = 0; ok && turn < items.count; ++turn) {
-                const Item w = items.get(L, plan, outline, table, turn);
-                const int rows = w.n >> 1, t0 = w.t0 + (int)q * rows, m0 = w.m0 + 128 * (int)q;
-                const uint32_t bytes = (!COPY || L.tma_w ? 2 * Cfg::A_BYTES : 0) + (!COPY || L.tma_x ? 2 * rows * 128 : 0) +
-                                       (COPY ? 16 * kGroupWarps : 0);
-                for (int k = w.k0; k < w.k1; ++k) {
-                    if (!mbar_wait_idle(empty + slot, ph, abort_flag, L.a.status, kStatusTimeoutProducer, true)) {
-                        ok = false;
-                        break;
-                    }
-                    if (one) {
-                        uint8_t* to = smem + slot * Cfg::SLOT_BYTES;
-                        const uint32_t fb = mapa_shared(smem_u32(full + slot), 0);
-                        const int kk = k * kStepK;
-                        if (leader) mbar_arrive_expect_tx(full + slot, bytes);
-                        if (!COPY || L.tma_w) {
-                            if (MN) {
-                                tma_load_3d_pair(to, &L.map_w, fb, m0, kk, w.group);
-                                tma_load_3d_pair(to + Cfg::CHUNK_BYTES, &L.map_w, fb, m0 + 64, kk, w.group);
-                            } else {
-                                tma_load_3d_pair(to, &L.map_w, fb, kk, m0, w.group);
-                            }
-                        }
-                        if (COPY && !L.tma_x) {
-                        } else if (rows == 128) {
-                            tma_load_2d_pair(to + Cfg::A_BYTES, &L.map_x[0], fb, kk, t0);
-                        } else {
-                            int at = 0;
-#pragma unroll
-                            for (int b = 1; b < 4; ++b) {
-                                if (rows & (128 >> b)) {
-                                    tma_load_2d_pair(to + Cfg::A_BYTES + at * 128, &L.map_x[b], fb, kk, t0 + at);
-                                    at += 128 >> b;
-                                }
-                            }
-                        }
-                    }
-                    if (++slot == kRing) slot = 0, ph ^= 1u;
+        // for the tokens gains nothing more)
+        const bool one = elect_one();
+        uint32_t slot = 0, ph = 1;
+        bool ok = true;
+        for (int turn = 0; ok && turn < items.count; ++turn) {
+            const Item w = items.get(L, plan, outline, table, turn);
+            const int rows = w.n >> 1, t0 = w.t0 + (int)q * rows, m0 = w.m0 + 128 * (int)q;
+            for (int k = w.k0; k < w.k1; ++k) {
+                if (!mbar_wait_idle(empty + slot, ph, abort_flag, L.a.status, kStatusTimeoutProducer, true)) {
+                    ok = false;
+                    break;
                 }
+                if (one) {
+                    uint8_t* to = smem + slot * Cfg::SLOT_BYTES;
+                    const uint32_t fb = mapa_shared(smem_u32(full + slot), 0);
+                    const int kk = k * kStepK;
+                    if (leader) mbar_arrive_expect_tx(full + slot, 2 * (Cfg::A_BYTES + rows * 128));
+                    if (MN) {
+                        tma_load_3d_pair(to, &L.map_w, fb, m0, kk, w.group);
+                        tma_load_3d_pair(to + Cfg::CHUNK_BYTES, &L.map_w, fb, m0 + 64, kk, w.group);
+                    } else {
+                        tma_load_3d_pair(to, &L.map_w, fb, kk, m0, w.group);
+                    }
+                    if (rows == 128) {
+                        tma_load_2d_pair(to + Cfg::A_BYTES, &L.map_x[0], fb, kk, t0);
+                    } else {
+                        int at = 0;
+#pragma unroll
+                        for (int b = 1; b < 4; ++b) {
+                            if (rows & (128 >> b)) {
+                                tma_load_2d_pair(to + Cfg::A_BYTES + at * 128, &L.map_x[b], fb, kk, t0 + at);
+                                at += 128 >> b;
+                            }
+                        }
+                    }
+                }
+                if (++slot == kRing) slot = 0, ph ^= 1u;
             }
         }
     } else if (warp == 1) {
@@ -695,7 +632,7 @@ __global__ void __launch_bounds__(Roles<COPY>::kThreads) k_product(const __grid_
             }
             __syncwarp();
         }
-    } else if (warp < R::kCopyFirst) {
+    } else {
         // ---------------- epilogue
         Epilogue e;
         e.tmem_base = tmem_base;
@@ -705,53 +642,8 @@ __global__ void __launch_bounds__(Roles<COPY>::kThreads) k_product(const __grid_
         e.tfull = tfull;
         e.abort_flag = abort_flag;
         e.q = (int)q, e.wq = warp & 3, e.lane = lane;
-        e.first = (warp - kEpiFirst) / 4 * 32, e.step = R::kEpi / 4 * 32;
-        epilogue<COPY>(L, plan, outline, items, e);
-    } else if (COPY) {
-        // ---------------- copies of rows that are not aligned: group g takes every kCopyGroups-th step
-        const int cw = (warp - R::kCopyFirst) % kGroupWarps;
-        const uint32_t g = (warp - R::kCopyFirst) / kGroupWarps;
-        const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
-        const uint32_t signal_lead = mapa_shared(smem_u32(smem + Cfg::SIGNAL_OFFSET), 0) + 16 * (warp - R::kCopyFirst);
-        uint32_t it = 0, slot = 0, ph = 1;
-        bool ok = true;
-        for (int turn = 0; ok && turn < items.count; ++turn) {
-            const Item w = items.get(L, plan, outline, table, turn);
-            const int rows = w.n >> 1, t0 = w.t0 + (int)q * rows, m0 = w.m0 + 128 * (int)q;
-            const char* wp = static_cast<const char*>(L.a.weight) + (long long)w.group * L.a.m * L.a.n * 2;
-            const char* xp = static_cast<const char*>(L.a.x) + t0 * L.a.ldx * 2;
-            for (int k = w.k0; k < w.k1; ++k, ++it) {
-                const uint32_t s = slot, parity = ph;
-                if (++slot == kRing) slot = 0, ph ^= 1u;
-                if (it % kCopyGroups != g) continue;
-                if (!mbar_wait_idle(empty + s, parity, abort_flag, L.a.status, kStatusTimeoutProducer, true)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t sa = smem_u32(smem + s * Cfg::SLOT_BYTES);
-                const int kk = k * kStepK;
-                if (!L.tma_w) {
-                    if (MN) {
-                        const char* p = wp + (long long)kk * L.a.n * 2;
-                        copy_rows(p, L.a.n * 2ll, L.a.m - kk, m0, L.a.n, sa, kStepK, lane, cw);
-                        copy_rows(p, L.a.n * 2ll, L.a.m - kk, m0 + 64, L.a.n, sa + Cfg::CHUNK_BYTES, kStepK, lane, cw);
-                    } else {
-                        copy_rows(wp + (long long)m0 * L.a.n * 2, L.a.n * 2ll, L.a.m - m0, kk, L.a.n, sa, 128, lane, cw);
-                    }
-                }
-                if (!L.tma_x) copy_rows(xp, L.a.ldx * 2, w.end - t0, kk, L.k, sa + Cfg::A_BYTES, rows, lane, cw);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // writes visible to the MMAs
-                __syncwarp();
-                if (lane == 0) {
-                    // the odd CTA's arrival is a copy of 16 bytes that mean nothing, whose completion releases
-                    // at cluster scope, which no thread has to wait for
-                    if (leader)
-                        mbar_arrive(full + s);
-                    else
-                        bulk_signal(signal_lead, smem + Cfg::SIGNAL_OFFSET + 16 * (warp - R::kCopyFirst), full_lead + s * 8);
-                }
-            }
-        }
+        e.first = (warp - kEpiFirst) / 4 * 32;
+        epilogue(L, plan, outline, items, e);
     }
 
     __syncwarp();
@@ -780,45 +672,156 @@ bool map_tokens(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-typedef void (*ProductKernel)(ProductLaunch);
-ProductKernel pick(bool mn, bool copy) {
-    static const ProductKernel k[2][2] = {{k_product<false, false>, k_product<false, true>},
-                                          {k_product<true, false>, k_product<true, true>}};
-    return k[mn][copy];
-}
+// ------------------------------------------------------------------ rows that TMA cannot read
+// TMA takes rows whose addresses are multiples of 16 bytes.  Others are first copied into aligned rows in the
+// workspace, at HBM's rate, chunk by chunk where they do not fit: 8192 x 3584 x 3585 takes 174 us, its 16-byte
+// aligned neighbour 108 (396 when the
+// product's own warps copied each operand of each tile through shifts, bound by the latency of that way).
+struct Job {
+    const char* src;
+    char* dst;
+    long long pitch;      // of src, bytes
+    uint32_t dst_pitch;   // a multiple of 16
+    uint32_t rows;
+    int cols;
+    uint32_t per_expert;  // rows of each expert, of which those without tokens are left out; 0: all rows
+};
+struct AlignArgs {
+    Job job[2];
+    ProductArgs a;
+};
 
-}  // namespace
-
-cudaError_t product_prepare() {
-    for (int i = 0; i < 4; ++i) {
-        const cudaError_t e = cudaFuncSetAttribute(pick(i & 1, i >> 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   Cfg::SMEM_BYTES);
-        if (e != cudaSuccess) return e;
+constexpr int kAlignThreads = 256;
+__global__ void __launch_bounds__(kAlignThreads) k_align_rows(const AlignArgs args) {
+    const int lane = threadIdx.x & 31;
+    pdl_trigger();
+    pdl_wait();
+    for (int i = 0; i < 2; ++i) {
+        const Job& j = args.job[i];
+        for (RowWalk<kAlignThreads> w(j.cols); w.row < j.rows; w.next()) {
+            if (j.per_expert && args.a.offsets) {
+                int begin, end;
+                expert_range(args.a, (int)(w.row / j.per_expert), &begin, &end);
+                if (begin == end) continue;
+            }
+            const char* from = j.src + w.row * j.pitch;
+            char* to = j.dst + (uint64_t)w.row * j.dst_pitch;
+            Raw<true, kShifted> raw[kUnroll];
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) raw[k].load(from, w.col + k * kSeg, j.cols, lane);
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+                if (w.col + k * kSeg < j.cols) seg_store_words<true, kAligned>(to, w.col + k * kSeg, j.cols, lane, raw[k].r);
+        }
     }
-    return cudaSuccess;
 }
 
-cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s) {
+typedef void (*ProductKernel)(ProductLaunch);
+ProductKernel pick(bool mn) { return mn ? k_product<true> : k_product<false>; }
+
+// A product whose rows are aligned: of a.groups weights whose rows are `pitch` elements apart, `out` outputs.
+cudaError_t launch_aligned(const ProductArgs& a, int out, long long pitch, int sm_count, cudaStream_t s) {
     ProductLaunch L;
     L.a = a;
-    L.out = a.transposed ? a.n : a.m;
+    L.out = out;
     L.k = a.transposed ? a.m : a.n;
     L.steps = (L.k + kStepK - 1) / kStepK;
     L.tiles_m = (L.out + 255) / 256;
     L.by_tiles.set(L.tiles_m);
     for (int i = 0; i < 3; ++i) L.tiles[i] = (int)((a.tokens + (256 >> i) - 1) / (256 >> i));
     if ((a.tokens / 64 + a.groups) * L.tiles_m >= (1ll << 31)) return cudaErrorInvalidValue;
-    L.tma_w = a.n % 8 == 0 && (reinterpret_cast<uintptr_t>(a.weight) & 15) == 0;
-    L.tma_x = ((reinterpret_cast<uintptr_t>(a.x) | (uintptr_t)(a.ldx * 2)) & 15) == 0;
     L.wide = L.out % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)(a.ldy * 2)) & 7) == 0;
-    if (L.tma_w && !muon_impl::make_map(&L.map_w, const_cast<void*>(a.weight), true, a.n, a.m, a.groups, a.n, 64,
-                                        a.transposed ? 64 : 128))
+    // weights: rows of the contraction or of the outputs
+    if (!muon_impl::make_map(&L.map_w, const_cast<void*>(a.weight), true, a.transposed ? out : a.n,
+                             a.transposed ? a.m : out, a.groups, pitch, 64, a.transposed ? 64 : 128))
         return cudaErrorInvalidValue;
-    for (int b = 0; L.tma_x && b < 4; ++b)
+    for (int b = 0; b < 4; ++b)
         if (!map_tokens(&L.map_x[b], a.x, L.k, a.tokens, a.ldx * 2, 128 >> b)) return cudaErrorInvalidValue;
-    const bool copy = !L.tma_w || !L.tma_x;
-    return launch_pdl_cluster(pick(a.transposed, copy), dim3(2 * std::min(sm_count / 2, kMaxPairs)),
-                              dim3(copy ? Roles<true>::kThreads : Roles<false>::kThreads), Cfg::SMEM_BYTES, s, 2u, L);
+    return launch_pdl_cluster(pick(a.transposed), dim3(2 * std::min(sm_count / 2, kMaxPairs)), dim3(kThreads),
+                              Cfg::SMEM_BYTES, s, 2u, L);
+}
+
+long long aligned_pitch(long long cols) { return muon_impl::round_up(cols, 8); }
+// As many units of `size` elements as fit into `room`, of `all`: a multiple of 256 or, where fewer fit, of 8.
+long long chunk_of(long long all, long long size, long long room) {
+    const long long n = room / size;
+    return n >= muon_impl::round_up(all, 8) ? all : n >= 256 ? n / 256 * 256 : n / 8 * 8;
+}
+
+}  // namespace
+
+cudaError_t product_prepare() {
+    for (int i = 0; i < 2; ++i) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(pick(i), cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s) {
+    const int out = a.transposed ? a.n : a.m, k = a.transposed ? a.m : a.n;
+    const bool align_w = a.n % 8 != 0 || (reinterpret_cast<uintptr_t>(a.weight) & 15) != 0;
+    const bool align_x = ((reinterpret_cast<uintptr_t>(a.x) | (uintptr_t)(a.ldx * 2)) & 15) != 0;
+    if (!align_w && !align_x) return launch_aligned(a, out, a.n, sm_count, s);
+    // Room for the aligned rows, in elements: the tokens', then the weights'.
+    char* room = static_cast<char*>(a.aligned);
+    const long long px = aligned_pitch(k), all = kAlignedBytes / 2;
+    const long long pw = aligned_pitch(a.n), each = a.m * pw, wish = align_w ? std::min(a.groups * each, all / 2) : 0;
+    const long long tokens = align_x ? chunk_of(a.tokens, px, all - wish) : a.tokens;
+    const long long used = align_x ? muon_impl::round_up(tokens * px, 128) : 0;
+    char* room_w = room + used * 2;
+    // chunks of experts, or of the outputs of one that is too large
+    long long experts = a.groups, outs = out;
+    if (align_w) {
+        experts = std::min<long long>((all - used) / each, a.groups);
+        if (experts == 0) experts = 1, outs = chunk_of(out, a.transposed ? a.m : pw, all - used);
+    }
+    for (long long g = 0; g < a.groups; g += experts)
+        for (long long o = 0; o < out; o += outs)
+            for (long long t = 0; t < a.tokens; t += tokens) {
+                ProductArgs c = a;
+                const int n_out = (int)std::min(outs, out - o);
+                c.groups = (int)std::min(experts, a.groups - g);
+                c.offsets = a.offsets ? a.offsets + g : nullptr;
+                c.first = (int)t, c.tokens = std::min(tokens, a.tokens - t);
+                c.x = static_cast<const char*>(a.x) + t * a.ldx * 2;
+                c.y = static_cast<char*>(a.y) + (t * a.ldy + o) * 2;
+                c.weight = static_cast<const char*>(a.weight) + (g * a.m * a.n + (a.transposed ? o : o * a.n)) * 2;
+                long long pitch = a.n;
+                AlignArgs r{};
+                r.a = c;
+                r.job[0].cols = r.job[1].cols = 1;
+                if (align_w) {
+                    pitch = aligned_pitch(a.transposed ? n_out : a.n);
+                    if (t == 0) {
+                        Job& j = r.job[0];
+                        j.src = static_cast<const char*>(c.weight), j.dst = room_w, j.pitch = a.n * 2ll;
+                        j.dst_pitch = (uint32_t)(pitch * 2), j.cols = a.transposed ? n_out : a.n;
+                        j.per_expert = a.transposed ? a.m : n_out, j.rows = c.groups * j.per_expert;
+                    }
+                    c.weight = room_w;
+                }
+                if (align_x && (tokens < a.tokens || (g == 0 && o == 0))) {
+                    Job& j = r.job[1];
+                    j.src = static_cast<const char*>(c.x), j.dst = room, j.pitch = a.ldx * 2, j.dst_pitch = (uint32_t)(px * 2);
+                    j.rows = (uint32_t)c.tokens, j.cols = k;
+                }
+                if (align_x) c.x = room, c.ldx = px;
+                // an expert's weights are wanted by any of its tokens, not by this chunk's alone
+                r.a.first = 0, r.a.tokens = a.tokens;
+                long long units = 0;
+                for (const Job& j : r.job) units = std::max(units, j.rows * ((j.cols + 511ll) / 512));
+                if (units > 0) {
+                    const long long blocks = std::min<long long>((units + 7) / 8, 24ll * sm_count);
+                    const cudaError_t e = launch_pdl(k_align_rows, dim3((unsigned)blocks), dim3(kAlignThreads), 0, s, r);
+                    if (e != cudaSuccess) return e;
+                }
+                c.m = a.transposed ? a.m : n_out, c.n = a.transposed ? n_out : a.n;
+                const cudaError_t e = launch_aligned(c, n_out, pitch, sm_count, s);
+                if (e != cudaSuccess) return e;
+            }
+    return cudaSuccess;
 }
 
 }  // namespace muon

@@ -188,6 +188,21 @@ def test_weights_beyond_2_31_values(plan, dgrad):  # noqa: F811
     check(plan, bf16((40, m if dgrad else n), 19, 0.1), w, [0, 0, 10] + [10] * 14 + [40], dgrad)
 
 
+@pytest.mark.parametrize("dgrad", [False, True])
+@pytest.mark.parametrize("tokens,m,n,groups", [(36000, 521, 4001, 0), (40, 16001, 8193, 0), (16100, 8193, 4097, 0),
+                                               (700, 2501, 3001, 24), (36000, 264, 4000, 0)])
+def test_rows_that_are_not_aligned_in_chunks(plan, tokens, m, n, groups, dgrad):  # noqa: F811
+    """Operands that do not fit the room for aligned rows at once: chunks of tokens, of experts and of outputs."""
+    rng = np.random.default_rng(7)
+    x = bf16((tokens, m if dgrad else n), 28, pad=1)      # an odd pitch whatever the width
+    w = bf16((groups, m, n) if groups else (m, n), 29, 0.1)
+    edges = None
+    if groups:
+        edges = [3] + (3 + np.sort(rng.integers(0, tokens - 9, groups - 1))).tolist() + [tokens - 4]
+        edges[5] = edges[6]                                # an expert without tokens
+    check(plan, x, w, edges, dgrad)
+
+
 def test_no_tokens(plan):  # noqa: F811
     import torch
     x, out = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), torch.empty((0, 32), dtype=torch.bfloat16, device="cuda")
