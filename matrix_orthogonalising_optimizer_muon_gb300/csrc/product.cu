@@ -64,9 +64,16 @@ struct Divisor {
         while ((1ull << s) < d) ++s;
         m = (uint32_t)(((((1ull << s) - d) << 32) / d) + 1);
     }
-    __device__ __forceinline__ int div(int n) const {
-        return (int)(((unsigned long long)(uint32_t)n + __umulhi((uint32_t)n, m)) >> s);
+    __host__ __device__ __forceinline__ int div(int n) const {
+        return (int)(((unsigned long long)(uint32_t)n + ((unsigned long long)(uint32_t)n * m >> 32)) >> s);
     }
+};
+
+// What every thread knows of the launch's plan.
+struct Outline {
+    int cap, units, turns, stretches;   // greatest height of a tile, tiles, whole turns, stretches of the last
+    int span, least;                    // steps of the last turn's tiles; of a part, the least
+    int stride, bins;                   // experts per bin of Plan::tiles
 };
 
 struct ProductLaunch {
@@ -74,8 +81,11 @@ struct ProductLaunch {
     ProductArgs a;
     int out, k, steps, tiles_m;    // outputs, contraction, its steps, tiles along the outputs
     int wide;                      // rows of y are aligned to four elements
-    Divisor by_tiles;              // by tiles_m
-    int tiles[3];                  // one weight: token tiles when they are at most 256, 128, 64 tokens high
+    int pairs;                     // CTA pairs
+    Divisor by_tiles, by_band, by_pairs, by_steps;   // by tiles_m, kBand tiles_m, pairs, steps
+    // one weight: the plan
+    Outline outline;
+    int count, height, start[kMaxPairs + 1];
 };
 
 // The launch's plan in shared memory.  Where there is more than one turn, experts are placed by decreasing height
@@ -86,16 +96,9 @@ struct Plan {
     uint16_t height[kBins], order[kBins];     // of each expert; the expert at each place
     int start[kMaxPairs + 4];   // begins of the pairs' stretches, in steps from the first tile of the last turn
     int next[12];                // places of the heights while they are dealt out
-    int sums[4];                 // token tiles when they are at most 256, 128, 64 tokens high
-    int pairs, pad[3];           // stretches
+    int sums[8];                 // token tiles when they are at most 256, 128, 64 tokens high
 };
 static_assert(sizeof(Plan) == Cfg::ITEM_OFFSET - Cfg::PLAN_OFFSET, "plan's place");
-
-// What every thread knows of the plan.
-struct Outline {
-    int cap, units, turns, stretches;   // greatest height of a tile, tiles, whole turns, stretches
-    int stride, bins;                   // experts per bin of Plan::tiles
-};
 
 struct __align__(16) Item {
     int m0, t0, end, group;    // first output, first token, end of the expert's tokens
@@ -111,10 +114,14 @@ __device__ __forceinline__ void expert_range(const ProductArgs& a, int g, int* b
 
 // An expert's token tiles: as few as the greatest height allows, of equal height in steps of 32 (the last
 // may be lower).
-__device__ __forceinline__ void cut_range(int tokens, int cap, int* count, int* height) {
+__host__ __device__ __forceinline__ void cut_range(int tokens, int cap, int* count, int* height) {
     const int n = (int)((uint32_t)(tokens + cap - 1) >> (cap == 256 ? 8 : cap == 128 ? 7 : 6));
     // 32 times the quotient rounded down, then up to what holds all tokens: at most twice, for the division's error
-    int h = (int)((float)tokens / (float)max(n, 1) * 0.03125f) << 5;
+#ifdef __CUDA_ARCH__
+    int h = (int)(__fdividef((float)tokens, (float)max(n, 1)) * 0.03125f) << 5;
+#else
+    int h = tokens / (n > 0 ? n : 1) / 32 * 32;
+#endif
     if ((long long)h * n < tokens) h += 32;
     if ((long long)h * n < tokens) h += 32;
     *count = n, *height = h;
@@ -160,7 +167,7 @@ __device__ __forceinline__ Item decode_unit(const ProductLaunch& L, const Plan& 
     uint32_t r = u - before * L.tiles_m;
     int band = 0;
     if (count > kBand) {
-        band = (int)(r / (uint32_t)(kBand * L.tiles_m));
+        band = L.by_band.div((int)r);
         r -= band * kBand * L.tiles_m;
     }
     const uint32_t wide = min(kBand, count - band * kBand), m = r / wide;
@@ -199,62 +206,88 @@ __device__ __forceinline__ void order_experts(Plan& p, int groups, int lane) {
     }
 }
 
-// Begins of the stretches of the last turn's `rest` tiles, one warp: parts of a tile have at least `edge` steps.
-__device__ __forceinline__ void cut_last_turn(const ProductLaunch& L, Plan& p, int stretches, int span, int least,
-                                              int lane) {
-    const int edge = max(min(least, L.steps / 2), 1);
-    for (int i = lane; i <= stretches; i += 32) {
-        int at = i == stretches ? span : (int)((long long)span * i / stretches);
-        const int k = at % L.steps;
-        if (k < edge)
-            at -= k;
-        else if (k > L.steps - edge)
-            at += L.steps - k;
-        p.start[i] = at;
+// How tiles of at most 32 `high` tokens would be dealt out, and the time that takes, in 32 cycles.  A step takes as
+// long as its MMAs, and 256 cycles for the weight's 16 KB besides.  The tiles of the last, incomplete turn are cut
+// along the contraction into stretches of equal length, one per pair, where that saves more than joining the parts
+// takes: about 6 steps' time and, to write and read them, 34 more for 256 tokens.
+struct Dealt {
+    int units, whole, rest, time;
+    bool cut;
+    __host__ __device__ __forceinline__ Dealt(const ProductLaunch& L, int tiles, int high) {
+        const int step = 8 + high, turn = L.steps * step;   // steps <= 2^14
+        units = tiles * L.tiles_m;
+        whole = L.by_pairs.div(units);
+        rest = units - whole * L.pairs;
+        const int joined = L.by_pairs.div(rest * turn) + (6 + 34 * high / 8) * step;
+        cut = rest > 0 && joined < turn;
+        // beyond 2^31 any height does
+        const long long t = (long long)whole * turn + (cut ? joined : rest > 0 ? turn : 0);
+        time = t < 0x7fffffff ? (int)t : 0x7fffffff;
     }
+};
+
+// n0, n1, n2: token tiles when they are at most 256, 128, 64 tokens high.  The greatest height is the fastest of these.
+__host__ __device__ __forceinline__ Outline outline_of(const ProductLaunch& L, int n0, int n1, int n2) {
+    Outline o;
+    const int groups = L.a.groups;
+    o.stride = (groups + kBins - 1) / kBins;
+    o.bins = (groups + o.stride - 1) / o.stride;
+    Dealt d(L, n2, 2);
+    o.cap = 64;
+    if (n1 < n2) {   // some expert has more than 64 tokens
+        const Dealt e(L, n1, 4);
+        if (e.time <= d.time) d = e, o.cap = 128;
+    }
+    if (n0 < n1) {
+        const Dealt e(L, n0, 8);
+        if (e.time <= d.time) d = e, o.cap = 256;
+    }
+    o.units = d.units;
+    o.turns = d.whole + (d.rest > 0 && !d.cut);
+    o.least = 2 + (o.cap >> 5);
+    o.span = d.cut ? d.rest * L.steps : 0;
+    o.stretches = d.cut ? (o.span >= o.least * L.pairs ? L.pairs : o.span >= o.least ? o.span / o.least : 1) : 0;
+    return o;
+}
+
+// Begin of stretch i, in steps from the first tile of the last turn: parts of a tile have at least `edge` steps.
+__host__ __device__ __forceinline__ int stretch_start(const ProductLaunch& L, const Outline& o, int i) {
+    if (i == o.stretches) return o.span;
+    int at = o.stretches == L.pairs ? L.by_pairs.div(o.span * i) : o.span * i / o.stretches;   // below 2^28
+    const int edge = o.least < L.steps / 2 ? o.least : L.steps > 3 ? L.steps / 2 : 1;
+    const int k = at - L.by_steps.div(at) * L.steps;
+    if (k < edge)
+        at -= k;
+    else if (k > L.steps - edge)
+        at += L.steps - k;
+    return at;
 }
 
 // Fills the plan: all threads of the CTA.
 __device__ __forceinline__ Outline make_plan(const ProductLaunch& L, Plan& p, int threads) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pairs = gridDim.x >> 1, groups = L.a.groups;
-    Outline o;
-    o.stride = (groups + kBins - 1) / kBins;
-    o.bins = (groups + o.stride - 1) / o.stride;
-    int n0 = L.tiles[0], n1 = L.tiles[1], n2 = L.tiles[2];
-    if (groups > 1 || L.a.offsets) {
-        if (tid < 4) p.sums[tid] = 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, groups = L.a.groups;
+    if (!L.a.offsets) {   // one weight: the host knows it
+        if (tid <= L.outline.stretches) p.start[tid] = L.start[tid];
+        if (tid == 0) p.begin[0] = 0, p.end[0] = (int)L.a.tokens, p.count[0] = L.count, p.height[0] = (uint16_t)L.height;
         __syncthreads();
-        n0 = n1 = n2 = 0;
-        for (int g = tid; g < groups; g += threads) {
-            int b, e;
-            expert_range(L.a, g, &b, &e);
-            if (o.stride == 1) p.begin[g] = b, p.end[g] = e;
-            n0 += (e - b + 255) >> 8, n1 += (e - b + 127) >> 7, n2 += (e - b + 63) >> 6;
-        }
-        n0 = __reduce_add_sync(0xffffffffu, n0), n1 = __reduce_add_sync(0xffffffffu, n1);
-        n2 = __reduce_add_sync(0xffffffffu, n2);
-        if (lane == 0 && n2 > 0) atomicAdd(p.sums, n0), atomicAdd(p.sums + 1, n1), atomicAdd(p.sums + 2, n2);
-        __syncthreads();
-        n0 = p.sums[0], n1 = p.sums[1], n2 = p.sums[2];
-    } else if (tid == 0) {
-        p.begin[0] = 0, p.end[0] = (int)L.a.tokens;
+        return L.outline;
     }
-    // the greatest height is 256 tokens if such tiles fill the GPU once, else 128 or 64
-    int n = n0;
-    o.cap = 256;
-    if (n0 == n2 || (n0 * L.tiles_m < pairs && n1 * L.tiles_m < pairs))
-        o.cap = 64, n = n2;
-    else if (n0 == n1 || n0 * L.tiles_m < pairs)
-        o.cap = 128, n = n1;
-    o.units = n * L.tiles_m;
-    // The tiles of the last, incomplete turn are cut along the contraction into stretches of equal length, one
-    // per pair, where that saves more than joining the parts takes: about 6 steps' time and, to write and read
-    // them, 34 more for 256 tokens.
-    const int whole = o.units / pairs, rest = o.units - whole * pairs, high = o.cap >> 5, least = 2 + high;
-    const bool cut = rest > 0 && L.steps * (pairs - rest) > (6 + 34 * high / 8) * pairs;   // steps <= 2^14
-    o.turns = whole + (rest > 0 && !cut);
-    o.stretches = cut ? max(min(pairs, rest * L.steps / least), 1) : 0;
-    if (o.stride == 1) {
+    const bool few = groups <= kBins;
+    if (tid < 4) p.sums[tid] = 0;
+    __syncthreads();
+    int n0 = 0, n1 = 0, n2 = 0;
+    for (int g = tid; g < groups; g += threads) {
+        int b, e;
+        expert_range(L.a, g, &b, &e);
+        if (few) p.begin[g] = b, p.end[g] = e;
+        n0 += (e - b + 255) >> 8, n1 += (e - b + 127) >> 7, n2 += (e - b + 63) >> 6;
+    }
+    n0 = __reduce_add_sync(0xffffffffu, n0), n1 = __reduce_add_sync(0xffffffffu, n1);
+    n2 = __reduce_add_sync(0xffffffffu, n2);
+    if (lane == 0 && n2 > 0) atomicAdd(p.sums, n0), atomicAdd(p.sums + 1, n1), atomicAdd(p.sums + 2, n2);
+    __syncthreads();
+    const Outline o = outline_of(L, p.sums[0], p.sums[1], p.sums[2]);
+    if (few) {
         for (int g = tid; g < groups; g += threads) {
             int count, height;
             cut_range(p.end[g] - p.begin[g], o.cap, &count, &height);
@@ -272,17 +305,18 @@ __device__ __forceinline__ Outline make_plan(const ProductLaunch& L, Plan& p, in
             p.tiles[b] = tiles;
         }
     }
-    if (cut && warp == 1) cut_last_turn(L, p, o.stretches, rest * L.steps, least, lane);
+    if (warp == 1)
+        for (int i = lane; o.stretches && i <= o.stretches; i += 32) p.start[i] = stretch_start(L, o, i);
     __syncthreads();
     if (o.bins > 1) {
         if (warp == 0) {
-            if (o.stride == 1 && o.units > pairs) {
+            if (few && o.units > L.pairs) {
                 order_experts(p, groups, lane);
                 __syncwarp();
             }
             int tiles = 0;
             for (int b0 = 0; b0 < o.bins; b0 += 32) {   // tiles of the places before
-                const int b = b0 + lane, t = b >= o.bins ? 0 : o.stride == 1 ? p.count[p.order[b]] : p.tiles[b];
+                const int b = b0 + lane, t = b >= o.bins ? 0 : few ? p.count[p.order[b]] : p.tiles[b];
                 int sum = t;
 #pragma unroll
                 for (int d = 1; d < 32; d *= 2) {
@@ -303,11 +337,11 @@ __device__ __forceinline__ Outline make_plan(const ProductLaunch& L, Plan& p, in
 struct Items {
     int pair, pairs, turns, count;
     __device__ __forceinline__ Items(const ProductLaunch& L, const Plan& p, const Outline& o)
-        : pair(blockIdx.x >> 1), pairs(gridDim.x >> 1), turns(o.turns) {
+        : pair(blockIdx.x >> 1), pairs(L.pairs), turns(o.turns) {
         if (turns > 0 && unit_of(turns - 1) >= o.units) --turns;
         count = turns;
         if (pair < o.stretches && p.start[pair + 1] > p.start[pair])
-            count += (p.start[pair + 1] - 1) / L.steps - p.start[pair] / L.steps + 1;
+            count += L.by_steps.div(p.start[pair + 1] - 1) - L.by_steps.div(p.start[pair]) + 1;
     }
     __device__ __forceinline__ int unit_of(int turn) const {
         return turn * pairs + (turn & 1 ? pairs - 1 - pair : pair);
@@ -315,7 +349,7 @@ struct Items {
     __device__ __forceinline__ Item decode(const ProductLaunch& L, const Plan& p, const Outline& o, int turn) const {
         if (turn < turns) return decode_unit(L, p, o, unit_of(turn));
         const int from = p.start[pair], to = p.start[pair + 1];
-        const int u = from / L.steps + turn - turns, begin = u * L.steps, end = begin + L.steps;
+        const int u = L.by_steps.div(from) + turn - turns, begin = u * L.steps, end = begin + L.steps;
         Item it = decode_unit(L, p, o, o.turns * pairs + u);
         it.k0 = max(from - begin, 0), it.k1 = min(to - begin, L.steps);
         if (it.k0 > 0 || it.k1 < L.steps) {
@@ -727,9 +761,15 @@ cudaError_t launch_aligned(const ProductArgs& a, int out, long long pitch, int s
     L.k = a.transposed ? a.m : a.n;
     L.steps = (L.k + kStepK - 1) / kStepK;
     L.tiles_m = (L.out + 255) / 256;
-    L.by_tiles.set(L.tiles_m);
-    for (int i = 0; i < 3; ++i) L.tiles[i] = (int)((a.tokens + (256 >> i) - 1) / (256 >> i));
     if ((a.tokens / 64 + a.groups) * L.tiles_m >= (1ll << 31)) return cudaErrorInvalidValue;
+    L.pairs = std::min(sm_count / 2, kMaxPairs);
+    L.by_tiles.set(L.tiles_m), L.by_band.set(kBand * L.tiles_m), L.by_pairs.set(L.pairs), L.by_steps.set(L.steps);
+    if (!a.offsets) {
+        const int t = (int)a.tokens;
+        L.outline = outline_of(L, (int)((t + 255ll) >> 8), (int)((t + 127ll) >> 7), (int)((t + 63ll) >> 6));
+        cut_range(t, L.outline.cap, &L.count, &L.height);
+        for (int i = 0; L.outline.stretches && i <= L.outline.stretches; ++i) L.start[i] = stretch_start(L, L.outline, i);
+    }
     L.wide = L.out % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)(a.ldy * 2)) & 7) == 0;
     // weights: rows of the contraction or of the outputs
     if (!muon_impl::make_map(&L.map_w, const_cast<void*>(a.weight), true, a.transposed ? out : a.n,
@@ -737,7 +777,7 @@ cudaError_t launch_aligned(const ProductArgs& a, int out, long long pitch, int s
         return cudaErrorInvalidValue;
     for (int b = 0; b < 4; ++b)
         if (!map_tokens(&L.map_x[b], a.x, L.k, a.tokens, a.ldx * 2, 128 >> b)) return cudaErrorInvalidValue;
-    return launch_pdl_cluster(pick(a.transposed), dim3(2 * std::min(sm_count / 2, kMaxPairs)), dim3(kThreads),
+    return launch_pdl_cluster(pick(a.transposed), dim3(2 * L.pairs), dim3(kThreads),
                               Cfg::SMEM_BYTES, s, 2u, L);
 }
 
