@@ -613,8 +613,9 @@ muon_status muon_wgrad(muon_grad_plan p, const void* dy, int64_t lddy, const muo
  *              multiplied with its expert's weight.  Rows of the output outside every expert are
  *              left as they were, whatever the input holds there.
  * Products and sums are fp32 and rounded to bf16 once.  The sums' order depends on the sizes and
- * the offsets alone: the same inputs give the same bits.  1 <= m, n <= 2^20, 0 <= tokens < 2^31,
- * groups <= 4096.
+ * the offsets alone: the same inputs give the same bits.  1 <= m, n <= 2^20, 0 <= tokens <=
+ * 2^31 - 4096, groups <= 4096.  Where rows of x (dy) or of the weight are not aligned to 16 bytes,
+ * they are first copied into the plan's workspace, which costs their bytes twice more.
  */
 muon_status muon_product(muon_grad_plan p, const void* x, int64_t ldx, const void* weight, int64_t tokens, int64_t m,
                          int64_t n, const int32_t* offsets, int32_t groups, void* y, int64_t ldy, void* stream);

@@ -166,6 +166,7 @@ muon_status product(muon_grad_plan_s* p, const void* x, int64_t ldx, const void*
     MUON_CALL(begin(&cx, tokens, transposed ? m : n, MUON_BF16, kMaxDim));
     MUON_CALL(begin(&cy, tokens, transposed ? n : m, MUON_BF16, kMaxDim));
     if (!p || groups < 0 || groups > kMostExperts || (groups > 0) != (offsets != nullptr)) return MUON_ERR_INVALID_ARG;
+    if (tokens > (1ll << 31) - 4096) return MUON_ERR_UNSUPPORTED;   // rows of the last tile are counted in 32 bits
     cx.mat(&mat, x, ldx, false, tokens == 0);
     if (!cx.ok) return MUON_ERR_INVALID_ARG;
     cy.ops.add(x, tokens, cx.cols * 2, ldx * 2, false);

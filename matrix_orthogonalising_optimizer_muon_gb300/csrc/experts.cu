@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const MoveArgs a) {
 }
 
 // Choices whose rows are on their way together: with one, the loads do not cover HBM's latency (backward, 8192 x 4
-// rows of 3584 in bf16: 98 us, 84 with four).
+// rows of 3584 in bf16: 101 us, 81 with four, 96 % of the copy rate).
 template <bool BF16>
 constexpr int kTogether = BF16 ? 4 : 2;
 
@@ -315,15 +315,16 @@ cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s) {
     // whose ranking is bound by instruction issue, unless reading all CTAs' counts takes longer: 65536 ids of 256
     // 12.8 us with eight CTAs and 14.3 with sixteen, 131072 of 128 16.1 and 13.3, of 4096 51 and 84.
     const int lc = a.n <= 2048 ? 0 : a.n >= 100000 && a.experts <= 1024 ? 4 : 3;
-    if (lc == 4) {
-        const cudaError_t e = cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
     const size_t bytes = (size_t)((1 << lw) + 3) * a.experts * sizeof(int);
-    // per call: an attribute of the current device
-    const cudaError_t set =
-        cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (set != cudaSuccess) return set;
+    // Per call, as an attribute of the current device; the same for every call, as another thread may be between its
+    // own setting and its launch.
+    constexpr int kMostBytes = (8 + 3) * 4096 * (int)sizeof(int);
+    static_assert(kMostBytes >= (32 + 3) * 1024 * (int)sizeof(int) && kMostBytes >= (16 + 3) * 2048 * (int)sizeof(int),
+                  "the most of any number of experts");
+    cudaError_t e = cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
+    if (e == cudaSuccess && lc == 4)
+        e = cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     return launch_pdl_cluster(k_expert_order, dim3(1 << lc), dim3(kOrderThreads), bytes, s, 1u << lc, a, lw, lc);
 }
 

@@ -236,8 +236,9 @@ cudaError_t launch_grad_norm(const GradList& l, const GradNormArgs& a, cudaStrea
     for (int from = 0; from == 0 || from < l.n; from += kTableMost) {
         const int to = std::min(l.n, from + kTableMost);
         const bool last = to == l.n;
-        const cudaError_t e = to - from <= kTableFew ? norm_of<kTableFew>(l, from, to, a, last, s)
-                                                     : norm_of<kTableMost>(l, from, to, a, last, s);
+        const cudaError_t e = to - from <= kTableFew    ? norm_of<kTableFew>(l, from, to, a, last, s)
+                              : to - from <= kTableSome ? norm_of<kTableSome>(l, from, to, a, last, s)
+                                                        : norm_of<kTableMost>(l, from, to, a, last, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -246,8 +247,9 @@ cudaError_t launch_grad_norm(const GradList& l, const GradNormArgs& a, cudaStrea
 cudaError_t launch_grad_clip(const GradList& l, const float* norm, float max_norm, int sm_count, cudaStream_t s) {
     for (int from = 0; from < l.n; from += kTableMost) {
         const int to = std::min(l.n, from + kTableMost);
-        const cudaError_t e = to - from <= kTableFew ? clip_of<kTableFew>(l, from, to, norm, max_norm, sm_count, s)
-                                                     : clip_of<kTableMost>(l, from, to, norm, max_norm, sm_count, s);
+        const cudaError_t e = to - from <= kTableFew    ? clip_of<kTableFew>(l, from, to, norm, max_norm, sm_count, s)
+                              : to - from <= kTableSome ? clip_of<kTableSome>(l, from, to, norm, max_norm, sm_count, s)
+                                                        : clip_of<kTableMost>(l, from, to, norm, max_norm, sm_count, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

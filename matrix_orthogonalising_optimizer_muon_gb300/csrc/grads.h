@@ -22,7 +22,7 @@ struct GradEntry {
 };
 
 // Parameters of one launch: at most 32764 bytes, the few for short lists.
-constexpr int kTableFew = 30, kTableMost = 960;
+constexpr int kTableFew = 30, kTableSome = 220, kTableMost = 960;
 constexpr int kMostBlocks = 640;
 template <int N>
 struct GradTable {

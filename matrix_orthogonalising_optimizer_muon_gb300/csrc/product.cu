@@ -14,7 +14,7 @@
 // 16 KB of tokens per CTA, in a ring of six.
 //
 // How the work is dealt out (every CTA derives the same plan from the offsets): tiles in the order experts,
-// bands of kBand token tiles, outputs, token tiles, one per CTA pair and turn, so that the tiles in flight share
+// bands of token tiles, outputs, token tiles, one per CTA pair and turn, so that the tiles in flight share
 // operands in L2.  (A contiguous run of tiles per pair balances ragged experts better, but each operand is then
 // read again a whole tile later, when L2 has lost it: 102 us against 64 for the 32 experts below.)  The last,
 // incomplete turn may be cut along the contraction; its partial sums meet in the workspace, and the part that
@@ -36,7 +36,6 @@ constexpr int kStepK = 64;
 constexpr int kRing = 6;
 constexpr int kEpiFirst = 2, kEpi = 8;             // epilogue warps
 constexpr int kThreads = 32 * (kEpiFirst + kEpi);
-constexpr int kBand = 8;
 constexpr int kBins = 512;                         // experts are searched in at most this many bins
 constexpr int kItems = 96;                         // items decoded at the start
 
@@ -81,8 +80,8 @@ struct ProductLaunch {
     ProductArgs a;
     int out, k, steps, tiles_m;    // outputs, contraction, its steps, tiles along the outputs
     int wide;                      // rows of y are aligned to four elements
-    int pairs;                     // CTA pairs
-    Divisor by_tiles, by_band, by_pairs, by_steps;   // by tiles_m, kBand tiles_m, pairs, steps
+    int pairs, band;               // CTA pairs; token tiles whose outputs are taken before the next ones'
+    Divisor by_tiles, by_band, by_pairs, by_steps;   // by tiles_m, band tiles_m, pairs, steps
     // one weight: the plan
     Outline outline;
     int count, height, start[kMaxPairs + 1];
@@ -166,14 +165,14 @@ __device__ __forceinline__ Item decode_unit(const ProductLaunch& L, const Plan& 
     }
     uint32_t r = u - before * L.tiles_m;
     int band = 0;
-    if (count > kBand) {
+    if (count > L.band) {
         band = L.by_band.div((int)r);
-        r -= band * kBand * L.tiles_m;
+        r -= band * L.band * L.tiles_m;
     }
-    const uint32_t wide = min(kBand, count - band * kBand), m = r / wide;
-    it.m0 = (int)m * 256, it.t0 += (band * kBand + (int)(r - m * wide)) * height;
+    const uint32_t wide = min(L.band, count - band * L.band), m = r / wide;
+    it.m0 = (int)m * 256, it.t0 += (band * L.band + (int)(r - m * wide)) * height;
     it.k0 = 0, it.k1 = L.steps, it.part = 0;
-    it.n = min(height, (it.end - it.t0 + 31) & ~31);
+    it.n = min(height, (it.end - it.t0 + 31) & ~31);   // tokens < 2^31 - 4096
     return it;
 }
 
@@ -763,7 +762,10 @@ cudaError_t launch_aligned(const ProductArgs& a, int out, long long pitch, int s
     L.tiles_m = (L.out + 255) / 256;
     if ((a.tokens / 64 + a.groups) * L.tiles_m >= (1ll << 31)) return cudaErrorInvalidValue;
     L.pairs = std::min(sm_count / 2, kMaxPairs);
-    L.by_tiles.set(L.tiles_m), L.by_band.set(kBand * L.tiles_m), L.by_pairs.set(L.pairs), L.by_steps.set(L.steps);
+    // A wider band reads the weight fewer times, as long as its tokens stay in L2 (16 tiles of 4096 values: 32 MB):
+    // eight experts of 18944 x 3584 1365 us with 16 and 1397 with eight, 8192 x 8192 x 8192 592 and 580.
+    L.band = L.k <= 4096 ? 16 : 8;
+    L.by_tiles.set(L.tiles_m), L.by_band.set(L.band * L.tiles_m), L.by_pairs.set(L.pairs), L.by_steps.set(L.steps);
     if (!a.offsets) {
         const int t = (int)a.tokens;
         L.outline = outline_of(L, (int)((t + 255ll) >> 8), (int)((t + 127ll) >> 7), (int)((t + 63ll) >> 6));

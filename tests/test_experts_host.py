@@ -24,7 +24,7 @@ def handle():
 @pytest.mark.parametrize("name", ["muon_product", "muon_dgrad"])
 @pytest.mark.parametrize("kw,code", [
     (dict(plan=None), BAD), (dict(x=None), BAD), (dict(w=None), BAD), (dict(y=None), BAD), (dict(tokens=-1), BAD),
-    (dict(tokens=1 << 31), UNSUP), (dict(m=0), BAD), (dict(n=0), BAD), (dict(m=(1 << 20) + 1, ld=1 << 21), UNSUP),
+    (dict(tokens=1 << 31), UNSUP), (dict(tokens=(1 << 31) - 4095), UNSUP), (dict(m=0), BAD), (dict(n=0), BAD), (dict(m=(1 << 20) + 1, ld=1 << 21), UNSUP),
     (dict(n=(1 << 20) + 1, ld=1 << 21), UNSUP), (dict(ldx=49), BAD), (dict(ldy=49), BAD), (dict(x=A + 1), BAD),
     (dict(y=C + 1), BAD), (dict(w=B + 1), BAD), (dict(groups=-1), BAD), (dict(groups=4097, offsets=D), BAD),
     (dict(groups=2), BAD), (dict(offsets=D), BAD), (dict(offsets=D + 2, groups=2), BAD), (dict(y=A), BAD),

@@ -179,6 +179,23 @@ def test_one_weight_of_many_turns(plan, dgrad):  # noqa: F811
 
 
 @pytest.mark.parametrize("dgrad", [False, True])
+@pytest.mark.parametrize("groups", [0, 7, 600])
+def test_more_turns_than_are_decoded_at_the_start(plan, groups, dgrad):  # noqa: F811
+    """Short sums and thousands of tiles: one weight, a few experts, and more experts than have a place each."""
+    rng = np.random.default_rng(9)
+    if groups == 600:
+        edges = np.concatenate([[0], np.cumsum(rng.integers(0, 90, groups))]).tolist()
+        m, n = 3600, 16
+    else:
+        edges = [0] + np.sort(rng.integers(0, 100000, max(groups, 1) - 1)).tolist() + [100000]
+        m, n = 6000, 8
+    if dgrad:
+        m, n = n, m
+    w = bf16((groups, m, n) if groups else (m, n), 30)
+    check(plan, bf16((edges[-1], m if dgrad else n), 31), w, edges if groups else None, dgrad)
+
+
+@pytest.mark.parametrize("dgrad", [False, True])
 def test_weights_beyond_2_31_values(plan, dgrad):  # noqa: F811
     import torch
     m, n, groups = 8192, 16384, 17
