@@ -160,8 +160,10 @@ __global__ void __launch_bounds__(kOrderThreads) k_expert_order(const OrderArgs 
 constexpr int kThreads = 256;
 constexpr int kSms = 152;
 using Walk = RowWalk<kThreads>;
-template <bool VEC>
-constexpr int kMode = VEC ? kAligned : kShifted;
+// Rows that are not aligned: bf16 in shifted pieces, fp32 by value, whose loads are whole lines, too, and need no
+// shifts (13384 x 6 rows of 453: 29 us by value, 61 shifted).
+template <bool BF16, bool VEC>
+constexpr int kMode = VEC ? kAligned : BF16 ? kShifted : kByValue;
 
 // A slot as a row of the experts' tensor, or -1.
 __device__ __forceinline__ int slot_row(const MoveArgs& a, uint32_t token, int j) {
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const MoveArgs a) {
     pdl_trigger();
     pdl_wait();
     for (Walk w(a.cols); w.row < a.tokens; w.next()) {
-        Raw<BF16, kMode<VEC>> raw[kUnroll];
+        Raw<BF16, kMode<BF16, VEC>> raw[kUnroll];
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) raw[k].load(row_ptr(a.x, w.row), w.col + k * kSeg, a.cols, lane);
         for (int j = 0; j < a.choices; ++j) {
@@ -184,8 +186,15 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const MoveArgs a) {
             if (s < 0) continue;
 #pragma unroll
             for (int k = 0; k < kUnroll; ++k)
-                if (w.col + k * kSeg < a.cols)
-                    seg_store_words<BF16, kMode<VEC>>(row_ptr(a.y, s), w.col + k * kSeg, a.cols, lane, raw[k].r);
+                if (w.col + k * kSeg < a.cols) {
+                    if constexpr (BF16 || VEC) {
+                        seg_store_words<BF16, kMode<BF16, VEC>>(row_ptr(a.y, s), w.col + k * kSeg, a.cols, lane, raw[k].r);
+                    } else {
+                        float v[8];
+                        raw[k].get(v);
+                        seg_store<BF16, kMode<BF16, VEC>>(row_ptr(a.y, s), w.col + k * kSeg, a.cols, lane, v);
+                    }
+                }
         }
     }
 }
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const MoveArgs a) {
         float acc[kUnroll][8] = {};
         for (int j0 = 0; j0 < a.choices; j0 += kJ) {
             int s[kJ];
-            Raw<BF16, kMode<VEC>> raw[kJ][kUnroll];
+            Raw<BF16, kMode<BF16, VEC>> raw[kJ][kUnroll];
 #pragma unroll
             for (int j = 0; j < kJ; ++j) s[j] = j0 + j < a.choices ? slot_row(a, w.row, j0 + j) : -1;
 #pragma unroll
@@ -230,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const MoveArgs a) {
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
             if (w.col + k * kSeg < a.cols)
-                seg_store<BF16, kMode<VEC>>(row_ptr(a.x, w.row), w.col + k * kSeg, a.cols, lane, acc[k]);
+                seg_store<BF16, kMode<BF16, VEC>>(row_ptr(a.x, w.row), w.col + k * kSeg, a.cols, lane, acc[k]);
     }
 }
 
@@ -255,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_combine_backward(const MoveArgs
                 f[j] = s[j] >= 0 ? a.weights[(uint64_t)t * a.choices + j0 + j] : 0.f;
             }
             for (int c0 = q * kSeg; t < a.tokens && c0 < a.cols; c0 += span * kSeg) {
-                Raw<BF16, kMode<VEC>> xr, yr[kJ];
+                Raw<BF16, kMode<BF16, VEC>> xr, yr[kJ];
                 float x[8];
                 xr.load(row_ptr(a.x, t), c0, a.cols, lane);
                 if (a.dweights) {
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_combine_backward(const MoveArgs
                     if (a.dy.p) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[i] = x[i] * f[j];
-                        seg_store<BF16, kMode<VEC>>(row_ptr(a.dy, s[j]), c0, a.cols, lane, v);
+                        seg_store<BF16, kMode<BF16, VEC>>(row_ptr(a.dy, s[j]), c0, a.cols, lane, v);
                     }
                 }
             }

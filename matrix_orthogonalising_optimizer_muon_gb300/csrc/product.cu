@@ -707,44 +707,61 @@ bool map_tokens(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows
 
 // ------------------------------------------------------------------ rows that TMA cannot read
 // TMA takes rows whose addresses are multiples of 16 bytes.  Others are first copied into aligned rows in the
-// workspace, at HBM's rate, chunk by chunk where they do not fit: 8192 x 3584 x 3585 takes 174 us, its 16-byte
+// workspace, at HBM's rate, chunk by chunk where they do not fit: 8192 x 3584 x 3585 takes 137 us, its 16-byte
 // aligned neighbour 108 (396 when the
 // product's own warps copied each operand of each tile through shifts, bound by the latency of that way).
 struct Job {
     const char* src;
     char* dst;
-    long long pitch;      // of src, bytes
-    uint32_t dst_pitch;   // a multiple of 16
-    uint32_t rows;
-    int cols;
-    uint32_t per_expert;  // rows of each expert, of which those without tokens are left out; 0: all rows
+    long long pitch;       // of src, bytes
+    uint32_t dst_pitch;    // a multiple of 128
+    int bytes;             // of a row
+    int pieces;            // 16 bytes each, of all rows
+    Divisor by_row;        // pieces of a row
+    Divisor by_expert;     // rows of each expert, of which those without tokens are left out; d 0: all rows
 };
 struct AlignArgs {
     Job job[2];
     ProductArgs a;
 };
 
-constexpr int kAlignThreads = 256;
+// A lane makes 16 bytes from the two aligned pieces that hold them, of which each holds a value of the row.
+constexpr int kAlignThreads = 256, kAlignUnroll = 4;
 __global__ void __launch_bounds__(kAlignThreads) k_align_rows(const AlignArgs args) {
-    const int lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
     for (int i = 0; i < 2; ++i) {
         const Job& j = args.job[i];
-        for (RowWalk<kAlignThreads> w(j.cols); w.row < j.rows; w.next()) {
-            if (j.per_expert && args.a.offsets) {
-                int begin, end;
-                expert_range(args.a, (int)(w.row / j.per_expert), &begin, &end);
-                if (begin == end) continue;
+        constexpr int kBlock = kAlignThreads * kAlignUnroll;
+        for (long long p0 = (long long)blockIdx.x * kBlock + threadIdx.x; p0 < j.pieces; p0 += (long long)gridDim.x * kBlock) {
+            uint32_t v[kAlignUnroll][8];
+            int d[kAlignUnroll];
+            char* to[kAlignUnroll];
+#pragma unroll
+            for (int k = 0; k < kAlignUnroll; ++k) {
+                const long long p = p0 + k * kAlignThreads;
+                const int row = p < j.pieces ? j.by_row.div((int)p) : 0, at = ((int)p - row * (int)j.by_row.d) * 16;
+                bool live = p < j.pieces;
+                if (live && j.by_expert.d) {
+                    int begin, end;
+                    expert_range(args.a, j.by_expert.div(row), &begin, &end);
+                    live = begin < end;
+                }
+                const char* line = j.src + row * j.pitch;
+                d[k] = (int)(reinterpret_cast<uintptr_t>(line) & 15);
+                const uint4* q = reinterpret_cast<const uint4*>(line + at - d[k]);
+                uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                if (live) x = q[0];
+                if (live && d[k] && reinterpret_cast<const char*>(q + 1) < line + j.bytes) y = q[1];
+                v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+                v[k][4] = y.x, v[k][5] = y.y, v[k][6] = y.z, v[k][7] = y.w;
+                to[k] = live ? j.dst + (uint64_t)row * j.dst_pitch + at : nullptr;
             }
-            const char* from = j.src + w.row * j.pitch;
-            char* to = j.dst + (uint64_t)w.row * j.dst_pitch;
-            Raw<true, kShifted> raw[kUnroll];
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k) raw[k].load(from, w.col + k * kSeg, j.cols, lane);
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
-                if (w.col + k * kSeg < j.cols) seg_store_words<true, kAligned>(to, w.col + k * kSeg, j.cols, lane, raw[k].r);
+            for (int k = 0; k < kAlignUnroll; ++k) {
+                words_down<true>(v[k], d[k]);
+                if (to[k]) *reinterpret_cast<uint4*>(to[k]) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
+            }
         }
     }
 }
@@ -783,12 +800,21 @@ cudaError_t launch_aligned(const ProductArgs& a, int out, long long pitch, int s
                               Cfg::SMEM_BYTES, s, 2u, L);
 }
 
-long long aligned_pitch(long long cols) { return muon_impl::round_up(cols, 8); }
-// As many units of `size` elements as fit into `room`, of `all`: a multiple of 256 or, where fewer fit, of 8.
+// Rows begin at multiples of 128 bytes, so that a box's rows are whole lines of L2.
+long long aligned_pitch(long long cols) { return muon_impl::round_up(cols, 64); }
+// As many units of `size` elements as fit into `room`, of `all`: a multiple of 256 or, where fewer fit, of 64 (that
+// many always do: sizes are at most 2^20, room at least 2^26).
 long long chunk_of(long long all, long long size, long long room) {
     const long long n = room / size;
-    return n >= muon_impl::round_up(all, 8) ? all : n >= 256 ? n / 256 * 256 : n / 8 * 8;
+    return n >= muon_impl::round_up(all, 64) ? all : n >= 256 ? n / 256 * 256 : n / 64 * 64;
 }
+void set_job(Job* j, const void* src, long long pitch, void* dst, long long dst_pitch, long long rows, int cols) {
+    j->src = static_cast<const char*>(src), j->dst = static_cast<char*>(dst), j->pitch = pitch * 2;
+    j->dst_pitch = (uint32_t)(dst_pitch * 2), j->bytes = cols * 2;
+    j->by_row.set((uint32_t)((cols + 7) / 8));
+    j->pieces = (int)(rows * ((cols + 7) / 8));   // within kAlignedBytes
+}
+static_assert(kAlignedBytes / 2 / 2 >= 1ll << 26, "room for the least chunks");
 
 }  // namespace
 
@@ -833,29 +859,21 @@ cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s) {
                 long long pitch = a.n;
                 AlignArgs r{};
                 r.a = c;
-                r.job[0].cols = r.job[1].cols = 1;
                 if (align_w) {
-                    pitch = aligned_pitch(a.transposed ? n_out : a.n);
+                    const int cols = a.transposed ? n_out : a.n, rows = a.transposed ? a.m : n_out;
+                    pitch = aligned_pitch(cols);
                     if (t == 0) {
-                        Job& j = r.job[0];
-                        j.src = static_cast<const char*>(c.weight), j.dst = room_w, j.pitch = a.n * 2ll;
-                        j.dst_pitch = (uint32_t)(pitch * 2), j.cols = a.transposed ? n_out : a.n;
-                        j.per_expert = a.transposed ? a.m : n_out, j.rows = c.groups * j.per_expert;
+                        set_job(&r.job[0], c.weight, a.n, room_w, pitch, (long long)c.groups * rows, cols);
+                        if (a.offsets) r.job[0].by_expert.set(rows);
                     }
                     c.weight = room_w;
                 }
-                if (align_x && (tokens < a.tokens || (g == 0 && o == 0))) {
-                    Job& j = r.job[1];
-                    j.src = static_cast<const char*>(c.x), j.dst = room, j.pitch = a.ldx * 2, j.dst_pitch = (uint32_t)(px * 2);
-                    j.rows = (uint32_t)c.tokens, j.cols = k;
-                }
+                if (align_x && (tokens < a.tokens || (g == 0 && o == 0))) set_job(&r.job[1], c.x, a.ldx, room, px, c.tokens, k);
                 if (align_x) c.x = room, c.ldx = px;
                 // an expert's weights are wanted by any of its tokens, not by this chunk's alone
                 r.a.first = 0, r.a.tokens = a.tokens;
-                long long units = 0;
-                for (const Job& j : r.job) units = std::max(units, j.rows * ((j.cols + 511ll) / 512));
-                if (units > 0) {
-                    const long long blocks = std::min<long long>((units + 7) / 8, 24ll * sm_count);
+                if (const long long pieces = std::max(r.job[0].pieces, r.job[1].pieces)) {
+                    const long long blocks = std::min<long long>((pieces + 1023) / 1024, 24ll * sm_count);
                     const cudaError_t e = launch_pdl(k_align_rows, dim3((unsigned)blocks), dim3(kAlignThreads), 0, s, r);
                     if (e != cudaSuccess) return e;
                 }
