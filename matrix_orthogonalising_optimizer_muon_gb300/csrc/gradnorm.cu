@@ -121,12 +121,12 @@ __device__ __forceinline__ double chunk_squares(const GradEntry& e, long long g0
 struct ChunkWalk {
     uint32_t c, to;
     int i;
-    template <int N>
-    __device__ __forceinline__ explicit ChunkWalk(const GradTable<N>& t)
+    template <typename Table>
+    __device__ __forceinline__ explicit ChunkWalk(const Table& t)
         : c((uint32_t)((uint64_t)t.chunks * blockIdx.x / gridDim.x)),
           to((uint32_t)((uint64_t)t.chunks * (blockIdx.x + 1) / gridDim.x)), i(t.start[blockIdx.x]) {}
-    template <int N>
-    __device__ __forceinline__ const GradEntry& entry(const GradTable<N>& t) {
+    template <typename Table>
+    __device__ __forceinline__ const GradEntry& entry(const Table& t) {
         while (i + 1 < t.n && t.e[i + 1].first <= c) ++i;
         return t.e[i];
     }
@@ -147,7 +147,7 @@ __device__ __forceinline__ double block_sum(double d) {
 // Block b sums a contiguous share of the chunks; the block that comes last adds up all blocks' sums in
 // their order, so the same gradients give the same bits.
 template <int N>
-__global__ void __launch_bounds__(kThreads, kFit) k_grad_norm(const __grid_constant__ GradTable<N> t, double* partial,
+__global__ void __launch_bounds__(kThreads, kFit) k_grad_norm(const __grid_constant__ GradTable<N, false> t, double* partial,
                                                         double* running, int* arrived, float* norm, int first, int last) {
     pdl_trigger();
     pdl_wait();
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, kFit) k_grad_norm(const __grid_const
 }
 
 template <bool IN16, bool OUT16>
-__device__ __forceinline__ void chunk_scale(const GradEntry& e, long long g0, float f) {
+__device__ __forceinline__ void chunk_scale(const GradEntry& e, void* out, long long g0, float f) {
     Groups<IN16> g;
     g.load(e, g0, ((reinterpret_cast<uintptr_t>(e.p) - e.pad * (IN16 ? 2 : 4)) & 15) == 0);
 #pragma unroll
@@ -189,14 +189,14 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& e, long long g0, fl
         g.get(i, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= f;
-        store_eight<OUT16>(e.out, (g0 + i * kThreads + threadIdx.x) * 8 - e.pad, e.count, v);
+        store_eight<OUT16>(out, (g0 + i * kThreads + threadIdx.x) * 8 - e.pad, e.count, v);
     }
 }
 
 // out = g times max_norm / norm where the norm is finite and beyond max_norm, else g itself; in place
 // nothing is read or written then.
 template <int N>
-__global__ void __launch_bounds__(kThreads, kFit) k_grad_clip(const __grid_constant__ GradTable<N> t, const float* norm,
+__global__ void __launch_bounds__(kThreads, kFit) k_grad_clip(const __grid_constant__ GradTable<N, true> t, const float* norm,
                                                         float max_norm, int in_place) {
     pdl_trigger();
     pdl_wait();
@@ -207,25 +207,25 @@ __global__ void __launch_bounds__(kThreads, kFit) k_grad_clip(const __grid_const
         const GradEntry& e = w.entry(t);
         const long long k = w.c - e.first;
         if (e.bf16)
-            e.out_bf16 ? chunk_scale<true, true>(e, k * kChunkGroups16, f)
-                       : chunk_scale<true, false>(e, k * kChunkGroups16, f);
+            e.out_bf16 ? chunk_scale<true, true>(e, t.out[w.i], k * kChunkGroups16, f)
+                       : chunk_scale<true, false>(e, t.out[w.i], k * kChunkGroups16, f);
         else
-            e.out_bf16 ? chunk_scale<false, true>(e, k * kChunkGroups32, f)
-                       : chunk_scale<false, false>(e, k * kChunkGroups32, f);
+            e.out_bf16 ? chunk_scale<false, true>(e, t.out[w.i], k * kChunkGroups32, f)
+                       : chunk_scale<false, false>(e, t.out[w.i], k * kChunkGroups32, f);
     }
 }
 
 template <int N>
 cudaError_t norm_of(const GradList& l, int from, int to, const GradNormArgs& a, bool last, cudaStream_t s) {
-    GradTable<N> t;
+    GradTable<N, false> t;
     const int blocks = l.table(from, to, kFit * a.sm_count, &t);
-    return launch_pdl(k_grad_norm<N>, dim3(blocks), dim3(kThreads), 0, s, t, a.partial, a.running, a.arrived,
-                      a.norm, from == 0, (int)last);
+    return launch_pdl(k_grad_norm<N>, dim3(blocks), dim3(kThreads), 0, s, t, a.partial, a.running, a.arrived, a.norm,
+                      from == 0, (int)last);
 }
 template <int N>
 cudaError_t clip_of(const GradList& l, int from, int to, const float* norm, float max_norm, int sm_count,
                     cudaStream_t s) {
-    GradTable<N> t;
+    GradTable<N, true> t;
     const int blocks = l.table(from, to, kFit * sm_count, &t);
     return launch_pdl(k_grad_clip<N>, dim3(blocks), dim3(kThreads), 0, s, t, norm, max_norm, (int)l.in_place);
 }
@@ -233,23 +233,23 @@ cudaError_t clip_of(const GradList& l, int from, int to, const float* norm, floa
 }  // namespace
 
 cudaError_t launch_grad_norm(const GradList& l, const GradNormArgs& a, cudaStream_t s) {
-    for (int from = 0; from == 0 || from < l.n; from += kTableMost) {
-        const int to = std::min(l.n, from + kTableMost);
+    for (int from = 0; from == 0 || from < l.n; from += kTableNorm) {
+        const int to = std::min(l.n, from + kTableNorm);
         const bool last = to == l.n;
         const cudaError_t e = to - from <= kTableFew    ? norm_of<kTableFew>(l, from, to, a, last, s)
                               : to - from <= kTableSome ? norm_of<kTableSome>(l, from, to, a, last, s)
-                                                        : norm_of<kTableMost>(l, from, to, a, last, s);
+                                                        : norm_of<kTableNorm>(l, from, to, a, last, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
 cudaError_t launch_grad_clip(const GradList& l, const float* norm, float max_norm, int sm_count, cudaStream_t s) {
-    for (int from = 0; from < l.n; from += kTableMost) {
-        const int to = std::min(l.n, from + kTableMost);
+    for (int from = 0; from < l.n; from += kTableClip) {
+        const int to = std::min(l.n, from + kTableClip);
         const cudaError_t e = to - from <= kTableFew    ? clip_of<kTableFew>(l, from, to, norm, max_norm, sm_count, s)
                               : to - from <= kTableSome ? clip_of<kTableSome>(l, from, to, norm, max_norm, sm_count, s)
-                                                        : clip_of<kTableMost>(l, from, to, norm, max_norm, sm_count, s);
+                                                        : clip_of<kTableClip>(l, from, to, norm, max_norm, sm_count, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -14,7 +14,6 @@ constexpr int kChunkGroups16 = 2048, kChunkGroups32 = 1024;   // groups of a chu
 
 struct GradEntry {
     const void* p;
-    void* out;               // clip
     long long count;
     uint32_t first;          // first chunk
     uint8_t bf16, out_bf16;
@@ -22,15 +21,19 @@ struct GradEntry {
 };
 
 // Parameters of one launch: at most 32764 bytes, the few for short lists.
-constexpr int kTableFew = 30, kTableSome = 220, kTableMost = 960;
+constexpr int kTableFew = 30, kTableSome = 220, kTableNorm = 1280, kTableClip = 960;
 constexpr int kMostBlocks = 640;
-template <int N>
+template <int N, bool OUT>
 struct GradTable {
+    static constexpr bool kOut = OUT;
     GradEntry e[N];
+    void* out[OUT ? N : 1];        // clip: where the result goes
     uint16_t start[kMostBlocks];   // the gradient that each block's first chunk lies in
     int n;
     uint32_t chunks;
 };
+static_assert(sizeof(GradTable<kTableNorm, false>) <= 32764 - 64 && sizeof(GradTable<kTableClip, true>) <= 32764 - 64,
+              "a launch's parameters");
 
 struct GradList {
     const void* const* p;
@@ -42,16 +45,17 @@ struct GradList {
     bool in_place;
 
     // The table of gradients from .. to - 1 for at most `most` blocks, which share the chunks evenly; returns how many.
-    template <int N>
-    int table(int from, int to, int most, GradTable<N>* t) const {
+    template <typename Table>
+    int table(int from, int to, int most, Table* t) const {
         t->n = to - from;
         long long chunks = 0;
         for (int i = from; i < to; ++i) {
             GradEntry& e = t->e[i - from];
-            e.p = p[i], e.out = out ? out[i] : nullptr, e.count = counts[i];
-            e.bf16 = dtypes[i] == 1, e.out_bf16 = out ? out_dtypes[i] == 1 : 0;
-            const uintptr_t at = reinterpret_cast<uintptr_t>(out ? e.out : e.p);
-            const int esz = (out ? e.out_bf16 : e.bf16) ? 2 : 4, groups = e.bf16 ? kChunkGroups16 : kChunkGroups32;
+            e.p = p[i], e.count = counts[i];
+            e.bf16 = dtypes[i] == 1, e.out_bf16 = Table::kOut ? out_dtypes[i] == 1 : 0;
+            if (Table::kOut) t->out[i - from] = out[i];
+            const uintptr_t at = reinterpret_cast<uintptr_t>(Table::kOut ? out[i] : p[i]);
+            const int esz = (Table::kOut ? e.out_bf16 : e.bf16) ? 2 : 4, groups = e.bf16 ? kChunkGroups16 : kChunkGroups32;
             e.pad = (uint16_t)((at & 15) / esz);
             e.first = (uint32_t)chunks;
             if (counts[i] > 0) chunks += ((counts[i] + e.pad + 7) / 8 + groups - 1) / groups;

@@ -36,7 +36,7 @@ def norm_of(plan, ts):  # noqa: F811
 
 CASES = [([1], ["f32"]), ([1], ["bf16"]), ([7, 9], ["bf16", "f32"]), ([8192], ["bf16"]), ([8193, 5], ["f32", "bf16"]),
          ([100000, 1, 0, 77777, 0], ["bf16", "f32", "bf16", "f32", "bf16"]), ([3, 4] * 20, ["bf16", "f32"] * 20),
-         (list(range(1, 2100)), ["bf16", "f32", "bf16"] * 700), ([5000000], ["bf16"]), ([0, 0], ["f32", "bf16"])]
+         (list(range(1, 2700)), ["bf16", "f32", "bf16"] * 900), ([5000000], ["bf16"]), ([0, 0], ["f32", "bf16"])]
 
 
 @pytest.mark.parametrize("shift", [0, 1, 3])
