@@ -722,6 +722,7 @@ struct Job {
 };
 struct AlignArgs {
     Job job[2];
+    int blocks;            // of the first job; the others are the second's
     ProductArgs a;
 };
 
@@ -730,38 +731,38 @@ constexpr int kAlignThreads = 256, kAlignUnroll = 4;
 __global__ void __launch_bounds__(kAlignThreads) k_align_rows(const AlignArgs args) {
     pdl_trigger();
     pdl_wait();
-    for (int i = 0; i < 2; ++i) {
-        const Job& j = args.job[i];
-        constexpr int kBlock = kAlignThreads * kAlignUnroll;
-        for (long long p0 = (long long)blockIdx.x * kBlock + threadIdx.x; p0 < j.pieces; p0 += (long long)gridDim.x * kBlock) {
-            uint32_t v[kAlignUnroll][8];
-            int d[kAlignUnroll];
-            char* to[kAlignUnroll];
+    const bool second = (int)blockIdx.x >= args.blocks;
+    const Job& j = args.job[second];
+    const int block = second ? blockIdx.x - args.blocks : blockIdx.x, blocks = second ? gridDim.x - args.blocks : args.blocks;
+    constexpr int kBlock = kAlignThreads * kAlignUnroll;
+    for (long long p0 = (long long)block * kBlock + threadIdx.x; p0 < j.pieces; p0 += (long long)blocks * kBlock) {
+        uint32_t v[kAlignUnroll][8];
+        int d[kAlignUnroll];
+        char* to[kAlignUnroll];
 #pragma unroll
-            for (int k = 0; k < kAlignUnroll; ++k) {
-                const long long p = p0 + k * kAlignThreads;
-                const int row = p < j.pieces ? j.by_row.div((int)p) : 0, at = ((int)p - row * (int)j.by_row.d) * 16;
-                bool live = p < j.pieces;
-                if (live && j.by_expert.d) {
-                    int begin, end;
-                    expert_range(args.a, j.by_expert.div(row), &begin, &end);
-                    live = begin < end;
-                }
-                const char* line = j.src + row * j.pitch;
-                d[k] = (int)(reinterpret_cast<uintptr_t>(line) & 15);
-                const uint4* q = reinterpret_cast<const uint4*>(line + at - d[k]);
-                uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                if (live) x = q[0];
-                if (live && d[k] && reinterpret_cast<const char*>(q + 1) < line + j.bytes) y = q[1];
-                v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
-                v[k][4] = y.x, v[k][5] = y.y, v[k][6] = y.z, v[k][7] = y.w;
-                to[k] = live ? j.dst + (uint64_t)row * j.dst_pitch + at : nullptr;
+        for (int k = 0; k < kAlignUnroll; ++k) {
+            const long long p = p0 + k * kAlignThreads;
+            const int row = p < j.pieces ? j.by_row.div((int)p) : 0, at = ((int)p - row * (int)j.by_row.d) * 16;
+            bool live = p < j.pieces;
+            if (live && j.by_expert.d) {
+                int begin, end;
+                expert_range(args.a, j.by_expert.div(row), &begin, &end);
+                live = begin < end;
             }
+            const char* line = j.src + row * j.pitch;
+            d[k] = (int)(reinterpret_cast<uintptr_t>(line) & 15);
+            const uint4* q = reinterpret_cast<const uint4*>(line + at - d[k]);
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (live) x = q[0];
+            if (live && d[k] && reinterpret_cast<const char*>(q + 1) < line + j.bytes) y = q[1];
+            v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+            v[k][4] = y.x, v[k][5] = y.y, v[k][6] = y.z, v[k][7] = y.w;
+            to[k] = live ? j.dst + (uint64_t)row * j.dst_pitch + at : nullptr;
+        }
 #pragma unroll
-            for (int k = 0; k < kAlignUnroll; ++k) {
-                words_down<true>(v[k], d[k]);
-                if (to[k]) *reinterpret_cast<uint4*>(to[k]) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
-            }
+        for (int k = 0; k < kAlignUnroll; ++k) {
+            words_down<true>(v[k], d[k]);
+            if (to[k]) *reinterpret_cast<uint4*>(to[k]) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
         }
     }
 }
@@ -872,9 +873,14 @@ cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s) {
                 if (align_x) c.x = room, c.ldx = px;
                 // an expert's weights are wanted by any of its tokens, not by this chunk's alone
                 r.a.first = 0, r.a.tokens = a.tokens;
-                if (const long long pieces = std::max(r.job[0].pieces, r.job[1].pieces)) {
-                    const long long blocks = std::min<long long>((pieces + 1023) / 1024, 24ll * sm_count);
-                    const cudaError_t e = launch_pdl(k_align_rows, dim3((unsigned)blocks), dim3(kAlignThreads), 0, s, r);
+                int blocks[2];
+                for (int i = 0; i < 2; ++i)
+                    blocks[i] = std::min((r.job[i].pieces + kAlignThreads * kAlignUnroll - 1) / (kAlignThreads * kAlignUnroll),
+                                         12 * sm_count);
+                r.blocks = blocks[0];
+                if (blocks[0] + blocks[1] > 0) {
+                    const cudaError_t e =
+                        launch_pdl(k_align_rows, dim3(blocks[0] + blocks[1]), dim3(kAlignThreads), 0, s, r);
                     if (e != cudaSuccess) return e;
                 }
                 c.m = a.transposed ? a.m : n_out, c.n = a.transposed ? n_out : a.n;
