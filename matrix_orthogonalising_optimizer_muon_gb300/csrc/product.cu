@@ -95,7 +95,9 @@ struct Plan {
     uint16_t height[kBins], order[kBins];     // of each expert; the expert at each place
     int start[kMaxPairs + 4];   // begins of the pairs' stretches, in steps from the first tile of the last turn
     int next[12];                // places of the heights while they are dealt out
-    int sums[8];                 // token tiles when they are at most 256, 128, 64 tokens high
+    int sums[4];                 // token tiles when they are at most 256, 128, 64 tokens high
+    unsigned long long all;      // the last of them
+    int pad[2];
 };
 static_assert(sizeof(Plan) == Cfg::ITEM_OFFSET - Cfg::PLAN_OFFSET, "plan's place");
 
@@ -273,6 +275,7 @@ __device__ __forceinline__ Outline make_plan(const ProductLaunch& L, Plan& p, in
     }
     const bool few = groups <= kBins;
     if (tid < 4) p.sums[tid] = 0;
+    if (tid == 0) p.all = 0;
     __syncthreads();
     int n0 = 0, n1 = 0, n2 = 0;
     for (int g = tid; g < groups; g += threads) {
@@ -281,11 +284,18 @@ __device__ __forceinline__ Outline make_plan(const ProductLaunch& L, Plan& p, in
         if (few) p.begin[g] = b, p.end[g] = e;
         n0 += (e - b + 255) >> 8, n1 += (e - b + 127) >> 7, n2 += (e - b + 63) >> 6;
     }
+    // Offsets that decrease may give the experts many times the tokens that there are, and more tiles than can be
+    // counted: they get none.
+    const unsigned low = __reduce_add_sync(0xffffffffu, n2 & 0xffff), high = __reduce_add_sync(0xffffffffu, n2 >> 16);
     n0 = __reduce_add_sync(0xffffffffu, n0), n1 = __reduce_add_sync(0xffffffffu, n1);
     n2 = __reduce_add_sync(0xffffffffu, n2);
-    if (lane == 0 && n2 > 0) atomicAdd(p.sums, n0), atomicAdd(p.sums + 1, n1), atomicAdd(p.sums + 2, n2);
+    if (lane == 0 && (low | high)) {
+        atomicAdd(p.sums, n0), atomicAdd(p.sums + 1, n1), atomicAdd(p.sums + 2, n2);
+        atomicAdd(&p.all, ((unsigned long long)high << 16) + low);
+    }
     __syncthreads();
-    const Outline o = outline_of(L, p.sums[0], p.sums[1], p.sums[2]);
+    const bool counted = p.all <= (unsigned long long)(L.a.tokens / 64 + groups);
+    const Outline o = outline_of(L, counted ? p.sums[0] : 0, counted ? p.sums[1] : 0, counted ? p.sums[2] : 0);
     if (few) {
         for (int g = tid; g < groups; g += threads) {
             int count, height;

@@ -95,6 +95,18 @@ def test_offsets_are_clamped(plan, edges, dgrad):  # noqa: F811
     check(plan, bf16((300, 264 if dgrad else 136), 3), bf16((len(edges) - 1, 264, 136), 4, 0.1), edges, dgrad)
 
 
+@pytest.mark.parametrize("groups", [9, 4096])
+def test_offsets_that_go_back_and_forth(plan, groups):  # noqa: F811
+    """More tokens among the experts than there are: no fault, and nothing beside the output's rows is written."""
+    import torch
+    tokens, m, n = 20000, 40, 24
+    offsets = torch.tensor([0 if i % 2 == 0 else tokens for i in range(groups + 1)], dtype=torch.int32, device="cuda")
+    wide = torch.full((tokens + 2, m), 3.0, dtype=torch.bfloat16, device="cuda")
+    plan.product(bf16((tokens, n), 1), bf16((groups, m, n), 2), wide[1:-1], offsets=offsets)
+    plan.sync()
+    assert bool((wide[0] == 3).all()) and bool((wide[-1] == 3).all())
+
+
 @pytest.mark.parametrize("dgrad", [False, True])
 @pytest.mark.parametrize("pad,lead", [(8, 8), (16, 0), (3, 1), (7, 2)])
 @pytest.mark.parametrize("m,n", [(256, 192), (271, 333)])
