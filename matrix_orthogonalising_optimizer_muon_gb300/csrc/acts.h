@@ -1,6 +1,7 @@
 // Parameter blocks and launch entry points of the layer-side operators: activations in
-// 8 bits, the RMS norm, SwiGLU and the weight gradient.  Host entry points in acts.cu,
-// kernels in act_elementwise.cu, rmsnorm.cu and wgrad.cu.
+// 8 bits, the RMS norm, SwiGLU, the weight gradient and the other two products of a weight, and
+// tokens in their experts' order.  Host entry points in acts.cu, kernels in act_elementwise.cu,
+// rmsnorm.cu, wgrad.cu, product.cu and experts.cu; lists of gradients in grads.h.
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -10,8 +10,18 @@
 // A cluster of two CTAs computes tiles of 256 outputs x up to 256 tokens (tcgen05.mma.cta_group::2, fp32
 // accumulators in TMEM, double-buffered).  Per CTA: warp 0 issues the TMA loads, warp 1 the MMAs (the
 // even CTA's), warps 2-9 are the epilogue, two for each quarter of the TMEM lanes, on alternate blocks of 32
-// tokens.  A step is 64 values of the contraction: 16 KB of the weight and up to
-// 16 KB of tokens per CTA, in a ring of six.
+// tokens.  A step is 64 values of the contraction: 16 KB of the weight and up to 16 KB of tokens per CTA, in
+// a ring of six (five: 2 % slower).
+//
+// What bounds it: the way from L2 to the SMs.  A step of a 256 x 256 tile takes 64 KB through it in 0.33 us, 15 TB/s
+// over all pairs, about as long as its MMAs at the full clock; requests that bring later steps into L2 make it slower
+// (the 32 experts below 65 us, 106 through TMA).  Measured: 8192 x 3584 x 3584 107 us (1970 TFLOP/s, 103 % of the
+// measured burst rate of a library product), 16384 x 18944 x 3584 1160-1260 us under the power cap, eight experts of
+// 18944 x 3584 over 16384 rows 1365 us.  32 experts of 1024 x 2048 over 16384 ragged rows 59 us: 308 tiles of 256
+// outputs, low ones among them, whose steps cost their weight's 32 KB all the same, in five turns, and about 10 us
+// around them (launch 2, set-up 0.6, plan 2.5, first loads 1, last epilogue 2).  Few rows are bound by the weights'
+// bytes and those 10 us: 32 rows for 32 experts 28 us (HBM 20), eight rows for eight of them 12.4 (HBM 5), one row of
+// one weight of 3584 x 3584 10.4 (HBM 3.8).
 //
 // How the work is dealt out (every CTA derives the same plan from the offsets): tiles in the order experts,
 // bands of token tiles, outputs, token tiles, one per CTA pair and turn, so that the tiles in flight share
@@ -210,7 +220,8 @@ __device__ __forceinline__ void order_experts(Plan& p, int groups, int lane) {
 // How tiles of at most 32 `high` tokens would be dealt out, and the time that takes, in 32 cycles.  A step takes as
 // long as its MMAs, and 256 cycles for the weight's 16 KB besides.  The tiles of the last, incomplete turn are cut
 // along the contraction into stretches of equal length, one per pair, where that saves more than joining the parts
-// takes: about 6 steps' time and, to write and read them, 34 more for 256 tokens.
+// takes: about 24 steps' time and, to write and read them, 34 more for 256 tokens (8 rows for eight of 32 experts, 32
+// steps: 11.5 us whole, 12.6 cut; 16 rows of 18944 values, 296 steps: 61 whole, 30 cut).
 struct Dealt {
     int units, whole, rest, time;
     bool cut;
@@ -219,7 +230,7 @@ struct Dealt {
         units = tiles * L.tiles_m;
         whole = L.by_pairs.div(units);
         rest = units - whole * L.pairs;
-        const int joined = L.by_pairs.div(rest * turn) + (6 + 34 * high / 8) * step;
+        const int joined = L.by_pairs.div(rest * turn) + (24 + 34 * high / 8) * step;
         cut = rest > 0 && joined < turn;
         // beyond 2^31 any height does
         const long long t = (long long)whole * turn + (cut ? joined : rest > 0 ? turn : 0);
@@ -717,9 +728,9 @@ bool map_tokens(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows
 
 // ------------------------------------------------------------------ rows that TMA cannot read
 // TMA takes rows whose addresses are multiples of 16 bytes.  Others are first copied into aligned rows in the
-// workspace, at HBM's rate, chunk by chunk where they do not fit: 8192 x 3584 x 3585 takes 137 us, its 16-byte
-// aligned neighbour 108 (396 when the
-// product's own warps copied each operand of each tile through shifts, bound by the latency of that way).
+// workspace, chunk by chunk where they do not fit: 8192 x 3584 x 3585 takes 137 us, its aligned neighbour 107 (358 to
+// 396 when warps of the product itself copied each operand of each tile through shifts, bound by the latency of that
+// way however they were arranged).  The copy is bound by HBM, 5 TB/s read and written.
 struct Job {
     const char* src;
     char* dst;
