@@ -612,8 +612,10 @@ muon_status muon_wgrad(muon_grad_plan p, const void* dy, int64_t lddy, const muo
  *              (device, groups + 1 int32, non-decreasing, clamped to [0, tokens]); each token is
  *              multiplied with its expert's weight.  Rows of the output outside every expert are
  *              left as they were, whatever the input holds there.
- * Products and sums are fp32 and rounded to bf16 once.  The sums' order depends on the sizes and
- * the offsets alone: the same inputs give the same bits.  1 <= m, n <= 2^20, 0 <= tokens <=
+ * Products and sums are fp32, those of a tile in the accumulators of the tensor cores, whose
+ * additions truncate (a sum of one sign drifts by about 6e-9 of itself per term), and are rounded to
+ * bf16 once.  Their order depends on the sizes and the offsets alone: the same inputs give the same
+ * bits.  1 <= m, n <= 2^20, 0 <= tokens <=
  * 2^31 - 4096, groups <= 4096.  Where rows of x (dy) or of the weight are not aligned to 16 bytes,
  * they are first copied into the plan's workspace, which costs their bytes twice more.
  */

@@ -203,19 +203,19 @@ bool lists_overlap(const void* const* grads, const int64_t* counts, const int32_
                    const int32_t* out_dtypes, const float* norm) {
     struct Span {
         uintptr_t from, to;
-        int index;      // a tensor that is its own output counts once
         bool written;
     };
     std::vector<Span> spans;
     spans.reserve(2 * (size_t)n + 1);
-    spans.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, -1, false});
+    spans.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, false});
     for (int i = 0; i < n; ++i) {
         if (counts[i] == 0) continue;
         const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
         const uintptr_t o = out ? reinterpret_cast<uintptr_t>(out[i]) : g;
         const int32_t od = out ? out_dtypes[i] : dtypes[i];
-        spans.push_back({o, o + (uintptr_t)counts[i] * (od == MUON_BF16 ? 2 : 4), i, true});
-        if (o != g || od != dtypes[i]) spans.push_back({g, g + (uintptr_t)counts[i] * (dtypes[i] == MUON_BF16 ? 2 : 4), i, false});
+        spans.push_back({o, o + (uintptr_t)counts[i] * (od == MUON_BF16 ? 2 : 4), true});
+        if (o != g || od != dtypes[i])   // a tensor that is its own output counts once
+            spans.push_back({g, g + (uintptr_t)counts[i] * (dtypes[i] == MUON_BF16 ? 2 : 4), false});
     }
     std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.from < b.from; });
     uintptr_t read_to = 0, written_to = 0;   // ends of what came before

@@ -28,7 +28,8 @@ __device__ __forceinline__ int remote_int(uint32_t local_saddr, uint32_t rank) {
 }
 
 // Ids from .. of one batch, -1 for those that are no expert or at and beyond `to`.
-__device__ __forceinline__ void load_ids(const OrderArgs& a, long long from, long long to, int lane, int (&id)[kBatch]) {
+__device__ __forceinline__ void load_ids(const OrderArgs& a, long long from, long long to, int lane,
+                                         int (&id)[kBatch]) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) id[j] = from + 32 * j + lane < to ? a.ids[from + 32 * j + lane] : -1;
 #pragma unroll
@@ -189,7 +190,8 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const MoveArgs a) {
             for (int k = 0; k < kUnroll; ++k)
                 if (w.col + k * kSeg < a.cols) {
                     if constexpr (BF16 || VEC) {
-                        seg_store_words<BF16, kMode<BF16, VEC>>(row_ptr(a.y, s), w.col + k * kSeg, a.cols, lane, raw[k].r);
+                        seg_store_words<BF16, kMode<BF16, VEC>>(row_ptr(a.y, s), w.col + k * kSeg, a.cols, lane,
+                                                                raw[k].r);
                     } else {
                         float v[8];
                         raw[k].get(v);
@@ -322,16 +324,18 @@ cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s) {
     int lw = 5;
     while ((a.experts << lw) > kOrderCounts) --lw;
     // One CTA for the smallest (8192 ids of 256: 10.8 us, 8.1 with eight), the largest cluster there is for long ones,
-    // whose ranking is bound by instruction issue, unless reading all CTAs' counts takes longer: 65536 ids of 256
+    // whose ranks take longest, unless reading all CTAs' counts takes longer: 65536 ids of 256
     // 12.8 us with eight CTAs and 14.3 with sixteen, 131072 of 128 16.1 and 13.3, of 4096 51 and 84.
     const int lc = a.n <= 2048 ? 0 : a.n >= 100000 && a.experts <= 1024 ? 4 : 3;
     const size_t bytes = (size_t)((1 << lw) + 3) * a.experts * sizeof(int);
-    // Per call, as an attribute of the current device; the same for every call, as another thread may be between its
-    // own setting and its launch.
+    // Beyond 48 KB an attribute of the current device has to allow it: set per call, and the same by every call, as
+    // another thread may be between its own setting and its launch.
     constexpr int kMostBytes = (8 + 3) * 4096 * (int)sizeof(int);
     static_assert(kMostBytes >= (32 + 3) * 1024 * (int)sizeof(int) && kMostBytes >= (16 + 3) * 2048 * (int)sizeof(int),
                   "the most of any number of experts");
-    cudaError_t e = cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
+    cudaError_t e = cudaSuccess;
+    if (bytes > 48 * 1024)
+        e = cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
     if (e == cudaSuccess && lc == 4)
         e = cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -353,8 +357,8 @@ cudaError_t launch_expert_combine_backward(const MoveArgs& a, bool bf16, bool ve
                                                 k_combine_backward<true, false>, k_combine_backward<true, true>};
     int span = 1;
     while (span < kThreads / 32 && span * kSeg < a.cols) span *= 2;
-    return launch_pdl(k[(bf16 ? 2 : 0) + (vec ? 1 : 0)], dim3(blocks_for((long long)a.tokens * span, 8)), dim3(kThreads),
-                      0, s, a, span);
+    return launch_pdl(k[(bf16 ? 2 : 0) + (vec ? 1 : 0)], dim3(blocks_for((long long)a.tokens * span, 8)),
+                      dim3(kThreads), 0, s, a, span);
 }
 
 }  // namespace muon

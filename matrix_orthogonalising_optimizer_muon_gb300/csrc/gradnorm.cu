@@ -2,8 +2,8 @@
 // tensors of any sizes.  The list travels in the kernel's parameters: no table is copied to
 // the device, so a call enqueues kernels alone and can be captured.  Both are HBM-bound: a 7B layer's 233 million fp32
 // values 138 us for the norm and 207 us scaled into bf16 (6.75 TB/s, the copy rate), 1036 matrices of at most 128 x
-// 3584 in bf16 73 us (6.0 TB/s).  What is left for short lists are about 6 us of launch, first loads and the last block's
-// sum, and 5 more for the 32 KB of parameters of long ones.
+// 3584 in bf16 73 us (6.0 TB/s).  What is left for short lists are about 6 us of launch, first loads and the last
+// block's sum, and 5 more for the 32 KB of parameters of long ones.
 #include "act8.cuh"
 #include "grads.h"
 #include "kernels.h"
@@ -44,7 +44,8 @@ struct Groups {
                     v[j] = at + j >= 0 && at + j < e.count ? load_one<BF16>(e.p, at + j) : 0.f;
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    r[i * kPer + j] = BF16 ? bf16_bits(v[2 * j]) | bf16_bits(v[2 * j + 1]) << 16 : __float_as_uint(v[j]);
+                    r[i * kPer + j] =
+                        BF16 ? bf16_bits(v[2 * j]) | bf16_bits(v[2 * j + 1]) << 16 : __float_as_uint(v[j]);
             }
         }
     }

@@ -280,7 +280,10 @@ __device__ __forceinline__ Outline make_plan(const ProductLaunch& L, Plan& p, in
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, groups = L.a.groups;
     if (!L.a.offsets) {   // one weight: the host knows it
         if (tid <= L.outline.stretches) p.start[tid] = L.start[tid];
-        if (tid == 0) p.begin[0] = 0, p.end[0] = (int)L.a.tokens, p.count[0] = L.count, p.height[0] = (uint16_t)L.height;
+        if (tid == 0) {
+            p.begin[0] = 0, p.end[0] = (int)L.a.tokens;
+            p.count[0] = L.count, p.height[0] = (uint16_t)L.height;
+        }
         __syncthreads();
         return L.outline;
     }
@@ -421,8 +424,8 @@ __device__ __forceinline__ void release_tmem(const Epilogue& e, uint32_t acc) {
 // Stores a warp's 32 outputs x 32 tokens, f: this lane's output of each token.  Tokens t .. t + 31 below `end`.
 // Aligned rows: pairs of tokens in bf16 through shared memory, from which a lane takes four outputs of two
 // tokens; else a lane stores its output of each token, a warp 64 bytes of a row at a time.
-__device__ __forceinline__ void store_block(const ProductLaunch& L, const Epilogue& e, const float (&f)[32], int c0, int t,
-                                            int end) {
+__device__ __forceinline__ void store_block(const ProductLaunch& L, const Epilogue& e, const float (&f)[32], int c0,
+                                            int t, int end) {
     char* y = static_cast<char*>(L.a.y);
     const uint32_t blk = e.blk;
     if (L.wide) {
@@ -441,7 +444,8 @@ __device__ __forceinline__ void store_block(const ProductLaunch& L, const Epilog
             for (int i = 0; i < 4; ++i, to += 8 * pitch) {
                 const int r = t + 2 * (p0 + 4 * i);
                 if (r < end)
-                    *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(x[i].x, x[i].y, 0x5410), __byte_perm(x[i].z, x[i].w, 0x5410));
+                    *reinterpret_cast<uint2*>(to) =
+                        make_uint2(__byte_perm(x[i].x, x[i].y, 0x5410), __byte_perm(x[i].z, x[i].w, 0x5410));
                 if (r + 1 < end)
                     *reinterpret_cast<uint2*>(to + pitch) =
                         make_uint2(__byte_perm(x[i].x, x[i].y, 0x7632), __byte_perm(x[i].z, x[i].w, 0x7632));
@@ -484,7 +488,8 @@ __device__ __forceinline__ void epilogue(const ProductLaunch& L, const Plan& pla
     for (int turn = 0; turn < items.count; ++turn, ++local) {
         const Item w = items.get(L, plan, outline, e.table, turn);
         const uint32_t acc = local & 1;
-        if (!mbar_wait_idle(e.tfull + acc, local >> 1 & 1u, e.abort_flag, L.a.status, kStatusTimeoutEpilogue, true)) return;
+        if (!mbar_wait_idle(e.tfull + acc, local >> 1 & 1u, e.abort_flag, L.a.status, kStatusTimeoutEpilogue, true))
+            return;
         tc_fence_after();
         const uint32_t tbase = e.tmem_base + acc * 256 + (static_cast<uint32_t>(e.wq * 32) << 16);
         const int c0 = w.m0 + 128 * e.q + 32 * e.wq;
@@ -754,7 +759,8 @@ __global__ void __launch_bounds__(kAlignThreads) k_align_rows(const AlignArgs ar
     pdl_wait();
     const bool second = (int)blockIdx.x >= args.blocks;
     const Job& j = args.job[second];
-    const int block = second ? blockIdx.x - args.blocks : blockIdx.x, blocks = second ? gridDim.x - args.blocks : args.blocks;
+    const int block = second ? blockIdx.x - args.blocks : blockIdx.x;
+    const int blocks = second ? gridDim.x - args.blocks : args.blocks;
     constexpr int kBlock = kAlignThreads * kAlignUnroll;
     for (long long p0 = (long long)block * kBlock + threadIdx.x; p0 < j.pieces; p0 += (long long)blocks * kBlock) {
         uint32_t v[kAlignUnroll][8];
@@ -809,7 +815,8 @@ cudaError_t launch_aligned(const ProductArgs& a, int out, long long pitch, int s
         const int t = (int)a.tokens;
         L.outline = outline_of(L, (int)((t + 255ll) >> 8), (int)((t + 127ll) >> 7), (int)((t + 63ll) >> 6));
         cut_range(t, L.outline.cap, &L.count, &L.height);
-        for (int i = 0; L.outline.stretches && i <= L.outline.stretches; ++i) L.start[i] = stretch_start(L, L.outline, i);
+        for (int i = 0; L.outline.stretches && i <= L.outline.stretches; ++i)
+            L.start[i] = stretch_start(L, L.outline, i);
     }
     L.wide = L.out % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)(a.ldy * 2)) & 7) == 0;
     // weights: rows of the contraction or of the outputs
@@ -890,14 +897,14 @@ cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s) {
                     }
                     c.weight = room_w;
                 }
-                if (align_x && (tokens < a.tokens || (g == 0 && o == 0))) set_job(&r.job[1], c.x, a.ldx, room, px, c.tokens, k);
+                if (align_x && (tokens < a.tokens || (g == 0 && o == 0)))
+                    set_job(&r.job[1], c.x, a.ldx, room, px, c.tokens, k);
                 if (align_x) c.x = room, c.ldx = px;
                 // an expert's weights are wanted by any of its tokens, not by this chunk's alone
                 r.a.first = 0, r.a.tokens = a.tokens;
                 int blocks[2];
-                for (int i = 0; i < 2; ++i)
-                    blocks[i] = std::min((r.job[i].pieces + kAlignThreads * kAlignUnroll - 1) / (kAlignThreads * kAlignUnroll),
-                                         12 * sm_count);
+                constexpr int kBlock = kAlignThreads * kAlignUnroll;
+                for (int i = 0; i < 2; ++i) blocks[i] = std::min((r.job[i].pieces + kBlock - 1) / kBlock, 12 * sm_count);
                 r.blocks = blocks[0];
                 if (blocks[0] + blocks[1] > 0) {
                     const cudaError_t e =
