@@ -226,3 +226,56 @@ def test_captured(mu):  # noqa: F811
         count = torch.tensor((want[1] >= 0).sum(1), device="cuda")[:, None]
         # up to four copies: exact in fp32 (8 + 2 bits), rounded once
         assert torch.equal(y, (x.float() * count).bfloat16())
+
+
+def test_on_another_stream(mu):  # noqa: F811
+    """The calls run on the stream that they are given, behind what is on it."""
+    import torch
+    ids = on_gpu(np.random.default_rng(2).integers(0, 16, (2000, 3)))
+    x = rand((2000, 300), "bf16", 1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        big = torch.randn(4096, 4096, device="cuda")
+        for _ in range(3):
+            big = big @ big / 64           # what comes before on that stream
+        new = x * 2
+    offsets, slots = torch.empty(17, dtype=torch.int32, device="cuda"), torch.empty_like(ids)
+    xs, y, dw = torch.zeros((6000, 300), dtype=torch.bfloat16, device="cuda"), torch.empty_like(x), \
+        torch.empty((2000, 3), device="cuda")
+    ones = torch.ones((2000, 3), device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    mu.expert_order(ids, offsets, slots, stream=s)
+    mu.expert_dispatch(new, slots, xs, stream=s)
+    mu.expert_combine(xs, slots, y, stream=s)
+    mu.expert_combine_backward(y, slots, ones, rows=xs, dweights=dw, stream=s)
+    s.synchronize()
+    assert torch.equal(y, (x.float() * 6).bfloat16())   # three copies of 2 x
+    want = order(ids.cpu().numpy(), 16)
+    assert np.array_equal(slots.cpu().numpy(), want[1])
+    assert torch.allclose(dw, (y.float() * new.float()).sum(1, keepdim=True).expand(-1, 3), rtol=1e-4, atol=1e-3)
+
+
+def test_what_the_binding_refuses(mu):  # noqa: F811
+    import torch
+    ids, slots = on_gpu(np.zeros((8, 2))), on_gpu(np.arange(16).reshape(8, 2))
+    offsets, x, rows = torch.empty(5, dtype=torch.int32, device="cuda"), rand((8, 40), "f32", 1), rand((16, 40), "f32", 2)
+    w = torch.ones((8, 2), device="cuda")
+    bad = [lambda: mu.expert_order(ids.long(), offsets, slots), lambda: mu.expert_order(ids[:, :1], offsets, slots),
+           lambda: mu.expert_order(ids, offsets.long(), slots), lambda: mu.expert_order(ids, offsets[:1], slots),
+           lambda: mu.expert_order(ids.flatten(), offsets, slots), lambda: mu.expert_order(ids.t(), offsets, slots),
+           lambda: mu.expert_dispatch(x, slots[:4], rows), lambda: mu.expert_dispatch(x, slots, rows.bfloat16()),
+           lambda: mu.expert_dispatch(x, slots, rows[:, :39]), lambda: mu.expert_dispatch(x.half(), slots, rows.half()),
+           lambda: mu.expert_dispatch(x, slots, rows.cpu()), lambda: mu.expert_dispatch(x.t(), slots, rows),
+           lambda: mu.expert_combine(rows, slots, x, weights=w.bfloat16()),
+           lambda: mu.expert_combine(rows, slots, x, weights=w[:, :1]),
+           lambda: mu.expert_combine_backward(x, slots, w, rows=rows, drows=rows[:8].clone()),
+           lambda: mu.expert_combine_backward(x, slots, w, rows=rows, dweights=w.double())]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: mu.expert_dispatch(rows[:8], slots, rows), lambda: mu.expert_combine(rows, slots, rows[:8]),
+                 lambda: mu.expert_combine_backward(x, slots, w), lambda: mu.expert_combine_backward(x, slots, w, dweights=w),
+                 lambda: mu.expert_combine_backward(x, slots, w, rows=rows, drows=rows)):
+        with pytest.raises(mu.MuonError):
+            call()

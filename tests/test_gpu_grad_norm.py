@@ -182,3 +182,19 @@ def test_captured(mu, plan):  # noqa: F811
         assert abs(float(norm) - want) <= TOL * want
         # bf16 results: each rounded to 2^-9 of itself
         assert abs(norm64(ts) - min(want, 0.5)) <= 2.0 ** -8 * min(want, 0.5)
+
+
+def test_what_the_binding_refuses(mu, plan):  # noqa: F811
+    import torch
+    a, b = torch.zeros(10, device="cuda"), torch.zeros(20, device="cuda").bfloat16()
+    norm = torch.zeros(1, device="cuda")
+    for call in (lambda: mu.GradList([a.half()]), lambda: mu.GradList([a.cpu()]), lambda: mu.GradList([b.view(4, 5).t()]),
+                 lambda: plan.grad_norm([a], torch.zeros(2, device="cuda")), lambda: plan.grad_norm([a], norm.double()),
+                 lambda: plan.grad_clip([a, b], norm, 1.0, out=[b, a]), lambda: plan.grad_clip([a, b], norm, 1.0, out=[a])):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: plan.grad_clip([a, a], norm, 1.0), lambda: plan.grad_clip([a, a[5:]], norm, 1.0),
+                 lambda: plan.grad_clip([a], norm, 0.0), lambda: plan.grad_clip([a, norm], norm, 1.0),
+                 lambda: plan.grad_clip([a], norm, 1.0, out=[a.view(torch.bfloat16)[:10]])):
+        with pytest.raises(mu.MuonError):
+            call()

@@ -299,3 +299,23 @@ def test_the_three_products_agree_with_differences(mu, plan):  # noqa: F811
     # dx: (2 m + 8) u of its terms and a bf16 rounding (2^-8 of the result, which the terms bound); fp64 of loss
     assert abs(float((dx.double() * vx).sum()) - along_x) <= ((2 * m + 8) * U + 2.0 ** -8 + 1e-10) * size_x
     assert abs(float((dw.double() * vw).sum()) - along_w) <= ((2 * 90 + 8) * U + 1e-10) * size_w
+
+
+def test_what_the_binding_refuses(mu, plan):  # noqa: F811
+    import torch
+    x, w, y = bf16((8, 40), 1), bf16((3, 24, 40), 2), bf16((8, 24), 3)
+    o = torch.tensor([0, 2, 5, 8], dtype=torch.int32, device="cuda")
+    bad = [lambda: plan.product(x.float(), w, y, offsets=o), lambda: plan.product(x, w.float(), y, offsets=o),
+           lambda: plan.product(x, w, y.float(), offsets=o), lambda: plan.product(x, w, y, offsets=o.long()),
+           lambda: plan.product(x, w, y, offsets=o[:3]), lambda: plan.product(x, w, y, offsets=o[:1]),
+           lambda: plan.product(x, w, y), lambda: plan.product(x, w[0], y, offsets=o), lambda: plan.product(x, w[0], x),
+           lambda: plan.product(x, w.transpose(1, 2), y, offsets=o), lambda: plan.product(x[:, :39], w, y, offsets=o),
+           lambda: plan.product(x[:7], w, y, offsets=o), lambda: plan.dgrad(x, w, y, offsets=o),
+           lambda: plan.product(x.cpu(), w, y, offsets=o), lambda: plan.product(x, w.cpu(), y, offsets=o),
+           lambda: plan.product(x.t(), w, y, offsets=o)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    square = bf16((40, 40), 4)
+    with pytest.raises(mu.MuonError):
+        plan.product(x, square, x)                       # in place
