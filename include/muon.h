@@ -648,7 +648,7 @@ muon_status muon_expert_order(const int32_t* ids, int64_t tokens, int32_t choice
  *   muon_expert_combine_backward  drows[slots[t, j], :] = weights[t, j] dout[t, :] (other rows are left as
  *                                 they were; slots must not repeat a row) and dweights[t, j] = dout[t, :] .
  *                                 expert_rows[slots[t, j], :], 0 where there is no choice.  Either output may be
- *                                 NULL, and expert_rows without dweights.
+ *                                 NULL, and expert_rows without dweights or where rows is 0.
  * 1 <= choices <= 64, tokens * choices < 2^31, 0 <= rows < 2^31, 1 <= cols <= 2^20.
  */
 muon_status muon_expert_dispatch(const void* x, int64_t ldx, const int32_t* slots, int64_t tokens, int32_t choices,

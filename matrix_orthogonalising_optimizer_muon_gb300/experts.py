@@ -75,13 +75,15 @@ def expert_combine(rows, slots, out, weights=None, stream=None):
 
 def expert_combine_backward(dout, slots, weights, rows=None, drows=None, dweights=None, stream=None):
     """``muon_expert_combine_backward``: drows[slots[t, j]] = weights[t, j] * dout[t], other rows left as they were,
-    and dweights[t, j] = dout[t] . rows[slots[t, j]] (either may be None; rows is read for dweights alone)."""
+    and dweights[t, j] = dout[t] . rows[slots[t, j]] (either may be None; rows is read for dweights alone, which
+    needs it)."""
     tokens, cols, dt, code, dev = _shape(dout, "dout")
     ps, _, choices = _choices(slots, dev)
     if slots.shape[0] != tokens:
         raise ValueError("slots: need %d tokens, got %s" % (tokens, tuple(slots.shape)))
     given = rows if rows is not None else drows
-    n = given.shape[0] if given is not None else 0
+    # where neither says how many rows there are, slots may name any: dweights without rows is refused, as beside drows
+    n = given.shape[0] if given is not None else slots.numel()
     f32 = activations.torch.float32
     pd, ld = _mat(dout, tokens, cols, dt, dev, "dout")
     pr, lr = _mat(rows, n, cols, dt, dev, "rows")

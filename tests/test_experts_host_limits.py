@@ -1,0 +1,64 @@
+"""What the experts' and gradient-norm calls refuse or promise beyond single arguments, on the CPU."""
+import pytest
+
+import matrix_orthogonalising_optimizer_muon_gb300 as mu
+from matrix_orthogonalising_optimizer_muon_gb300 import experts
+
+torch = pytest.importorskip("torch")
+
+
+class OnDevice:
+    """Stands for a dense tensor of device 0, which this machine need not have."""
+    is_cuda, device = True, "cuda:0"
+    count = 0
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape = dtype, torch.Size(shape)
+        OnDevice.count += 1
+        self.at = OnDevice.count << 32
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def stride(self, i):
+        return self.shape[i + 1:].numel()
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.at
+
+
+class Stream:
+    cuda_stream = 0
+
+
+def test_gradient_of_the_weights_needs_the_rows(monkeypatch):
+    """dweights without rows: the call reaches the library with the rows' number above zero, so that it is refused, and
+    never as one of no rows, which gives zeros.  What is not refused is not called here."""
+    calls, lib = [], mu.load()
+
+    class Library:
+        @staticmethod
+        def muon_expert_combine_backward(*args):
+            calls.append(args)
+            rows, expert_rows = args[8], args[4]
+            return lib.muon_expert_combine_backward(*args) if rows > 0 and expert_rows is None else mu.MUON_OK
+    monkeypatch.setattr(experts, "load", lambda: Library)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    f32, i32 = torch.float32, torch.int32
+    dout, slots, w, dw = OnDevice(f32, 8, 40), OnDevice(i32, 8, 2), OnDevice(f32, 8, 2), OnDevice(f32, 8, 2)
+    for drows in (None, OnDevice(f32, 16, 40)):
+        with pytest.raises(mu.MuonError) as refused:
+            mu.expert_combine_backward(dout, slots, w, drows=drows, dweights=dw, stream=Stream)
+        assert refused.value.code == mu.MUON_ERR_INVALID_ARG
+    # rows of a batch whose tokens chose nothing: an empty tensor says so
+    mu.expert_combine_backward(dout, slots, w, rows=OnDevice(f32, 0, 40), dweights=dw, stream=Stream)
+    assert [c[8] for c in calls] == [16, 16, 0]
