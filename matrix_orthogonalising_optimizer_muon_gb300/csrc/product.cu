@@ -517,11 +517,12 @@ __device__ __forceinline__ void epilogue(const ProductLaunch& L, const Plan& pla
         } else if (parts) {
             int* count = L.a.counters + (first * 2 + e.q) * 8 + e.wq + (e.first >> 3);
             int seen = 0;
-            __syncwarp();   // the warp's sums before lane 0's release, the others' after its acquire
+            __syncwarp();   // the warp's sums before lane 0's release
             if (e.lane == 0)
                 asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(seen) : "l"(count) : "memory");
             if (__shfl_sync(0xffffffffu, seen, 0) == parts - 1) {   // the last part: all of them, in their order
                 if (e.lane == 0) *count = 0;   // for the next call
+                __syncwarp();   // all lanes' reads after lane 0's acquire: the shuffle orders no memory
                 for (int c = e.first; c < w.n; c += 64) {
                     Block a;
                     a.load(slot(0) + c * 32);

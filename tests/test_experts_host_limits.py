@@ -1,10 +1,14 @@
 """What the experts' and gradient-norm calls refuse or promise beyond single arguments, on the CPU."""
+import os
+import re
+
 import pytest
 
 import matrix_orthogonalising_optimizer_muon_gb300 as mu
 from matrix_orthogonalising_optimizer_muon_gb300 import experts
 
 torch = pytest.importorskip("torch")
+CSRC = os.path.join(os.path.dirname(os.path.abspath(mu.__file__)), "csrc")
 
 
 class OnDevice:
@@ -62,3 +66,14 @@ def test_gradient_of_the_weights_needs_the_rows(monkeypatch):
     # rows of a batch whose tokens chose nothing: an empty tensor says so
     mu.expert_combine_backward(dout, slots, w, rows=OnDevice(f32, 0, 40), dweights=dw, stream=Stream)
     assert [c[8] for c in calls] == [16, 16, 0]
+
+
+@pytest.mark.parametrize("source,load", [("product.cu", "a.load(")])
+def test_lanes_that_read_other_parts_are_ordered_behind_their_arrival(source, load):
+    """One lane counts the parts of a cut tile and tells the others by a shuffle, which orders no memory: a warp barrier
+    stands between the branch that the count decides and the first read of another CTA's part."""
+    src = open(os.path.join(CSRC, source)).read()
+    joins = re.findall(r"__shfl_sync\(0xffffffffu, seen, 0\) == (?:L\.)?parts - 1\) \{(.*?)" + re.escape(load), src, re.S)
+    assert len(joins) == 1
+    code = re.sub(r"//.*", "", joins[0])
+    assert "__syncwarp();" in code
