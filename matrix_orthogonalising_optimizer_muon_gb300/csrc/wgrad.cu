@@ -604,6 +604,7 @@ __device__ __forceinline__ void epilogue(const WgradLaunch& L, const EpilogueArg
             if (__shfl_sync(0xffffffffu, seen, 0) == L.parts - 1) {
                 if (e.lane == 0) *count = 0;   // for the next call
                 __threadfence();
+                __syncwarp();   // all lanes' reads after lane 0's fence: the shuffle orders no memory
                 const OutTile<BF16, WIDE> out(L, w, r0, e.lane);
                 for (int c0 = 0; c0 < 256; c0 += 32) {
                     float f[32];

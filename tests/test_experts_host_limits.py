@@ -68,7 +68,7 @@ def test_gradient_of_the_weights_needs_the_rows(monkeypatch):
     assert [c[8] for c in calls] == [16, 16, 0]
 
 
-@pytest.mark.parametrize("source,load", [("product.cu", "a.load(")])
+@pytest.mark.parametrize("source,load", [("product.cu", "a.load("), ("wgrad.cu", "part_load<WIDE>(")])
 def test_lanes_that_read_other_parts_are_ordered_behind_their_arrival(source, load):
     """One lane counts the parts of a cut tile and tells the others by a shuffle, which orders no memory: a warp barrier
     stands between the branch that the count decides and the first read of another CTA's part."""
