@@ -666,7 +666,7 @@ muon_status muon_expert_combine_backward(const void* dout, int64_t ldd, const in
  *   grads, counts, dtypes  HOST arrays of n device pointers, element counts (0: skipped) and
  *                          muon_dtype codes, read before the call returns.  Each gradient is dense and
  *                          aligned to its elements; the counts sum to at most 2^43.
- *   norm                   device, one fp32.
+ *   norm                   device, one fp32, outside the gradients.
  * Squares are summed in fp32 over at most 64 values, then in fp64, in a fixed order; they neither overflow
  * nor vanish, whatever the gradients' scale.  A NaN gives NaN, an infinity or a norm beyond fp32's range
  * infinity; no gradients give 0.

@@ -508,6 +508,12 @@ muon_status muon_grad_norm(muon_grad_plan p, const void* const* grads, const int
                            int32_t n, float* norm, void* stream) {
     if (!p || !norm || (reinterpret_cast<uintptr_t>(norm) & 3)) return MUON_ERR_INVALID_ARG;
     MUON_CALL(check_list(grads, counts, dtypes, n));
+    const uintptr_t at = reinterpret_cast<uintptr_t>(norm);
+    for (int i = 0; i < n; ++i) {   // written: not inside a gradient
+        const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
+        if (counts[i] > 0 && g < at + 4 && at < g + (uintptr_t)counts[i] * (dtypes[i] == MUON_BF16 ? 2 : 4))
+            return MUON_ERR_INVALID_ARG;
+    }
     MUON_CALL(check_grad_plan(p));
     const GradList l{grads, counts, dtypes, nullptr, nullptr, n, false};
     const GradNormArgs a{reinterpret_cast<double*>(p->partial), p->running, p->arrived, norm, p->sm_count};

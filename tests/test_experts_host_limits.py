@@ -1,4 +1,5 @@
 """What the experts' and gradient-norm calls refuse or promise beyond single arguments, on the CPU."""
+import ctypes
 import os
 import re
 
@@ -77,3 +78,18 @@ def test_lanes_that_read_other_parts_are_ordered_behind_their_arrival(source, lo
     assert len(joins) == 1
     code = re.sub(r"//.*", "", joins[0])
     assert "__syncwarp();" in code
+
+
+A, B = 0x100000000, 0x200000000   # far apart, 16-byte aligned, never dereferenced
+
+
+@pytest.mark.parametrize("spec,norm", [
+    ([(A, 100, 0)], A), ([(A, 100, 0)], A + 396), ([(A, 100, 0)], A + 200), ([(A, 101, 1)], A + 200),
+    ([(A + 2, 1, 1)], A), ([(B, 7, 1), (A, 0, 0), (A, 100, 0)], A + 4), ([(B + k * 4096, 8, 0) for k in range(3000)], B + 2999 * 4096)])
+def test_norm_does_not_lie_in_a_gradient(spec, norm):
+    """A norm that would overwrite a value of the gradients: the first, the last, half of a pair of bf16 values."""
+    n = len(spec)
+    p, c, d = ((t * n)(*[x[i] for x in spec]) for i, t in enumerate((ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32)))
+    # of a plan of no device, not read before the check
+    handle = ctypes.cast(ctypes.create_string_buffer(b"\xff" * 256, 256), ctypes.c_void_p)
+    assert mu.load().muon_grad_norm(handle, p, c, d, n, norm, None) == mu.MUON_ERR_INVALID_ARG
