@@ -548,16 +548,24 @@ muon_status muon_swiglu_backward(const void* da, int64_t ldda, const muon_act8* 
 
 /*
  * A grad plan owns what the reductions and the products need on the current device: one
- * workspace allocation of muon_grad_plan_workspace_size bytes, whatever shapes its
+ * workspace allocation of muon_grad_plan_workspace_size bytes (308 MB), whatever shapes its
  * calls have, and a status word.  Calls on one plan share the workspace: they are
- * ordered by the caller, as those of a muon_plan.  muon_grad_plan_create
+ * ordered by the caller, as those of a muon_plan.  The _ex forms take the bytes of the
+ * workspace that serve nothing but the copies which muon_product and muon_dgrad make of rows
+ * that are not aligned to 16 bytes: 0 to 2^34.  The others take 2^28 less the 43 MB that those
+ * copies share with the other calls; with 0 a plan is 83 MB.  Operands that do not fit are
+ * copied in pieces, a launch or two each, and where 64 rows of one (columns, of
+ * muon_dgrad's weight) are more than half of both shares the product is refused
+ * (MUON_ERR_UNSUPPORTED), which no size reaches without _ex.  muon_grad_plan_create
  * synchronises the host; so do muon_grad_plan_destroy (the whole device; NULL is ignored) and
  * muon_grad_plan_sync, which waits for stream, then reads and clears the status word
  * (MUON_ERR_TIMEOUT as muon_sync).
  */
 typedef struct muon_grad_plan_s* muon_grad_plan;
 muon_status muon_grad_plan_create(muon_grad_plan* out);
+muon_status muon_grad_plan_create_ex(muon_grad_plan* out, int64_t aligned_bytes);
 muon_status muon_grad_plan_workspace_size(int64_t* bytes);
+muon_status muon_grad_plan_workspace_size_ex(int64_t aligned_bytes, int64_t* bytes);
 void muon_grad_plan_destroy(muon_grad_plan p);
 muon_status muon_grad_plan_sync(muon_grad_plan p, void* stream);
 

@@ -129,7 +129,9 @@ EXPORTED = {
     "muon_swiglu_forward": (_I, [_P, _L, _P, _L, _L, _L, _I, _P, _L, _A, _A, _A, _P]),
     "muon_swiglu_backward": (_I, [_P, _L, _A, _A, _L, _L, _I, _P, _L, _P, _L, _A, _P]),
     "muon_grad_plan_create": (_I, [ctypes.POINTER(_P)]),
+    "muon_grad_plan_create_ex": (_I, [ctypes.POINTER(_P), _L]),
     "muon_grad_plan_workspace_size": (_I, [ctypes.POINTER(_L)]),
+    "muon_grad_plan_workspace_size_ex": (_I, [_L, ctypes.POINTER(_L)]),
     "muon_grad_plan_destroy": (None, [_P]),
     "muon_grad_plan_sync": (_I, [_P, _P]),
     "muon_rmsnorm_backward": (_I, [_P, _P, _L, _A, _P, _L, _P, _P, _P, _L, _L, _L, _I, _P, _L, _P,

@@ -181,10 +181,14 @@ def swiglu_backward(dout, saved_gate: Act8, saved_up: Act8, dgate, dup, saved_ou
            "muon_swiglu_backward")
 
 
-def grad_plan_workspace_size() -> int:
-    """Device bytes that every ``GradPlan`` allocates (``muon_grad_plan_workspace_size``; no GPU needed)."""
+def grad_plan_workspace_size(aligned_bytes: int | None = None) -> int:
+    """Device bytes that a ``GradPlan`` of these ``aligned_bytes`` allocates (``muon_grad_plan_workspace_size``; no GPU
+    needed)."""
     n = ctypes.c_int64()
-    _check(load().muon_grad_plan_workspace_size(ctypes.byref(n)), "muon_grad_plan_workspace_size")
+    if aligned_bytes is None:
+        _check(load().muon_grad_plan_workspace_size(ctypes.byref(n)), "muon_grad_plan_workspace_size")
+    else:
+        _check(load().muon_grad_plan_workspace_size_ex(aligned_bytes, ctypes.byref(n)), "muon_grad_plan_workspace_size_ex")
     return n.value
 
 
@@ -219,14 +223,19 @@ def _grads(grads, dev, name):
 
 class GradPlan:
     """Workspace and status word of the reductions and products on the current device
-    (``muon_grad_plan_create``); one serves calls of any shapes, one after another."""
+    (``muon_grad_plan_create``); one serves calls of any shapes, one after another.  ``aligned_bytes``: the part of the
+    workspace for copies of unaligned rows alone, which only ``product`` and ``dgrad`` make (0: the smallest plan, on
+    which large products of such rows are slower)."""
 
-    def __init__(self):
+    def __init__(self, aligned_bytes: int | None = None):
         if torch is None:
             _torch()
         self.lib = load()
         h = ctypes.c_void_p()
-        _check(self.lib.muon_grad_plan_create(ctypes.byref(h)), "muon_grad_plan_create")
+        if aligned_bytes is None:
+            _check(self.lib.muon_grad_plan_create(ctypes.byref(h)), "muon_grad_plan_create")
+        else:
+            _check(self.lib.muon_grad_plan_create_ex(ctypes.byref(h), aligned_bytes), "muon_grad_plan_create_ex")
         self.handle = h
 
     def close(self):

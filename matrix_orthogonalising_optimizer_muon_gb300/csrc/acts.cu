@@ -13,13 +13,14 @@ struct muon_grad_plan_s {
     double* running = nullptr;  // squares of the norm's launches so far
     int* counters = nullptr;
     float* partial = nullptr;
+    int64_t aligned = 0;        // bytes behind the partial sums, for the products' copies
 };
 
 namespace {
 using namespace muon_impl;
 
 constexpr size_t kWsHeader = 256 + kCounters * sizeof(int);   // status word, counters
-constexpr int64_t kGradWorkspace = (int64_t)kWsHeader + kPartialFloats * 4 + kAlignedBytes;
+constexpr int64_t kGradWorkspace = (int64_t)kWsHeader + kPartialFloats * 4;   // and the plan's aligned bytes
 static_assert(kWsHeader % 256 == 0, "the partial sums are aligned");
 
 constexpr int64_t kMostPitch = 1ll << 32;   // bytes from row to row
@@ -180,7 +181,8 @@ muon_status product(muon_grad_plan_s* p, const void* x, int64_t ldx, const void*
     a.x = x, a.ldx = ldx, a.weight = weight, a.y = y, a.ldy = ldy, a.tokens = tokens, a.m = (int)m, a.n = (int)n;
     a.transposed = transposed, a.offsets = offsets, a.groups = std::max(groups, 1);
     a.status = p->status, a.partial = p->partial, a.counters = p->counters;
-    a.aligned = p->partial + kPartialFloats;
+    a.aligned = p->partial + kJoinFloats, a.room = kSharedRoom + p->aligned;
+    if (!product_fits(a)) return MUON_ERR_UNSUPPORTED;
     return cuda_status(launch_product(a, p->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
@@ -315,21 +317,29 @@ muon_status muon_swiglu_backward(const void* da, int64_t ldda, const muon_act8* 
 }
 
 muon_status muon_grad_plan_workspace_size(int64_t* bytes) {
-    if (!bytes) return MUON_ERR_INVALID_ARG;
-    *bytes = kGradWorkspace;
+    return muon_grad_plan_workspace_size_ex(kAlignedBytes, bytes);
+}
+
+muon_status muon_grad_plan_workspace_size_ex(int64_t aligned_bytes, int64_t* bytes) {
+    if (!bytes || aligned_bytes < 0 || aligned_bytes > kMostAligned) return MUON_ERR_INVALID_ARG;
+    *bytes = kGradWorkspace + round_up(aligned_bytes, 256);
     return MUON_OK;
 }
 
-muon_status muon_grad_plan_create(muon_grad_plan* out) {
+muon_status muon_grad_plan_create(muon_grad_plan* out) { return muon_grad_plan_create_ex(out, kAlignedBytes); }
+
+muon_status muon_grad_plan_create_ex(muon_grad_plan* out, int64_t aligned_bytes) {
     if (!out) return MUON_ERR_INVALID_ARG;
     *out = nullptr;
+    int64_t bytes = 0;
+    MUON_CALL(muon_grad_plan_workspace_size_ex(aligned_bytes, &bytes));
     muon_grad_plan_s* p = new (std::nothrow) muon_grad_plan_s;
     if (!p) return MUON_ERR_OOM;
     muon_status st = cuda_status(cudaGetDevice(&p->device));
     if (st == MUON_OK)
         st = cuda_status(cudaDeviceGetAttribute(&p->sm_count, cudaDevAttrMultiProcessorCount, p->device));
     if (st == MUON_OK) {
-        const cudaError_t e = cudaMalloc(&p->ws, kGradWorkspace);
+        const cudaError_t e = cudaMalloc(&p->ws, bytes);
         if (e != cudaSuccess) {
             last_cuda_error() = e;
             (void)cudaGetLastError();
@@ -351,6 +361,7 @@ muon_status muon_grad_plan_create(muon_grad_plan* out) {
     p->running = reinterpret_cast<double*>(p->status + 2);
     p->counters = reinterpret_cast<int*>(static_cast<char*>(p->ws) + 256);
     p->partial = reinterpret_cast<float*>(static_cast<char*>(p->ws) + kWsHeader);
+    p->aligned = bytes - kGradWorkspace;
     *out = p;
     return MUON_OK;
 }

@@ -119,11 +119,12 @@ struct ProductArgs {
     const int* offsets;  // groups + 1, or null
     int groups;          // >= 1
     int* status;
-    float* partial;
+    float* partial;      // kJoinFloats
     int* counters;
-    void* aligned;       // kAlignedBytes for rows that are not
+    void* aligned;       // room for rows that are not
+    long long room;      // its bytes, a multiple of 256
 };
-constexpr long long kAlignedBytes = 256ll << 20;
+constexpr long long kJoinFloats = 2 * kMaxPairs * 8 * 8192ll;   // two parts of a tile per CTA pair
 
 // bf16: the dtype of the Mat operands; vec: every one of them (and ld) 16-byte aligned.
 cudaError_t launch_act_pack(const PackArgs& a, bool bf16, bool vec, cudaStream_t s);
@@ -137,6 +138,11 @@ int rmsnorm_backward_blocks(long long rows, int cols, int sm_count);
 constexpr long long kNormPartialFloats = 8ll << 20;   // bound on blocks x cols
 constexpr long long kPartialFloats = (kMaxParts + kMaxPairs) * 65536ll;   // of a grad plan, for either reduction
 static_assert(kPartialFloats >= kNormPartialFloats, "one region serves both");
+// Rows that the products copy take what their parts leave of that region, and, at its end, what the plan has for them
+// alone: a plan that is not asked for less has room for 2^28 bytes in all.
+constexpr long long kSharedRoom = (kPartialFloats - kJoinFloats) * 4, kAlignedBytes = (1ll << 28) - kSharedRoom;
+constexpr long long kMostAligned = 1ll << 34;   // 16-byte pieces of it are counted in 31 bits
+static_assert(kSharedRoom > 0 && kSharedRoom % 256 == 0 && kAlignedBytes > 0, "the room's place");
 cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a, bool bf16, bool vec, int sm_count, cudaStream_t s);
 cudaError_t wgrad_prepare();   // once per device, before the first launch
 cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s);
@@ -144,6 +150,7 @@ cudaError_t launch_expert_dispatch(const MoveArgs& a, bool bf16, bool vec, cudaS
 cudaError_t launch_expert_combine(const MoveArgs& a, bool bf16, bool vec, cudaStream_t s);
 cudaError_t launch_expert_combine_backward(const MoveArgs& a, bool bf16, bool vec, cudaStream_t s);
 cudaError_t product_prepare();   // once per device, before the first launch
+bool product_fits(const ProductArgs& a);   // where rows have to be copied, the room holds the least pieces
 cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_wgrad(const WgradArgs& a, bool bf16_grad, int sm_count, cudaStream_t s);
 

@@ -494,7 +494,7 @@ __device__ __forceinline__ void epilogue(const ProductLaunch& L, const Plan& pla
         const uint32_t tbase = e.tmem_base + acc * 256 + (static_cast<uint32_t>(e.wq * 32) << 16);
         const int c0 = w.m0 + 128 * e.q + 32 * e.wq;
         const int parts = w.part >> 16, part = w.part >> 8 & 255, first = w.part & 255;
-        // a pair has at most two parts of tiles: one that begins inside its tile, one that begins with it
+        // a pair has at most two parts of tiles: one that begins inside its tile, one that begins with it (kJoinFloats)
         auto slot = [&](int k) {
             return L.a.partial + ((2 * (first + k) + (k == 0)) * 8ll + 4 * e.q + e.wq) * 8192 + e.lane * 4;
         };
@@ -832,8 +832,8 @@ cudaError_t launch_aligned(const ProductArgs& a, int out, long long pitch, int s
 
 // Rows begin at multiples of 128 bytes, so that a box's rows are whole lines of L2.
 long long aligned_pitch(long long cols) { return muon_impl::round_up(cols, 64); }
-// As many units of `size` elements as fit into `room`, of `all`: a multiple of 256 or, where fewer fit, of 64 (that
-// many always do: sizes are at most 2^20, room at least 2^26).
+// As many units of `size` elements as fit into `room`, of `all`: a multiple of 256 or, where fewer fit, of 64; 0 where
+// not even those do.
 long long chunk_of(long long all, long long size, long long room) {
     const long long n = room / size;
     return n >= muon_impl::round_up(all, 64) ? all : n >= 256 ? n / 256 * 256 : n / 64 * 64;
@@ -842,9 +842,34 @@ void set_job(Job* j, const void* src, long long pitch, void* dst, long long dst_
     j->src = static_cast<const char*>(src), j->dst = static_cast<char*>(dst), j->pitch = pitch * 2;
     j->dst_pitch = (uint32_t)(dst_pitch * 2), j->bytes = cols * 2;
     j->by_row.set((uint32_t)((cols + 7) / 8));
-    j->pieces = (int)(rows * ((cols + 7) / 8));   // within kAlignedBytes
+    j->pieces = (int)(rows * ((cols + 7) / 8));   // within the room
 }
-static_assert(kAlignedBytes / 2 / 2 >= 1ll << 26, "room for the least chunks");
+static_assert((kSharedRoom + kAlignedBytes) / 2 / 2 >= 1ll << 26, "64 rows of 2^20 elements of each operand: any product fits");
+
+// What is copied, and in which pieces.
+struct Pieces {
+    bool align_w, align_x;
+    long long px, pw;                  // pitches of the copies, elements
+    long long tokens, experts, outs;   // of a piece: experts, or the outputs of one that is too large
+    long long used;                    // elements of the tokens' copies, behind which the weights' begin
+    bool fit;
+
+    explicit Pieces(const ProductArgs& a) {
+        const int out = a.transposed ? a.n : a.m, k = a.transposed ? a.m : a.n;
+        align_w = a.n % 8 != 0 || (reinterpret_cast<uintptr_t>(a.weight) & 15) != 0;
+        align_x = ((reinterpret_cast<uintptr_t>(a.x) | (uintptr_t)(a.ldx * 2)) & 15) != 0;
+        px = aligned_pitch(k), pw = aligned_pitch(a.n);
+        const long long all = a.room / 2, each = a.m * pw, wish = align_w ? std::min(a.groups * each, all / 2) : 0;
+        tokens = align_x ? chunk_of(a.tokens, px, all - wish) : a.tokens;
+        used = align_x ? muon_impl::round_up(tokens * px, 128) : 0;
+        experts = a.groups, outs = out;
+        if (align_w) {
+            experts = std::min<long long>((all - used) / each, a.groups);
+            if (experts == 0) experts = 1, outs = chunk_of(out, a.transposed ? a.m : pw, all - used);
+        }
+        fit = tokens > 0 && outs > 0;
+    }
+};
 
 }  // namespace
 
@@ -857,24 +882,17 @@ cudaError_t product_prepare() {
     return cudaSuccess;
 }
 
+bool product_fits(const ProductArgs& a) { return Pieces(a).fit; }
+
 cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t s) {
     const int out = a.transposed ? a.n : a.m, k = a.transposed ? a.m : a.n;
-    const bool align_w = a.n % 8 != 0 || (reinterpret_cast<uintptr_t>(a.weight) & 15) != 0;
-    const bool align_x = ((reinterpret_cast<uintptr_t>(a.x) | (uintptr_t)(a.ldx * 2)) & 15) != 0;
+    const Pieces p(a);
+    const bool align_w = p.align_w, align_x = p.align_x;
     if (!align_w && !align_x) return launch_aligned(a, out, a.n, sm_count, s);
-    // Room for the aligned rows, in elements: the tokens', then the weights'.
+    if (!p.fit) return cudaErrorInvalidValue;
     char* room = static_cast<char*>(a.aligned);
-    const long long px = aligned_pitch(k), all = kAlignedBytes / 2;
-    const long long pw = aligned_pitch(a.n), each = a.m * pw, wish = align_w ? std::min(a.groups * each, all / 2) : 0;
-    const long long tokens = align_x ? chunk_of(a.tokens, px, all - wish) : a.tokens;
-    const long long used = align_x ? muon_impl::round_up(tokens * px, 128) : 0;
-    char* room_w = room + used * 2;
-    // chunks of experts, or of the outputs of one that is too large
-    long long experts = a.groups, outs = out;
-    if (align_w) {
-        experts = std::min<long long>((all - used) / each, a.groups);
-        if (experts == 0) experts = 1, outs = chunk_of(out, a.transposed ? a.m : pw, all - used);
-    }
+    char* room_w = room + p.used * 2;
+    const long long px = p.px, tokens = p.tokens, experts = p.experts, outs = p.outs;
     for (long long g = 0; g < a.groups; g += experts)
         for (long long o = 0; o < out; o += outs)
             for (long long t = 0; t < a.tokens; t += tokens) {

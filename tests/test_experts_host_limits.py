@@ -93,3 +93,17 @@ def test_norm_does_not_lie_in_a_gradient(spec, norm):
     # of a plan of no device, not read before the check
     handle = ctypes.cast(ctypes.create_string_buffer(b"\xff" * 256, 256), ctypes.c_void_p)
     assert mu.load().muon_grad_norm(handle, p, c, d, n, norm, None) == mu.MUON_ERR_INVALID_ARG
+
+
+def test_the_room_for_copies_is_the_callers_choice():
+    """A plan for the reductions, clipping and aligned products alone need not pay for copies of unaligned rows."""
+    least, usual = mu.grad_plan_workspace_size(aligned_bytes=0), mu.grad_plan_workspace_size()
+    assert least < 84e6 and usual - least < 230e6
+    for more in (1, 256, 257, 1 << 34):
+        assert mu.grad_plan_workspace_size(aligned_bytes=more) == least + (more + 255) // 256 * 256
+    out, n = ctypes.c_void_p(), ctypes.c_int64()
+    for bad in (-1, (1 << 34) + 1, -1 << 62):
+        assert mu.load().muon_grad_plan_workspace_size_ex(bad, ctypes.byref(n)) == mu.MUON_ERR_INVALID_ARG
+        assert mu.load().muon_grad_plan_create_ex(ctypes.byref(out), bad) == mu.MUON_ERR_INVALID_ARG and not out.value
+    assert mu.load().muon_grad_plan_workspace_size_ex(0, None) == mu.MUON_ERR_INVALID_ARG
+    assert mu.load().muon_grad_plan_create_ex(None, 0) == mu.MUON_ERR_INVALID_ARG

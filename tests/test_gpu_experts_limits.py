@@ -2,7 +2,7 @@
 import pytest
 
 from test_gpu_experts import on_gpu, routed
-from test_gpu_layer import mu, plan, rand  # noqa: F401  (fixtures)
+from test_gpu_layer import U, mu, plan, rand  # noqa: F401  (fixtures)
 from test_gpu_product import bf16, check, run
 
 pytestmark = pytest.mark.gpu
@@ -51,3 +51,60 @@ def test_joined_parts_are_this_calls(plan, tokens, m, n, groups, dgrad):  # noqa
         same &= (out == want[i & 1]).all()
     plan.sync()
     assert bool(same)
+
+
+@pytest.fixture(scope="module")
+def least(mu):  # noqa: F811
+    """A plan without bytes for copies alone."""
+    with mu.GradPlan(aligned_bytes=0) as p:
+        yield p
+        p.sync()
+
+
+@pytest.mark.parametrize("dgrad", [False, True])
+@pytest.mark.parametrize("tokens,m,n,groups", [(33, 257, 129, 0), (4000, 521, 4001, 0), (40, 6001, 8193, 0),
+                                               (5001, 2049, 4097, 0), (700, 1001, 2001, 24), (9000, 264, 4000, 0)])
+def test_copies_in_the_shared_room(least, tokens, m, n, groups, dgrad):  # noqa: F811
+    """Unaligned rows on the smallest plan, in one piece and in many."""
+    x = bf16((tokens, m if dgrad else n), 28, pad=1)
+    w = bf16((groups, m, n) if groups else (m, n), 29, 0.1)
+    edges = [3] + [3 + (tokens - 9) * i * i // (groups * groups) for i in range(1, groups)] + [tokens - 4] if groups else None
+    check(least, x, w, edges, dgrad)
+
+
+def test_the_shared_room_between_other_calls(mu, least):  # noqa: F811
+    """Copies lie where the weight gradient keeps partial sums and the norm its own: each call finds what it needs."""
+    import torch
+    dy, x = bf16((9000, 512), 1), bf16((9000, 264), 2)
+    x8, dw = mu.Act8.empty(9000, 264, "int8"), [torch.empty((512, 264), device="cuda") for _ in range(2)]
+    mu.act_pack(x, x8)
+    mu.act_unpack(x8, x)
+    norm = [torch.zeros(1, device="cuda") for _ in range(2)]
+    odd, w = bf16((5000, 1001), 3), bf16((4001, 1001), 4, 0.1)
+    out = [torch.empty((5000, 4001), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for i in range(2):
+        least.wgrad(dy, x8, dw[i])
+        least.product(odd, w, out[i])
+        least.grad_norm([dw[i]], norm[i])
+    least.sync()
+    assert torch.equal(*dw) and torch.equal(*out) and torch.equal(*norm)
+    want, size = dy.double().t() @ x.double(), dy.double().abs().t() @ x.double().abs()
+    assert bool(((dw[0].double() - want).abs() <= (2 * 9000 + 8) * U * size).all())
+    check(least, odd, w, None, False)
+
+
+@pytest.mark.parametrize("dgrad", [False, True])
+def test_rows_that_no_piece_holds(mu, plan, least, dgrad):  # noqa: F811
+    """64 rows of 2^20 - 1 values: refused on the smallest plan with nothing written, computed on the usual one."""
+    import torch
+    m, n, tokens = 70, (1 << 20) - 1, 65
+    w = bf16((m, n), 5, 0.01)
+    if dgrad:
+        w = w.t().contiguous()
+    x, out = bf16((tokens, n), 6), torch.full((tokens, m), 7.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(mu.MuonError) as refused:
+        run(least, x, w, out, None, dgrad)
+    assert refused.value.code == mu.MUON_ERR_UNSUPPORTED
+    least.sync()
+    assert bool((out == 7).all())
+    check(plan, x, w, None, dgrad)
