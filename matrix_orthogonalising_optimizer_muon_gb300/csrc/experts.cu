@@ -324,9 +324,14 @@ cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s) {
     int lw = 5;
     while ((a.experts << lw) > kOrderCounts) --lw;
     // One CTA for the smallest (8192 ids of 256: 10.8 us, 8.1 with eight), the largest cluster there is for long ones,
-    // whose ranks take longest, unless reading all CTAs' counts takes longer: 65536 ids of 256
-    // 12.8 us with eight CTAs and 14.3 with sixteen, 131072 of 128 16.1 and 13.3, of 4096 51 and 84.
-    const int lc = a.n <= 2048 ? 0 : a.n >= 100000 && a.experts <= 1024 ? 4 : 3;
+    // whose ranks take longest, unless reading all CTAs' counts takes longer.  us with eight and with sixteen CTAs:
+    //   ids     64 experts   128          256          512          1024         4096
+    //   32768   8.4   8.5    9.0   9.9   10.2  13.1   12.6  19.8   16.8  28.9
+    //   65536  10.6   9.6   11.4  11.0   13.0  14.5   15.6  21.1   20.1  30.4
+    //  131072  15.2  11.9   16.3  13.5   18.1  17.1   21.3  24.1   26.2  33.6   51    84
+    //  262144  27.0  16.6   28.4  18.3   31.2  22.4   35.3  29.8   40.9  39.8
+    // 1048576  91.5  50.1   96.2  53.5    104  60.0    114  70.2    124  82.6
+    const int lc = a.n <= 2048 ? 0 : a.n >= 256ll * (a.experts + 128) && a.experts <= 1024 ? 4 : 3;
     const size_t bytes = (size_t)((1 << lw) + 3) * a.experts * sizeof(int);
     // Beyond 48 KB an attribute of the current device has to allow it: set per call, and the same by every call, as
     // another thread may be between its own setting and its launch.

@@ -1,7 +1,8 @@
 """Calls of the experts' operators at their limits, on the GPU."""
+import numpy as np
 import pytest
 
-from test_gpu_experts import on_gpu, routed
+from test_gpu_experts import on_gpu, order, ordered, routed
 from test_gpu_layer import U, mu, plan, rand  # noqa: F401  (fixtures)
 from test_gpu_product import bf16, check, run
 
@@ -108,3 +109,15 @@ def test_rows_that_no_piece_holds(mu, plan, least, dgrad):  # noqa: F811
     least.sync()
     assert bool((out == 7).all())
     check(plan, x, w, None, dgrad)
+
+
+@pytest.mark.parametrize("choices,experts", [(1, 64), (3, 64), (4, 300), (8, 512), (5, 1023), (4, 1024), (7, 1025)])
+def test_order_of_long_lists(mu, choices, experts):  # noqa: F811
+    """Lists just below and at the length from which the largest clusters are taken, and a million ids."""
+    rng = np.random.default_rng(experts + choices)
+    edge = -(-256 * (experts + 128) // choices)
+    for tokens in (edge - 1, edge, (1 << 20) // choices):
+        ids = rng.integers(-1, experts + 1, (tokens, choices))
+        offsets, slots = ordered(mu, ids, experts)
+        want = order(ids, experts)
+        assert np.array_equal(offsets.cpu().numpy(), want[0]) and np.array_equal(slots.cpu().numpy(), want[1])
