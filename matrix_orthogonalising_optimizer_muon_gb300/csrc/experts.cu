@@ -1,6 +1,7 @@
 // Tokens in their experts' order and back: the order itself (a stable counting sort of the
 // chosen experts), the move of rows into it, their weighted sum per token, and its gradients.
 #include <algorithm>
+#include <atomic>
 
 #include "act8.cuh"
 #include "kernels.h"
@@ -318,6 +319,39 @@ unsigned row_blocks(const MoveArgs& a, int fit) {
     return blocks_for((long long)a.tokens * ((a.cols + Walk::kWidth - 1) / Walk::kWidth), fit);
 }
 
+// Shared memory beyond 48 KB and clusters beyond eight CTAs are for attributes of the current device to allow: set per
+// call, and the same by every call, as another thread may be between its own setting and its launch.
+constexpr int kMostBytes = (8 + 3) * 4096 * (int)sizeof(int), kSixteenBytes = (32 + 3) * 1024 * (int)sizeof(int);
+static_assert(kMostBytes >= kSixteenBytes && kMostBytes >= (16 + 3) * 2048 * (int)sizeof(int),
+              "the most of any number of experts");
+cudaError_t allow_bytes() {
+    return cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
+}
+cudaError_t allow_sixteen() {
+    return cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+// Whether the current device has room for sixteen CTAs of up to 1024 experts in a cluster, which only eight always
+// have; asked once per device.
+bool places_sixteen() {
+    constexpr int kDevices = 64;
+    static std::atomic<signed char> known[kDevices];   // 0: not asked yet
+    int dev = 0, clusters = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
+    if (const signed char k = known[dev].load(std::memory_order_relaxed)) return k > 0;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(16), cfg.blockDim = dim3(kOrderThreads), cfg.dynamicSmemBytes = kSixteenBytes;
+    cfg.attrs = attr, cfg.numAttrs = 1;
+    cudaError_t e = allow_bytes();
+    if (e == cudaSuccess) e = allow_sixteen();
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, k_expert_order, &cfg);
+    if (e != cudaSuccess) (void)cudaGetLastError(), clusters = 0;
+    known[dev].store(clusters > 0 ? 1 : -1, std::memory_order_relaxed);
+    return clusters > 0;
+}
+
 }  // namespace
 
 cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s) {
@@ -331,18 +365,11 @@ cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s) {
     //  131072  15.2  11.9   16.3  13.5   18.1  17.1   21.3  24.1   26.2  33.6   51    84
     //  262144  27.0  16.6   28.4  18.3   31.2  22.4   35.3  29.8   40.9  39.8
     // 1048576  91.5  50.1   96.2  53.5    104  60.0    114  70.2    124  82.6
-    const int lc = a.n <= 2048 ? 0 : a.n >= 256ll * (a.experts + 128) && a.experts <= 1024 ? 4 : 3;
+    const bool is_long = a.n >= 256ll * (a.experts + 128) && a.experts <= 1024;
+    const int lc = a.n <= 2048 ? 0 : is_long && places_sixteen() ? 4 : 3;
     const size_t bytes = (size_t)((1 << lw) + 3) * a.experts * sizeof(int);
-    // Beyond 48 KB an attribute of the current device has to allow it: set per call, and the same by every call, as
-    // another thread may be between its own setting and its launch.
-    constexpr int kMostBytes = (8 + 3) * 4096 * (int)sizeof(int);
-    static_assert(kMostBytes >= (32 + 3) * 1024 * (int)sizeof(int) && kMostBytes >= (16 + 3) * 2048 * (int)sizeof(int),
-                  "the most of any number of experts");
-    cudaError_t e = cudaSuccess;
-    if (bytes > 48 * 1024)
-        e = cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
-    if (e == cudaSuccess && lc == 4)
-        e = cudaFuncSetAttribute(k_expert_order, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = bytes > 48 * 1024 ? allow_bytes() : cudaSuccess;
+    if (e == cudaSuccess && lc == 4) e = allow_sixteen();
     if (e != cudaSuccess) return e;
     return launch_pdl_cluster(k_expert_order, dim3(1 << lc), dim3(kOrderThreads), bytes, s, 1u << lc, a, lw, lc);
 }

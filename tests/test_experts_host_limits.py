@@ -107,3 +107,12 @@ def test_the_room_for_copies_is_the_callers_choice():
         assert mu.load().muon_grad_plan_create_ex(ctypes.byref(out), bad) == mu.MUON_ERR_INVALID_ARG and not out.value
     assert mu.load().muon_grad_plan_workspace_size_ex(0, None) == mu.MUON_ERR_INVALID_ARG
     assert mu.load().muon_grad_plan_create_ex(None, 0) == mu.MUON_ERR_INVALID_ARG
+
+
+def test_clusters_beyond_the_portable_size_are_asked_for_first():
+    """Eight CTAs always fit a cluster; whether sixteen do is the device's to say (one that is divided may lack a group of
+    as many SMs), and a launch of a cluster that does not fit fails."""
+    src = re.sub(r"//.*", "", open(os.path.join(CSRC, "experts.cu")).read())
+    launch = src[src.index("cudaError_t launch_expert_order"):]
+    launch = launch[:launch.index("\n}")]
+    assert "cudaOccupancyMaxActiveClusters" in src and "places_sixteen() ? 4 : 3" in launch
