@@ -121,3 +121,27 @@ def test_order_of_long_lists(mu, choices, experts):  # noqa: F811
         offsets, slots = ordered(mu, ids, experts)
         want = order(ids, experts)
         assert np.array_equal(offsets.cpu().numpy(), want[0]) and np.array_equal(slots.cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("tokens,m,n,groups", [(20000, 521, 392, 0), (12000, 264, 1032, 6)])
+def test_weight_gradient_of_copied_rows_over_many_rounds(mu, plan, tokens, m, n, groups):  # noqa: F811
+    """dy off 16-byte alignment, hundreds of rounds of the operands' ring, call after call: none gives up a wait, and all
+    give the same bits."""
+    import torch
+    dy, x = bf16((tokens, m), 1, 0.5, pad=1), bf16((tokens, n), 2)
+    x8 = mu.Act8.empty(tokens, n, "e4m3")
+    mu.act_pack(x, x8)
+    mu.act_unpack(x8, x)
+    edges = [tokens * i * i // (groups * groups) for i in range(groups + 1)] if groups else [0, tokens]
+    offsets = torch.tensor(edges, dtype=torch.int32, device="cuda") if groups else None
+    g = [torch.empty((groups, m, n) if groups else (m, n), device="cuda") for _ in range(2)]
+    same = torch.ones((), dtype=torch.bool, device="cuda")
+    for i in range(40):
+        plan.wgrad(dy, x8, g[i > 0], offsets=offsets)
+        same &= (g[i > 0] == g[0]).all()
+    plan.sync()                                   # raises where a wait ran out
+    assert bool(same)
+    for e, (a, b) in enumerate(zip(edges, edges[1:])):
+        d, v = dy[a:b].double().t(), x[a:b].double()
+        got = (g[0][e] if groups else g[0]).double()
+        assert bool(((got - d @ v).abs() <= (2 * (b - a) + 8) * U * (d.abs() @ v.abs())).all())
