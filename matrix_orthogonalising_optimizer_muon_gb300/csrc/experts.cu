@@ -17,7 +17,7 @@ namespace {
 // and smaller experts give each warp its first slot per expert; pass 2 deals the slots out, 32 ids at
 // a time, neighbours with the same expert by their rank among the warp's lanes.  What bounds it is latency:
 // a warp's ids are loaded kBatch groups of 32 at a time and, when that is all it has, kept for pass 2
-// (131072 ids of 128 experts: 13.3 us, 512 ids 6).
+// (131072 ids of 128 experts: 13.1 to 13.5 us, 512 ids 6).
 constexpr int kOrderThreads = 1024;
 constexpr int kOrderCounts = 32768;   // counts in shared memory: warps x experts
 constexpr int kBatch = 16;
@@ -174,7 +174,7 @@ __device__ __forceinline__ int slot_row(const MoveArgs& a, uint32_t token, int j
 }
 
 // out[slots[t, j], :] = x[t, :]: a warp loads a piece of a token's row once and stores it once per choice (HBM-bound:
-// 8192 x 4 rows of 3584 in bf16 44.1 us, 98 % of the copy rate).
+// 8192 x 4 rows of 3584 in bf16 44.1 us, 98 % of the copy rate; in fp32 117, 74 %).
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_dispatch(const MoveArgs a) {
     const int lane = threadIdx.x & 31;
@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const MoveArgs a) {
 template <bool BF16>
 constexpr int kTogether = BF16 ? 4 : 2;
 
-// x[t, :] = sum over j of weights[t, j] y[slots[t, j], :], in fp32, j ascending.
+// x[t, :] = sum over j of weights[t, j] y[slots[t, j], :], in fp32, j ascending.  HBM-bound: 8192 x 4 rows of 3584 in
+// bf16 48.7 us (89 % of the copy rate), in fp32 84.7.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_combine(const MoveArgs a) {
     constexpr int kJ = kTogether<BF16>;

@@ -1,9 +1,9 @@
 // The norm of all gradients together and their scaling to a largest norm, over lists of
 // tensors of any sizes.  The list travels in the kernel's parameters: no table is copied to
 // the device, so a call enqueues kernels alone and can be captured.  Both are HBM-bound: a 7B layer's 233 million fp32
-// values 138 us for the norm and 207 us scaled into bf16 (6.75 TB/s, the copy rate), 1036 matrices of at most 128 x
-// 3584 in bf16 73 us (6.0 TB/s).  What is left for short lists are about 6 us of launch, first loads and the last
-// block's sum, and 5 more for the 32 KB of parameters of long ones.
+// values 138 us for the norm, 207 us scaled into bf16 (6.75 TB/s, the copy rate) and 331 in place (5.6 TB/s), 1036
+// matrices of at most 128 x 3584 in bf16 73 us (6.0 TB/s).  What is left for short lists are about 6 us of launch, first
+// loads and the last block's sum, and 5 more for the 32 KB of parameters of long ones.
 #include "act8.cuh"
 #include "grads.h"
 #include "kernels.h"

@@ -20,7 +20,7 @@
 // 18944 x 3584 over 16384 rows 1365 us.  32 experts of 1024 x 2048 over 16384 ragged rows 59 us: 308 tiles of 256
 // outputs, low ones among them, whose steps cost their weight's 32 KB all the same, in five turns, and about 10 us
 // around them (launch 2, set-up 0.6, plan 2.5, first loads 1, last epilogue 2).  Few rows are bound by the weights'
-// bytes and those 10 us: 32 rows for 32 experts 28 us (HBM 20), eight rows for eight of them 12.4 (HBM 5), one row of
+// bytes and those 10 us: 32 rows for 32 experts 28 us (HBM 20), eight rows for eight of them 11.5 (HBM 5), one row of
 // one weight of 3584 x 3584 10.4 (HBM 3.8).
 //
 // How the work is dealt out (every CTA derives the same plan from the offsets): tiles in the order experts,
@@ -220,7 +220,8 @@ __device__ __forceinline__ void order_experts(Plan& p, int groups, int lane) {
 // How tiles of at most 32 `high` tokens would be dealt out, and the time that takes, in 32 cycles.  A step takes as
 // long as its MMAs, and 256 cycles for the weight's 16 KB besides.  The tiles of the last, incomplete turn are cut
 // along the contraction into stretches of equal length, one per pair, where that saves more than joining the parts
-// takes: about 24 steps' time and, to write and read them, 34 more for 256 tokens (8 rows for eight of 32 experts, 32
+// takes: about 24 steps' time and, to write and read them, 34 more for 256 tokens, all at the greatest height, though
+// the last turn's tiles are the lowest where there are several turns (8 rows for eight of 32 experts, 32
 // steps: 11.5 us whole, 12.6 cut; 16 rows of 18944 values, 296 steps: 61 whole, 30 cut).
 struct Dealt {
     int units, whole, rest, time;
