@@ -554,8 +554,8 @@ muon_status muon_swiglu_backward(const void* da, int64_t ldda, const muon_act8* 
  * workspace that serve nothing but the copies which muon_product and muon_dgrad make of rows
  * that are not aligned to 16 bytes: 0 to 2^34.  The others take 2^28 less the 43 MB that those
  * copies share with the other calls; with 0 a plan is 83 MB.  Operands that do not fit are
- * copied in pieces, a launch or two each, and where 64 rows of one (columns, of
- * muon_dgrad's weight) are more than half of both shares the product is refused
+ * copied in pieces, a launch or two each; a product of which 64 rows of an operand (columns, of
+ * muon_dgrad's weight) are more than half of the two shares together may be refused
  * (MUON_ERR_UNSUPPORTED), which no size reaches without _ex.  muon_grad_plan_create
  * synchronises the host; so do muon_grad_plan_destroy (the whole device; NULL is ignored) and
  * muon_grad_plan_sync, which waits for stream, then reads and clears the status word
